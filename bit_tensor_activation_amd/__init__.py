@@ -5,6 +5,7 @@ The codec runs in HIP kernels for gfx950 behind the C ABI of libbtq.so
 script, and a thin torch binding whose functions carry the C names.
 """
 from .api import (  # noqa: F401
+    btq_block_norm,
     btq_calib_update,
     btq_calib_update_noalloc,
     btq_calib_workspace_bytes,
@@ -15,8 +16,12 @@ from .api import (  # noqa: F401
     btq_decompress_reduce_bf16,
     btq_decompress_reduce_ex,
     btq_decompress_reduce_per_shard,
+    btq_int8_linear,
+    btq_int8_linear_workspace_bytes,
+    btq_int8_matmul,
     btq_packed_pitch,
     btq_packed_row_bytes,
+    btq_quantize_rows,
     btq_select_features,
     btq_select_outliers,
     btq_select_outliers_per_shard,

@@ -38,6 +38,14 @@ SIGNATURES = {
     "btq_decompress_reduce_ex": (_I, [_P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I, _P,
                                       _I, _P]),
     "btq_packed_pitch": (_I64, [_I64, _I64]),
+    "btq_quantize_rows": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    "btq_int8_matmul": (_I, [_P, _I64, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _I,
+                             _P]),
+    "btq_int8_linear": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _I, _P,
+                             _SZ, _P]),
+    "btq_int8_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "btq_block_norm": (_I, [_P, _I, _P, _I, _I64, _I64, _I, _P, _P, _F, _P, _I, _I64, _F, _I, _P,
+                            _P, _F, _P, _P, _I, _P, _P]),
     "btq_status_str": (_c.c_char_p, [_I]),
     "btq_version": (_c.c_char_p, []),
 }
@@ -59,6 +67,14 @@ BTQ_SETS_PER_SHARD = 1
 
 BTQ_Y_F32 = 0
 BTQ_Y_BF16 = 1
+
+BTQ_T_F32 = 0
+BTQ_T_BF16 = 1
+BTQ_T_INT8 = 2
+
+BTQ_NORM_NONE = 0
+BTQ_NORM_RMS = 1
+BTQ_NORM_LAYER = 2
 
 _lock = threading.Lock()
 _lib = None

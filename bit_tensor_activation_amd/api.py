@@ -22,6 +22,8 @@ Layouts (contiguous, row-major, last index fastest):
                 Bq up to 128)
   outliers      int16 [P,T,k]
   y             float32 [T,H]  (bf16 bits, int16 [T,H], for bf16 output)
+The 8-bit linear layer and the block norm take bf16 tensors in both forms too,
+and return bf16 as torch.bfloat16 where they are given torch.bfloat16.
 """
 from __future__ import annotations
 
@@ -358,6 +360,189 @@ def btq_decompress_reduce_per_shard(packed: torch.Tensor, outliers: torch.Tensor
     _need_dense(packed, outliers, H)
     return btq_decompress_reduce_ex(packed, outliers, H, scale, zero_point, fmap, True, y, False,
                                     stream)
+
+
+_T = {torch.float32: _lib.BTQ_T_F32, torch.bfloat16: _lib.BTQ_T_BF16, torch.int16: _lib.BTQ_T_BF16,
+      torch.int8: _lib.BTQ_T_INT8}
+_VALUES = (torch.float32, torch.bfloat16, torch.int16)
+_NORMS = {"none": _lib.BTQ_NORM_NONE, "rms": _lib.BTQ_NORM_RMS, "layer": _lib.BTQ_NORM_LAYER}
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtypes, shape, dev) -> Optional[int]:
+    """Data pointer of an optional contiguous tensor."""
+    if t is None:
+        return None
+    # the quick form of _need: its messages only when something is wrong
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.device != dev:
+        _need(t, name, dtypes, shape, dev)
+    return t.data_ptr() if t.numel() else None
+
+
+def _rows(x: torch.Tensor, name: str, dtypes, dev):
+    """(P or None, T, K, shard stride, row pitch) of rows [T,K] or [P,T,K] whose
+    last dimension is contiguous."""
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {x.dtype}, expected one of {dtypes}")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected [T,K] or [P,T,K]")
+    if x.device != dev:
+        raise ValueError(f"{name}: on {x.device}, expected {dev}")
+    if x.stride(-1) != 1 and x.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if x.dim() == 2:
+        return None, x.shape[0], x.shape[1], 0, x.stride(0)
+    return x.shape[0], x.shape[1], x.shape[2], x.stride(0), x.stride(1)
+
+
+def btq_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                      scale: Optional[torch.Tensor] = None, stream=None):
+    """8-bit codes and the scale of every row: (q int8, scale float32).
+
+    x is [T,K] or [P,T,K], float32 or bf16, the last dimension contiguous and
+    the others with any strides. q has x's shape and scale lacks its last
+    dimension. For weights [P,N,K] the rows are the output channels.
+    """
+    dev = _device(x)
+    P, T, K, shard, pitch = _rows(x, "x", _VALUES, dev)
+    shape = tuple(x.shape)
+    sh, ctx = _launch(dev, stream)
+    with ctx:
+        if q is None:
+            q = torch.empty(shape, dtype=torch.int8, device=dev)
+        if scale is None:
+            scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        st = _lib.load().btq_quantize_rows(
+            _ptr(x), _T[x.dtype], shard, pitch, 1 if P is None else P, T, K,
+            _opt(q, "q", (torch.int8,), shape, dev),
+            _opt(scale, "scale", (torch.float32,), shape[:-1], dev), sh)
+    _lib.check(st, "btq_quantize_rows")
+    return q, scale
+
+
+def _product_args(x_p, T, K, w, w_scale, bias, y, bf16, y_like, dev):
+    """Shape checks shared by the products; allocates y if needed."""
+    if w.dim() != 3:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected [P,N,K]")
+    P, N = w.shape[0], w.shape[1]
+    if x_p is not None and x_p != P:
+        raise ValueError(f"w: {P} shards, the activations have {x_p}")
+    wp = _opt(w, "w", (torch.int8,), (P, N, K), dev)
+    sp = _opt(w_scale, "w_scale", (torch.float32,), (P, N), dev)
+    bp = _opt(bias, "bias", (torch.float32,), (P, N), dev)
+    if y is None:
+        dt = torch.float32 if not bf16 else y_like
+        y = torch.empty((P, T, N), dtype=dt, device=dev)
+    return P, N, wp, sp, bp, y, _opt(y, "y", _VALUES, (P, T, N), dev)
+
+
+def btq_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
+                    w_scale: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    y: Optional[torch.Tensor] = None, bf16: bool = True,
+                    stream=None) -> torch.Tensor:
+    """y [P,T,N] = (a @ w^T per shard) * a_scale * w_scale (+ bias).
+
+    a int8 [P,T,K] (any strides but the last, which is contiguous) with
+    a_scale [P,T], or [T,K] with [T]: the same rows for every shard. w int8
+    [P,N,K], w_scale float32 [P,N], bias float32 [P,N]. Without `y` the result
+    is bf16 bits (int16), or float32 when not bf16; a given y may be float32,
+    torch.bfloat16 or int16.
+    """
+    dev = _device(a)
+    x_p, T, K, shard, pitch = _rows(a, "a", (torch.int8,), dev)
+    sh, ctx = _launch(dev, stream)
+    with ctx:
+        P, N, wp, sp, bp, y, yp = _product_args(x_p, T, K, w, w_scale, bias, y, bf16, torch.int16,
+                                                dev)
+        asp = _opt(a_scale, "a_scale", (torch.float32,), (T,) if x_p is None else (P, T), dev)
+        st = _lib.load().btq_int8_matmul(_ptr(a), shard, pitch, asp, 0 if x_p is None else T, wp,
+                                         sp, bp, P, T, N, K, yp, _T[y.dtype], sh)
+    _lib.check(st, "btq_int8_matmul")
+    return y
+
+
+def btq_int8_linear_workspace_bytes(P: int, T: int, K: int) -> int:
+    return int(_lib.load().btq_int8_linear_workspace_bytes(P, T, K))
+
+
+def btq_int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                    bias: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                    bf16: bool = True, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """8-bit linear layer: btq_quantize_rows of x, then btq_int8_matmul.
+
+    x float32 or bf16, [P,T,K], or [T,K] for the same rows on every shard.
+    y [P,T,N] as in btq_int8_matmul; without `y` a bf16 result has x's form
+    of bf16 (int16 bits for float32 x).
+    """
+    dev = _device(x)
+    x_p, T, K, shard, pitch = _rows(x, "x", _VALUES, dev)
+    like = torch.bfloat16 if x.dtype == torch.bfloat16 else torch.int16
+    sh, ctx = _launch(dev, stream)
+    with ctx:
+        P, N, wp, sp, bp, y, yp = _product_args(x_p, T, K, w, w_scale, bias, y, bf16, like, dev)
+        if workspace is None:
+            workspace = torch.empty(btq_int8_linear_workspace_bytes(P, T, K), dtype=torch.uint8,
+                                    device=dev)
+        st = _lib.load().btq_int8_linear(
+            _ptr(x), _T[x.dtype], shard, pitch, wp, sp, bp, P, T, N, K, yp, _T[y.dtype],
+            _ptr(workspace), workspace.numel() * workspace.element_size(), sh)
+    _lib.check(st, "btq_int8_linear")
+    return y
+
+
+def btq_block_norm(y: Optional[torch.Tensor], residual: torch.Tensor, post: str = "none",
+                   post_weight: Optional[torch.Tensor] = None,
+                   post_bias: Optional[torch.Tensor] = None,
+                   gate: Optional[torch.Tensor] = None, alpha: float = 1.0, pre: str = "rms",
+                   pre_weight: Optional[torch.Tensor] = None,
+                   pre_bias: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   post_eps: Optional[float] = None,
+                   residual_out: Optional[torch.Tensor] = None,
+                   n: Optional[torch.Tensor] = None, n_scale: Optional[torch.Tensor] = None,
+                   n_dtype: Optional[torch.dtype] = None, stream=None):
+    """r' = residual + alpha*gate*post(y) and n = pre(r'), one pass over the rows.
+
+    y [T,H] is the receiver's output (float32 or bf16), or None for the first
+    norm of a model. post and pre are "none", "rms" or "layer", with float32
+    weights and (layer) biases [H]. gate float32 or bf16 [G,H], G dividing T.
+    post_eps is eps unless given. residual_out may be residual itself.
+    n: n_dtype (by default the residual's type; float32, bf16 or int8).
+    Returns (residual_out, n), and n_scale [T] as a third for int8 n.
+    """
+    dev = _device(residual)
+    if residual.dim() != 2:
+        raise ValueError(f"residual: shape {tuple(residual.shape)}, expected [T,H]")
+    if post not in _NORMS or pre not in _NORMS:
+        raise ValueError(f"post and pre must be among {sorted(_NORMS)}")
+    shape = T, H = residual.shape
+    rp = _opt(residual, "residual", _VALUES, shape, dev)
+    yp = _opt(y, "y", _VALUES, shape, dev)
+    f32 = (torch.float32,)
+    pw, pb = _opt(post_weight, "post_weight", f32, (H,), dev), _opt(post_bias, "post_bias", f32,
+                                                                  (H,), dev)
+    nw, nb = _opt(pre_weight, "pre_weight", f32, (H,), dev), _opt(pre_bias, "pre_bias", f32, (H,),
+                                                                dev)
+    gp, gt, gr = None, 0, 1
+    if gate is not None:
+        gr = gate.shape[0] if gate.dim() == 2 else 0
+        gp, gt = _opt(gate, "gate", _VALUES, (gr, H), dev), _T[gate.dtype]
+    sh, ctx = _launch(dev, stream)
+    with ctx:
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        op = _opt(residual_out, "residual_out", (residual.dtype,), shape, dev)
+        if n is None:
+            n = torch.empty(shape, dtype=residual.dtype if n_dtype is None else n_dtype, device=dev)
+        np_ = _opt(n, "n", _VALUES + (torch.int8,), shape, dev)
+        if n.dtype == torch.int8 and n_scale is None:
+            n_scale = torch.empty((T,), dtype=torch.float32, device=dev)
+        sp = _opt(n_scale, "n_scale", f32, (T,), dev)
+        st = _lib.load().btq_block_norm(
+            yp, 0 if y is None else _T[y.dtype], rp, _T[residual.dtype], T, H, _NORMS[post], pw,
+            pb, eps if post_eps is None else post_eps, gp, gt, gr, alpha, _NORMS[pre], nw, nb, eps,
+            op, np_, _T[n.dtype], sp, sh)
+    _lib.check(st, "btq_block_norm")
+    return (residual_out, n, n_scale) if n.dtype == torch.int8 else (residual_out, n)
 
 
 def btq_status_str(status: int) -> str:

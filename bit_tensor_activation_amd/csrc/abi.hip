@@ -1,5 +1,6 @@
 // extern "C" entry points of libbtq: host-side argument checks, then the
-// launchers in calib.hip, select.hip, compress.hip and decompress.hip.
+// launchers in calib.hip, select.hip, compress.hip, decompress.hip, norm.hip,
+// rows8.hip and matmul8.hip.
 // The contract of each call is documented in include/btq.h.
 #include <math.h>
 
@@ -303,11 +304,139 @@ int btq_decompress_reduce_per_shard(const uint8_t* packed, const uint16_t* outli
                                   zero_point, fmap, BTQ_SETS_PER_SHARD, y, BTQ_Y_F32, stream);
 }
 
+namespace {
+
+bool value_type(int t) { return t == BTQ_T_F32 || t == BTQ_T_BF16; }
+size_t value_align(int t) { return t == BTQ_T_F32 ? 4 : t == BTQ_T_BF16 ? 2 : 1; }
+
+// Largest K whose sum of K products of two codes (at most 2^14 each) stays
+// inside int32.
+constexpr int64_t kMaxSumK = 131071;
+
+// Row strides of a [P,T,K] tensor: not negative, and P, T steps of them stay
+// inside 2^62 elements.
+int check_strides(int64_t P, int64_t T, int64_t shard, int64_t pitch) {
+  if (shard < 0 || pitch < 0) return BTQ_ERR_SHAPE;
+  if (shard > kMaxElems / P || (T > 0 && pitch > kMaxElems / T)) return BTQ_ERR_SHAPE;
+  return BTQ_OK;
+}
+
+int check_matmul(int64_t as_shard, const int8_t* w, const float* w_scale, const float* bias,
+                 int64_t P, int64_t T, int64_t N, int64_t K, const void* y, int y_type) {
+  int st = check_dims(P, T, K, 0);
+  if (st == BTQ_OK) st = check_dims(P, T, N, 0);
+  if (st == BTQ_OK) st = check_dims(P, N, K, 0);
+  if (st != BTQ_OK) return st;
+  if (N > kMaxH || N < 1 || K > kMaxSumK) return BTQ_ERR_SHAPE;
+  if (as_shard < 0 || as_shard > kMaxElems / P) return BTQ_ERR_SHAPE;
+  if (!value_type(y_type) || !w || !w_scale || (T > 0 && !y)) return BTQ_ERR_ARG;
+  if (!aligned(w_scale, 4) || !aligned(bias, 4) || !aligned(y, value_align(y_type)))
+    return BTQ_ERR_ALIGN;
+  return BTQ_OK;
+}
+
+// Workspace of btq_int8_linear: the codes with rows padded to 16 bytes, then
+// the scales.
+int64_t code_pitch(int64_t K) { return (K + 15) / 16 * 16; }
+
+}  // namespace
+
+int btq_quantize_rows(const void* x, int x_type, int64_t x_shard, int64_t x_pitch, int64_t P,
+                      int64_t T, int64_t K, int8_t* q, float* scale, void* stream) {
+  int st = check_dims(P, T, K, 0);
+  if (st == BTQ_OK) st = check_strides(P, T, x_shard, x_pitch);
+  if (st != BTQ_OK) return st;
+  if (!value_type(x_type) || (T > 0 && (!x || !q || !scale))) return BTQ_ERR_ARG;
+  if (!aligned(x, value_align(x_type)) || !aligned(scale, 4)) return BTQ_ERR_ALIGN;
+  if (T == 0) return BTQ_OK;
+  return hip_status(btq::launch_quantize_rows(x, x_type, x_shard, x_pitch, P, T, K, q, K, scale,
+                                              (hipStream_t)stream));
+}
+
+int btq_int8_matmul(const int8_t* a, int64_t a_shard, int64_t a_pitch, const float* a_scale,
+                    int64_t as_shard, const int8_t* w, const float* w_scale, const float* bias,
+                    int64_t P, int64_t T, int64_t N, int64_t K, void* y, int y_type,
+                    void* stream) {
+  int st = check_matmul(as_shard, w, w_scale, bias, P, T, N, K, y, y_type);
+  if (st == BTQ_OK) st = check_strides(P, T, a_shard, a_pitch);
+  if (st != BTQ_OK) return st;
+  if (T > 0 && (!a || !a_scale)) return BTQ_ERR_ARG;
+  if (!aligned(a_scale, 4)) return BTQ_ERR_ALIGN;
+  if (T == 0) return BTQ_OK;
+  const btq::MatmulArgs m = {a, a_shard, a_pitch, a_scale, as_shard, w, w_scale, bias,
+                             P, T, N, K, y, y_type};
+  return hip_status(btq::launch_int8_matmul(m, (hipStream_t)stream));
+}
+
+size_t btq_int8_linear_workspace_bytes(int64_t P, int64_t T, int64_t K) {
+  if (check_dims(P, T, K, 0) != BTQ_OK || K > kMaxSumK) return 0;
+  return (size_t)(P * T * (code_pitch(K) + (int64_t)sizeof(float)));
+}
+
+int btq_int8_linear(const void* x, int x_type, int64_t x_shard, int64_t x_pitch, const int8_t* w,
+                    const float* w_scale, const float* bias, int64_t P, int64_t T, int64_t N,
+                    int64_t K, void* y, int y_type, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  int st = check_matmul(0, w, w_scale, bias, P, T, N, K, y, y_type);
+  if (st == BTQ_OK) st = check_strides(P, T, x_shard, x_pitch);
+  if (st != BTQ_OK) return st;
+  if (!value_type(x_type) || (T > 0 && (!x || !workspace))) return BTQ_ERR_ARG;
+  if (!aligned(x, value_align(x_type)) || !aligned(workspace, 16)) return BTQ_ERR_ALIGN;
+  if (workspace_bytes < btq_int8_linear_workspace_bytes(P, T, K)) return BTQ_ERR_WORKSPACE;
+  if (T == 0) return BTQ_OK;
+  const int64_t pitch = code_pitch(K);
+  const int64_t rows = x_shard == 0 ? 1 : P;   // shards of activations
+  int8_t* q = (int8_t*)workspace;
+  float* scale = (float*)(q + P * T * pitch);
+  st = hip_status(btq::launch_quantize_rows(x, x_type, x_shard, x_pitch, rows, T, K, q, pitch,
+                                            scale, (hipStream_t)stream));
+  if (st != BTQ_OK) return st;
+  const btq::MatmulArgs m = {q, rows == 1 ? 0 : T * pitch, pitch, scale, rows == 1 ? 0 : T,
+                             w, w_scale, bias, P, T, N, K, y, y_type};
+  return hip_status(btq::launch_int8_matmul(m, (hipStream_t)stream));
+}
+
+int btq_block_norm(const void* y, int y_type, const void* residual, int r_type, int64_t T,
+                   int64_t H, int post, const float* post_weight, const float* post_bias,
+                   float post_eps, const void* gate, int gate_type, int64_t gate_rows,
+                   float alpha, int pre, const float* pre_weight, const float* pre_bias,
+                   float pre_eps, void* residual_out, void* n, int n_type, float* n_scale,
+                   void* stream) {
+  int st = check_dims(1, T, H, 0);
+  if (st != BTQ_OK) return st;
+  if (gate && (gate_rows < 1 || T % gate_rows != 0)) return BTQ_ERR_SHAPE;
+  if (post < BTQ_NORM_NONE || post > BTQ_NORM_LAYER || pre < BTQ_NORM_NONE ||
+      pre > BTQ_NORM_LAYER)
+    return BTQ_ERR_ARG;
+  if (!value_type(y_type) || !value_type(r_type) || !value_type(gate_type)) return BTQ_ERR_ARG;
+  if (!value_type(n_type) && n_type != BTQ_T_INT8) return BTQ_ERR_ARG;
+  if ((post_weight && post == BTQ_NORM_NONE) || (post_bias && post != BTQ_NORM_LAYER) ||
+      (pre_weight && pre == BTQ_NORM_NONE) || (pre_bias && pre != BTQ_NORM_LAYER))
+    return BTQ_ERR_ARG;
+  if (!(post_eps >= 0.0f && post_eps < INFINITY) || !(pre_eps >= 0.0f && pre_eps < INFINITY) ||
+      !(alpha > -INFINITY && alpha < INFINITY))
+    return BTQ_ERR_ARG;
+  if (T > 0 && (!residual || (!y && (post != BTQ_NORM_NONE || gate)) || (!residual_out && !n)))
+    return BTQ_ERR_ARG;
+  if ((n && n_type == BTQ_T_INT8) ? (T > 0 && !n_scale) : n_scale != nullptr) return BTQ_ERR_ARG;
+  const size_t r_align = value_align(r_type);
+  if (!aligned(y, value_align(y_type)) || !aligned(residual, r_align) ||
+      !aligned(residual_out, r_align) || !aligned(gate, value_align(gate_type)) ||
+      !aligned(n, value_align(n_type)) || !aligned(post_weight, 4) || !aligned(post_bias, 4) ||
+      !aligned(pre_weight, 4) || !aligned(pre_bias, 4) || !aligned(n_scale, 4))
+    return BTQ_ERR_ALIGN;
+  if (T == 0) return BTQ_OK;
+  const btq::NormArgs a = {y, residual, y_type, r_type, T, H, post, pre, post_weight, post_bias,
+                           pre_weight, pre_bias, post_eps, pre_eps, gate, gate_type,
+                           gate ? T / gate_rows : 1, alpha, residual_out, n, n_type, n_scale};
+  return hip_status(btq::launch_block_norm(a, (hipStream_t)stream));
+}
+
 const char* btq_status_str(int status) {
   switch (status) {
     case BTQ_OK: return "ok";
-    case BTQ_ERR_ARG: return "invalid argument (null pointer, unknown option, or momentum outside [0,1))";
-    case BTQ_ERR_SHAPE: return "invalid shape (P, T, H, k or the packed pitch out of range)";
+    case BTQ_ERR_ARG: return "invalid argument (null pointer, unknown option, or a factor out of range)";
+    case BTQ_ERR_SHAPE: return "invalid shape (a size, a stride or the packed pitch out of range)";
     case BTQ_ERR_ALIGN: return "pointer not aligned to its element type";
     case BTQ_ERR_WORKSPACE: return "workspace too small";
     case BTQ_ERR_HIP: return "HIP call failed";
@@ -317,6 +446,6 @@ const char* btq_status_str(int status) {
   }
 }
 
-const char* btq_version(void) { return "0.3.0"; }
+const char* btq_version(void) { return "0.4.0"; }
 
 }  // extern "C"

@@ -123,6 +123,49 @@ __device__ __forceinline__ TileGeom tile_geom(const int32_t* __restrict__ cmap, 
   return g;
 }
 
+// ---- values of the calls around the codec ----
+enum ValueType { kF32 = 0, kBf16 = 1, kInt8 = 2 };   // btq_type
+
+// fp32 -> bf16 bits, round to nearest even; NaN stays NaN (made quiet).
+__device__ __forceinline__ uint32_t f32_to_bf16(float f) {
+  const uint32_t u = __float_as_uint(f);
+  const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+  return (u & 0x7fffffffu) > 0x7f800000u ? (u >> 16) | 0x40u : r;
+}
+
+// The 8-bit scale of a row from the largest |x| of the row as fp32 bits
+// (bits order as values do, and Inf and NaN come above every finite value).
+// code = rint(x*mul). mul is 127/m raised by 2^-21 of itself: that outweighs
+// the three roundings of x*mul (each at most 2^-24), so an exact tie lands
+// above the half and rounds away from zero. For bf16 x no other value comes
+// that near to a tie: x*127/m = 127*mx/(ma*2^j) with mx, ma < 256 differs
+// from (2n+1)/2 by 0 or by at least 1/(254*255) of itself.
+struct RowScale {
+  float scale, mul;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t absmax_bits) {
+  const float m = __uint_as_float(absmax_bits);
+  RowScale r;
+  r.scale = m / 127.0f;
+  r.mul = 127.0f / m * (1.0f + 0x1p-21f);
+  if (absmax_bits >= 0x7f800000u) {
+    r.scale = __uint_as_float(0x7fc00000u);
+    r.mul = 0.0f;
+  } else if (r.scale < 0x1p-126f) {
+    r.scale = 1.0f;
+    r.mul = 0.0f;
+  }
+  return r;
+}
+
+// The code in the low byte: adding 1.5*2^23 leaves the rounded integer, in
+// two's complement, in the low mantissa bits. A row with mul 0 may hold Inf
+// or NaN; its codes are 0 whatever x is.
+__device__ __forceinline__ uint32_t code_bits(float x, float mul) {
+  const uint32_t b = __float_as_uint(__builtin_fmaf(x, mul, 12582912.0f));
+  return mul == 0.0f ? 0u : b & 0xffu;
+}
+
 // ---- host-side launchers (one per kernel family), called by abi.hip ----
 struct CalibPlan {
   int64_t nchunk;          // token-axis chunks reduced in parallel
@@ -168,5 +211,44 @@ hipError_t launch_decompress(const uint8_t* packed, int64_t pitch, const uint16_
                              int64_t T, int64_t H, int64_t k, const float* scale,
                              const uint8_t* zp, const int32_t* fmap, bool per_shard, void* y,
                              bool bf16, hipStream_t s);
+
+// Per-row 8-bit codes: x fp32 or bf16 [P,T,K] with row strides in elements,
+// q [P,T,q_pitch] (bytes past K are not written), scale [P,T].
+hipError_t launch_quantize_rows(const void* x, int x_type, int64_t x_shard, int64_t x_pitch,
+                                int64_t P, int64_t T, int64_t K, int8_t* q, int64_t q_pitch,
+                                float* scale, hipStream_t s);
+
+struct MatmulArgs {
+  const int8_t* a;
+  int64_t a_shard, a_pitch;
+  const float* a_scale;
+  int64_t as_shard;
+  const int8_t* w;          // [P,N,K]
+  const float* w_scale;     // [P,N]
+  const float* bias;        // [P,N] or null
+  int64_t P, T, N, K;
+  void* y;                  // [P,T,N]
+  int y_type;
+};
+hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s);
+
+struct NormArgs {
+  const void* y;            // null: no block output
+  const void* residual;
+  int y_type, r_type;
+  int64_t T, H;
+  int post, pre;            // btq_norm
+  const float *post_weight, *post_bias, *pre_weight, *pre_bias;
+  float post_eps, pre_eps;
+  const void* gate;         // null: 1
+  int gate_type;
+  int64_t gate_each;        // tokens that share one gate row
+  float alpha;
+  void* residual_out;
+  void* n;
+  int n_type;
+  float* n_scale;
+};
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
 
 }  // namespace btq

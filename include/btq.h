@@ -354,6 +354,121 @@ int btq_decompress_reduce_ex(const uint8_t *packed, int64_t packed_pitch,
  * to a multiple of 128; -1 for invalid sizes. */
 int64_t btq_packed_pitch(int64_t H, int64_t k);
 
+/* ------------------------------------------------------------------------
+ * Around the codec: the 8-bit linear layer that makes the partial sums, and
+ * the block norm that reads the reduced sum.
+ *
+ * Extra conventions of these calls
+ *  - Value types are BTQ_T_F32, BTQ_T_BF16 (raw 16-bit patterns) and, for
+ *    norm outputs, BTQ_T_INT8. Any other value returns BTQ_ERR_ARG.
+ *  - Sums, statistics and norms are fp32 (integer sums int32, exact). Each
+ *    output is rounded once, to nearest even (codes: see the calls).
+ *  - NaN and Inf are carried, not excluded: see each call.
+ *  - T == 0 does nothing. Sizes: P <= 65535, H, N, K in [1, 2^30], and every
+ *    tensor under 2^62 elements.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { BTQ_T_F32 = 0, BTQ_T_BF16 = 1, BTQ_T_INT8 = 2 } btq_type;
+
+/*
+ * Per-row 8-bit codes: activations (one scale a token) or, once, weights
+ * (one scale an output channel).
+ *
+ * For every row of K values, m = max|x| and
+ *   scale = m/127, code = x*(127/m) rounded to the nearest integer, ties away
+ *   from zero; codes lie in -127..127.
+ * For bf16 input the codes are those of exact arithmetic, ties included. A
+ * row with m/127 below 2^-126 (a row of zeros among them) gets scale 1 and
+ * codes 0. A row that holds NaN or Inf gets scale NaN and codes 0, so that
+ * everything computed from it is NaN.
+ *   x      fp32 or bf16 [P,T,K]  in; row (p,t) starts at element
+ *                                p*x_shard + t*x_pitch, its K values are
+ *                                contiguous (a row-parallel layer's shards can
+ *                                be column slices of one [T,P*K] matrix). Rows
+ *                                may overlap or coincide; strides are >= 0.
+ *   q      i8   [P,T,K]          out, contiguous
+ *   scale  fp32 [P,T]            out
+ */
+int btq_quantize_rows(const void *x, int x_type, int64_t x_shard, int64_t x_pitch,
+                      int64_t P, int64_t T, int64_t K, int8_t *q, float *scale, void *stream);
+
+/*
+ * Matrix product of 8-bit codes with a scale for each token and each output
+ * channel, for all P shards:
+ *   y[p,t,n] = (sum over k of a[p,t,k]*w[p,n,k]) * a_scale[p,t] * w_scale[p,n]
+ *              (+ bias[p,n])
+ * The sum is exact in int32 (K <= 131071, BTQ_ERR_SHAPE beyond it); it is
+ * then rounded to fp32, multiplied by a_scale, by w_scale, added to bias, each
+ * one fp32 operation, and rounded to the output type. y has the sender's
+ * layout: bf16 y is an x of btq_compress_pack.
+ *   a        i8 [P,T,K]  in; row (p,t) starts at p*a_shard + t*a_pitch
+ *            (a_shard 0: one set of rows for all shards, as in a
+ *            column-parallel layer). Strides are >= 0.
+ *   a_scale  fp32        in; of row (p,t) at p*as_shard + t, as_shard >= 0
+ *   w        i8 [P,N,K], w_scale fp32 [P,N]  in, contiguous
+ *   bias     fp32 [P,N]  in, or NULL
+ *   y        fp32 or bf16 [P,T,N]  out, contiguous
+ * Fast kernels run when a, w and their strides are multiples of 16 (so K is);
+ * other layouts are as exact and slower.
+ */
+int btq_int8_matmul(const int8_t *a, int64_t a_shard, int64_t a_pitch,
+                    const float *a_scale, int64_t as_shard,
+                    const int8_t *w, const float *w_scale, const float *bias,
+                    int64_t P, int64_t T, int64_t N, int64_t K,
+                    void *y, int y_type, void *stream);
+
+/*
+ * btq_quantize_rows on x, then btq_int8_matmul of its codes: a linear layer
+ * with 8-bit weights on fp32 or bf16 activations. Bit for bit the result of
+ * the two calls. workspace: device scratch of at least
+ * btq_int8_linear_workspace_bytes(P,T,K) bytes, 16-byte aligned, with no
+ * initial value. x_shard == 0 quantizes one set of T rows for all shards.
+ */
+int btq_int8_linear(const void *x, int x_type, int64_t x_shard, int64_t x_pitch,
+                    const int8_t *w, const float *w_scale, const float *bias,
+                    int64_t P, int64_t T, int64_t N, int64_t K,
+                    void *y, int y_type, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes for btq_int8_linear (0 for invalid sizes or T == 0). */
+size_t btq_int8_linear_workspace_bytes(int64_t P, int64_t T, int64_t K);
+
+typedef enum { BTQ_NORM_NONE = 0, BTQ_NORM_RMS = 1, BTQ_NORM_LAYER = 2 } btq_norm;
+
+/*
+ * The norms after one block and before the next, with the block's gate, its
+ * residual scale and the residual sum, in one pass:
+ *   u  = post(y)
+ *   r' = residual + alpha * (gate * u)
+ *   n  = pre(r')
+ * where, over the H features of a row,
+ *   BTQ_NORM_NONE   norm(v) = v
+ *   BTQ_NORM_RMS    norm(v) = v * (1/sqrt(mean(v^2) + eps)) * weight
+ *   BTQ_NORM_LAYER  the same of v - mean(v), plus bias
+ * All of it is fp32; n is computed from r' before r' is rounded to its type.
+ *   y             fp32 or bf16 [T,H]  in (the receiver's output), or NULL:
+ *                 then r' = residual, and post and gate must be NONE and NULL
+ *   residual      fp32 or bf16 [T,H]  in
+ *   post_weight, post_bias, pre_weight, pre_bias  fp32 [H] in, or NULL (1, 0);
+ *                 bias only for BTQ_NORM_LAYER (BTQ_ERR_ARG otherwise)
+ *   gate          fp32 or bf16 [gate_rows,H]  in, or NULL (1). gate_rows
+ *                 divides T; token t takes gate row t / (T/gate_rows): 1 is a
+ *                 gate per feature, T one per token and feature, between them
+ *                 one per sequence of equal length.
+ *   residual_out  [T,H] of the residual's type, out, or NULL. It may be
+ *                 residual itself; no other overlap is allowed.
+ *   n             [T,H] out: fp32, bf16, or int8 codes of each row as
+ *                 btq_quantize_rows defines them (of the fp32 n), or NULL
+ *   n_scale       fp32 [T] out, with int8 n only (else NULL)
+ * eps >= 0 and finite, alpha finite. NaN and Inf spread to their row's
+ * norms as the formulas give them.
+ */
+int btq_block_norm(const void *y, int y_type, const void *residual, int r_type,
+                   int64_t T, int64_t H,
+                   int post, const float *post_weight, const float *post_bias, float post_eps,
+                   const void *gate, int gate_type, int64_t gate_rows, float alpha,
+                   int pre, const float *pre_weight, const float *pre_bias, float pre_eps,
+                   void *residual_out, void *n, int n_type, float *n_scale, void *stream);
+
 /* Static text for a btq_status value (never NULL). */
 const char *btq_status_str(int status);
 
