@@ -1,6 +1,6 @@
 // extern "C" entry points of libbtq: host-side argument checks, then the
-// launchers in calib.hip, select.hip, compress.hip, decompress.hip, norm.hip,
-// rows8.hip and matmul8.hip.
+// launchers in calib.hip, select.hip, compress.hip, decompress.hip, rows.hip and
+// matmul8.hip.
 // The contract of each call is documented in include/btq.h.
 #include <math.h>
 

@@ -133,6 +133,14 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
   return (u & 0x7fffffffu) > 0x7f800000u ? (u >> 16) | 0x40u : r;
 }
 
+// Two at once (v_cvt_pk_bf16_f32): `lo` in the low half.
+__device__ __forceinline__ uint32_t f32_to_bf16x2(float lo, float hi) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const b2 v = __builtin_convertvector((f2{lo, hi}), b2);
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 // The 8-bit scale of a row from the largest |x| of the row as fp32 bits
 // (bits order as values do, and Inf and NaN come above every finite value).
 // code = rint(x*mul). mul is 127/m raised by 2^-21 of itself: that outweighs

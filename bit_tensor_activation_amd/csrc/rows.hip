@@ -1,0 +1,556 @@
+// The calls that work row by row: btq_block_norm (the norms after one block and
+// before the next, with the gate, the residual scale and the residual sum
+// between them) and btq_quantize_rows (8-bit codes with a scale for each row).
+#include "common.hpp"
+
+namespace btq {
+namespace {
+
+constexpr int kNone = 0, kLayer = 2;   // btq_norm
+
+__device__ __forceinline__ float load_value(const void* p, int type, int64_t i) {
+  return type == kBf16 ? bf16_to_f32(((const uint16_t*)p)[i]) : ((const float*)p)[i];
+}
+
+__device__ __forceinline__ void store_value(void* p, int type, int64_t i, float v) {
+  if (type == kBf16)
+    ((uint16_t*)p)[i] = (uint16_t)f32_to_bf16(v);
+  else
+    ((float*)p)[i] = v;
+}
+
+// ---- general kernels: any size, stride and alignment ----
+//
+// One block a row. Each statistic is a pass over the row, recomputed from the
+// inputs (which the caches hold after the first pass); the last pass writes.
+// They cover rows too long for the register kernels.
+constexpr int kGenThreads = 256;
+
+__device__ __forceinline__ float block_sum(float v, float* lds) {
+  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v, float* lds) {
+  for (int m = 32; m; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = __uint_as_float(v);
+  __syncthreads();
+  return max(max(__float_as_uint(lds[0]), __float_as_uint(lds[1])),
+             max(__float_as_uint(lds[2]), __float_as_uint(lds[3])));
+}
+
+__global__ __launch_bounds__(kGenThreads) void norm_general_kernel(NormArgs a) {
+  __shared__ float lds[4];
+  const float inv_h = 1.0f / (float)a.H;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int64_t row = t * a.H;
+    const int64_t grow = t / a.gate_each * a.H;
+    float mean_u = 0.0f, rstd_u = 1.0f, mean_r = 0.0f, rstd_r = 1.0f;
+
+    // value(h) summed over the row
+    auto sum = [&](auto value) {
+      float s = 0.0f;
+      for (int64_t h = threadIdx.x; h < a.H; h += kGenThreads) s += value(h);
+      return block_sum(s, lds);
+    };
+    auto y = [&](int64_t h) { return load_value(a.y, a.y_type, row + h); };
+    auto r = [&](int64_t h) {
+      const float res = load_value(a.residual, a.r_type, row + h);
+      if (!a.y) return res;
+      float u = y(h);
+      if (a.post != kNone) {
+        u = (u - mean_u) * rstd_u;
+        if (a.post_weight) u *= a.post_weight[h];
+        if (a.post_bias) u += a.post_bias[h];
+      }
+      if (a.gate) u *= load_value(a.gate, a.gate_type, grow + h);
+      return res + a.alpha * u;
+    };
+    if (a.post != kNone) {
+      if (a.post == kLayer) mean_u = sum(y) * inv_h;
+      const float var = sum([&](int64_t h) {
+        const float d = y(h) - mean_u;
+        return d * d;
+      }) * inv_h;
+      rstd_u = 1.0f / sqrtf(var + a.post_eps);
+    }
+    if (a.pre != kNone && a.n) {
+      if (a.pre == kLayer) mean_r = sum(r) * inv_h;
+      const float var = sum([&](int64_t h) {
+        const float d = r(h) - mean_r;
+        return d * d;
+      }) * inv_h;
+      rstd_r = 1.0f / sqrtf(var + a.pre_eps);
+    }
+    auto n = [&](int64_t h, float rv) {
+      if (a.pre == kNone) return rv;
+      float v = (rv - mean_r) * rstd_r;
+      if (a.pre_weight) v *= a.pre_weight[h];
+      if (a.pre_bias) v += a.pre_bias[h];
+      return v;
+    };
+    RowScale rs = {1.0f, 0.0f};
+    if (a.n && a.n_type == kInt8) {
+      uint32_t m = 0;
+      for (int64_t h = threadIdx.x; h < a.H; h += kGenThreads)
+        m = max(m, __float_as_uint(n(h, r(h))) & 0x7fffffffu);
+      rs = row_scale(block_max(m, lds));
+      if (threadIdx.x == 0) a.n_scale[t] = rs.scale;
+    }
+    for (int64_t h = threadIdx.x; h < a.H; h += kGenThreads) {
+      const float rv = r(h);
+      if (a.n) {
+        const float v = n(h, rv);
+        if (a.n_type == kInt8)
+          ((int8_t*)a.n)[row + h] = (int8_t)code_bits(v, rs.mul);
+        else
+          store_value(a.n, a.n_type, row + h, v);
+      }
+      if (a.residual_out) store_value(a.residual_out, a.r_type, row + h, rv);
+    }
+  }
+}
+
+__global__ __launch_bounds__(kGenThreads) void rows_general_kernel(
+    const void* __restrict__ x, int x_type, int64_t x_shard, int64_t x_pitch, int64_t rows,
+    int64_t T, int64_t K, int8_t* __restrict__ q, int64_t q_pitch, float* __restrict__ scale) {
+  __shared__ float lds[4];
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int64_t base = row / T * x_shard + row % T * x_pitch;
+    uint32_t m = 0;
+    for (int64_t k = threadIdx.x; k < K; k += kGenThreads)
+      m = max(m, __float_as_uint(load_value(x, x_type, base + k)) & 0x7fffffffu);
+    const RowScale rs = row_scale(block_max(m, lds));
+    if (threadIdx.x == 0) scale[row] = rs.scale;
+    for (int64_t k = threadIdx.x; k < K; k += kGenThreads)
+      q[row * q_pitch + k] = (int8_t)code_bits(load_value(x, x_type, base + k), rs.mul);
+  }
+}
+
+// ---- register kernels: a row stays in registers from its load to its store ----
+//
+// G lanes share a row, and each holds E = 8*NV of its elements. The row is
+// read once and written once; each statistic is a sum over registers, a
+// shuffle and (G > 64) one LDS exchange. A layer norm takes its variance from
+// the deviations in a second sum, so a large mean costs no precision.
+// kVec: element runs of 8 a lane, read and written as 16-byte vectors. Else
+// lanes take neighbouring elements, one at a time (odd H, odd addresses).
+// Every row access goes through a buffer descriptor over the row: what lies
+// past H loads as 0 and is not stored.
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+template <int G, int NV, bool kVec>
+struct RowMap {
+  static constexpr int E = 8 * NV;
+  int i;   // lane of the row's group
+  __device__ __forceinline__ int at(int v, int j) const {
+    return kVec ? (v * G + i) * 8 + j : (v * 8 + j) * G + i;
+  }
+  // raw words of 8 elements: 8 for fp32, 4 (or 8 halves, one a word) for bf16
+  template <int kType>
+  __device__ __forceinline__ void load(rsrc_t r, int v, uint32_t (&w)[8]) const {
+    if constexpr (!kVec) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w[j] = kType == kF32
+                   ? __builtin_amdgcn_raw_buffer_load_b32(r, (uint32_t)at(v, j) * 4u, 0, 0)
+                   : (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                         r, (uint32_t)at(v, j) * 2u, 0, 0);
+    } else if constexpr (kType == kF32) {
+      const v4u a = __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)at(v, 0) * 4u, 0, 0);
+      const v4u b = __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)at(v, 0) * 4u + 16u, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = a[j], w[4 + j] = b[j];
+    } else {
+      const v4u a = __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)at(v, 0) * 2u, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = a[j];
+    }
+  }
+  template <int kType>
+  static __device__ __forceinline__ float value(const uint32_t (&w)[8], int j) {
+    if constexpr (kType == kF32) return __uint_as_float(w[j]);
+    if constexpr (!kVec) return bf16_to_f32(w[j]);
+    return j & 1 ? __uint_as_float(w[j / 2] & 0xffff0000u) : __uint_as_float(w[j / 2] << 16);
+  }
+  template <int kType>
+  __device__ __forceinline__ void store(rsrc_t r, int v, const float (&f)[8]) const {
+    if constexpr (!kVec) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (kType == kF32)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[j]), r, (uint32_t)at(v, j) * 4u,
+                                                0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)f32_to_bf16(f[j]), r,
+                                                (uint32_t)at(v, j) * 2u, 0, 0);
+      }
+    } else if constexpr (kType == kF32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            v4u{__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]),
+                __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3])},
+            r, (uint32_t)at(v, 0) * 4u + 16u * h, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b128(
+          v4u{f32_to_bf16x2(f[0], f[1]), f32_to_bf16x2(f[2], f[3]), f32_to_bf16x2(f[4], f[5]),
+              f32_to_bf16x2(f[6], f[7])},
+          r, (uint32_t)at(v, 0) * 2u, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void store_codes(rsrc_t r, int v, const float (&f)[8],
+                                              float mul) const {
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = code_bits(f[j], mul);
+    if constexpr (kVec) {
+      __builtin_amdgcn_raw_buffer_store_b64(
+          v2u{c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
+              c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24},
+          r, (uint32_t)at(v, 0), 0, 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)c[j], r, (uint32_t)at(v, j), 0, 0);
+    }
+  }
+};
+
+// One value a lane combined over the G lanes of a row; all lanes get it.
+// `slot` is LDS that no other exchange in flight uses.
+template <int G, typename F>
+__device__ __forceinline__ uint32_t row_combine(uint32_t x, uint32_t* slot, F f) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) x = f(x, (uint32_t)__shfl_xor((int)x, m));
+  if constexpr (G > 64) {
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = x;
+    lds_barrier();
+    x = slot[0];
+#pragma unroll
+    for (int w = 1; w < G / 64; ++w) x = f(x, slot[w]);
+  }
+  return x;
+}
+template <int G>
+__device__ __forceinline__ float row_sum(float x, uint32_t* slot) {
+  return __uint_as_float(row_combine<G>(__float_as_uint(x), slot, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int G>
+__device__ __forceinline__ uint32_t row_max(uint32_t x, uint32_t* slot) {
+  return row_combine<G>(x, slot, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+
+// Statistics of the row in v: its mean (layer) and 1/sqrt(var + eps).
+template <int G, int NV, bool kVec>
+__device__ __forceinline__ void row_stats(const RowMap<G, NV, kVec>& m, const float (&v)[8 * NV],
+                                          int H, bool layer, float eps, uint32_t* slot,
+                                          float* mean, float* rstd) {
+  const float inv_h = 1.0f / (float)H;
+  float s = 0.0f;
+  *mean = 0.0f;
+  if (layer) {
+#pragma unroll
+    for (int e = 0; e < 8 * NV; ++e) s += v[e];
+    *mean = row_sum<G>(s, slot) * inv_h;
+    s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8 * NV; ++e) {
+      const float d = m.at(e / 8, e % 8) < H ? v[e] - *mean : 0.0f;
+      s = __builtin_fmaf(d, d, s);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8 * NV; ++e) s = __builtin_fmaf(v[e], v[e], s);
+  }
+  *rstd = 1.0f / sqrtf(row_sum<G>(s, slot + 16) * inv_h + eps);
+}
+
+// f = norm of 8 elements of the row.
+template <int G, int NV, bool kVec>
+__device__ __forceinline__ void row_norm(const RowMap<G, NV, kVec>& m, int v, float (&f)[8],
+                                         float mean, float rstd, const float* weight,
+                                         const float* bias, uint32_t bytes) {
+  uint32_t w[8];
+  if (weight) {
+    m.template load<kF32>(make_rsrc(weight, bytes), v, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd * __uint_as_float(w[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd;
+  }
+  if (bias) {
+    m.template load<kF32>(make_rsrc(bias, bytes), v, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] += __uint_as_float(w[j]);
+  }
+}
+
+template <int G, int NV, bool kVec, int kY, int kR>
+__global__ __launch_bounds__(G == 64 ? 256 : G) void norm_row_kernel(NormArgs a) {
+  constexpr int E = 8 * NV;
+  constexpr int kRows = G == 64 ? 4 : 1;   // rows of a block
+  // 5 exchanges a row, in two sets: a wave may enter the next row's while
+  // another still reads this one's, but never the one after that
+  __shared__ uint32_t lds[2][5 * 16];
+  RowMap<G, NV, kVec> m;
+  m.i = threadIdx.x % G;
+  const int H = (int)a.H;
+  const uint32_t h32 = (uint32_t)H * 4u;
+  int set = 0;
+  const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / G);
+  for (int64_t t = (int64_t)blockIdx.x * kRows + sub; t < a.T;
+       t += (int64_t)gridDim.x * kRows, set ^= 1) {
+    uint32_t* slot = lds[set];
+    const int64_t row = t * H;
+    constexpr int ysz = kY == kF32 ? 4 : 2, rsz = kR == kF32 ? 4 : 2;
+    const rsrc_t rr = make_rsrc((const char*)a.residual + row * rsz, (uint32_t)H * rsz);
+    float u[E];
+    uint32_t res[NV][8];
+    if (a.y) {
+      const rsrc_t ry = make_rsrc((const char*)a.y + row * ysz, (uint32_t)H * ysz);
+      uint32_t yw[NV][8];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) m.template load<kY>(ry, v, yw[v]);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) m.template load<kR>(rr, v, res[v]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) u[e] = m.template value<kY>(yw[e / 8], e % 8);
+      float mean = 0.0f, rstd = 1.0f;
+      if (a.post != kNone)
+        row_stats(m, u, H, a.post == kLayer, a.post_eps, slot, &mean, &rstd);
+      const rsrc_t rg = make_rsrc(
+          (const char*)a.gate + t / a.gate_each * H * (a.gate_type == kF32 ? 4 : 2),
+          (uint32_t)H * (a.gate_type == kF32 ? 4u : 2u));
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = u[v * 8 + j];
+        if (a.post != kNone) row_norm(m, v, f, mean, rstd, a.post_weight, a.post_bias, h32);
+        if (a.gate) {
+          uint32_t w[8];
+          if (a.gate_type == kF32) {
+            m.template load<kF32>(rg, v, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= m.template value<kF32>(w, j);
+          } else {
+            m.template load<kBf16>(rg, v, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= m.template value<kBf16>(w, j);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          u[v * 8 + j] = m.template value<kR>(res[v], j) + a.alpha * f[j];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) m.template load<kR>(rr, v, res[v]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) u[e] = m.template value<kR>(res[e / 8], e % 8);
+    }
+    if (a.residual_out) {
+      const rsrc_t ro = make_rsrc((char*)a.residual_out + row * rsz, (uint32_t)H * rsz);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = u[v * 8 + j];
+        m.template store<kR>(ro, v, f);
+      }
+    }
+    if (!a.n) continue;
+    float mean = 0.0f, rstd = 1.0f;
+    if (a.pre != kNone) {
+      row_stats(m, u, H, a.pre == kLayer, a.pre_eps, slot + 32, &mean, &rstd);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = u[v * 8 + j];
+        row_norm(m, v, f, mean, rstd, a.pre_weight, a.pre_bias, h32);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[v * 8 + j] = f[j];
+      }
+    }
+    const int nsz = a.n_type == kF32 ? 4 : a.n_type == kBf16 ? 2 : 1;
+    const rsrc_t rn = make_rsrc((char*)a.n + row * nsz, (uint32_t)(H * nsz));
+    RowScale rs = {1.0f, 0.0f};
+    if (a.n_type == kInt8) {
+      uint32_t big = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        big = max(big, m.at(e / 8, e % 8) < H ? __float_as_uint(u[e]) & 0x7fffffffu : 0u);
+      rs = row_scale(row_max<G>(big, slot + 64));
+      if (m.i == 0) a.n_scale[t] = rs.scale;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = u[v * 8 + j];
+      if (a.n_type == kInt8)
+        m.store_codes(rn, v, f, rs.mul);
+      else if (a.n_type == kBf16)
+        m.template store<kBf16>(rn, v, f);
+      else
+        m.template store<kF32>(rn, v, f);
+    }
+  }
+}
+
+// 8-bit codes of a row: the largest |x| from the bits, then the codes.
+template <int G, int NV, bool kVec, int kX>
+__global__ __launch_bounds__(G == 64 ? 256 : G) void rows_code_kernel(
+    const void* __restrict__ x, int64_t x_shard, int64_t x_pitch, uint32_t rows, uint32_t T, int K,
+    int8_t* __restrict__ q, int64_t q_pitch, float* __restrict__ scale) {
+  constexpr uint32_t kRows = G == 64 ? 4 : 1;
+  constexpr int sz = kX == kF32 ? 4 : 2;
+  __shared__ uint32_t lds[2][16];   // two rows' exchanges, as in norm_row_kernel
+  RowMap<G, NV, kVec> m;
+  m.i = threadIdx.x % G;
+  int set = 0;
+  const uint32_t sub = (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x / G);
+  for (uint32_t row = blockIdx.x * kRows + sub; row < rows; row += gridDim.x * kRows, set ^= 1) {
+    const int64_t base = (int64_t)(row / T) * x_shard + (int64_t)(row % T) * x_pitch;
+    const rsrc_t rx = make_rsrc((const char*)x + base * sz, (uint32_t)K * sz);
+    uint32_t w[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) m.template load<kX>(rx, v, w[v]);
+    uint32_t big = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        big = max(big, __float_as_uint(m.template value<kX>(w[v], j)) & 0x7fffffffu);
+    const RowScale rs = row_scale(row_max<G>(big, lds[set]));
+    if (m.i == 0) scale[row] = rs.scale;
+    const rsrc_t rq = make_rsrc(q + row * q_pitch, (uint32_t)K);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = m.template value<kX>(w[v], j);
+      m.store_codes(rq, v, f, rs.mul);
+    }
+  }
+}
+
+constexpr int64_t kMaxBlocks = int64_t(1) << 20;
+// The longest rows that stay in registers: 16 elements a lane of 1024, and
+// for a norm read by vectors 32 (element by element that spills).
+constexpr int64_t kMaxRow = 16384, kMaxVecRow = 32768;
+
+struct CodeArgs {
+  const void* x;
+  int64_t x_shard, x_pitch, P, T, K;
+  int8_t* q;
+  int64_t q_pitch;
+  float* scale;
+};
+
+template <int G, int NV, bool kVec, int kX>
+hipError_t launch_codes(const CodeArgs& c, hipStream_t s) {
+  constexpr int per = G == 64 ? 4 : 1;
+  const int64_t rows = c.P * c.T, blocks = (rows + per - 1) / per;
+  rows_code_kernel<G, NV, kVec, kX>
+      <<<dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), G == 64 ? 256 : G, 0, s>>>(
+          c.x, c.x_shard, c.x_pitch, (uint32_t)rows, (uint32_t)c.T, (int)c.K, c.q, c.q_pitch,
+          c.scale);
+  return hipGetLastError();
+}
+
+template <bool kVec, int kX>
+hipError_t launch_codes_sized(const CodeArgs& c, hipStream_t s) {
+  const bool few = c.P * c.T <= 512;
+  if (!few && c.K <= 512) return launch_codes<64, 1, kVec, kX>(c, s);
+  if (!few && c.K <= 1024) return launch_codes<64, 2, kVec, kX>(c, s);
+  if (c.K <= 2048) return launch_codes<256, 1, kVec, kX>(c, s);
+  if (!few && c.K <= 4096) return launch_codes<256, 2, kVec, kX>(c, s);
+  if (!few && c.K <= 8192) return launch_codes<256, 4, kVec, kX>(c, s);
+  if (c.K <= 8192) return launch_codes<1024, 1, kVec, kX>(c, s);
+  return launch_codes<1024, 2, kVec, kX>(c, s);
+}
+
+template <int G, int NV, bool kVec, int kY, int kR>
+hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
+  constexpr int rows = G == 64 ? 4 : 1;
+  const int64_t blocks = (a.T + rows - 1) / rows;
+  norm_row_kernel<G, NV, kVec, kY, kR>
+      <<<dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), G == 64 ? 256 : G, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int G, int NV, bool kVec>
+hipError_t launch_types(const NormArgs& a, hipStream_t s) {
+  if (a.y_type == kF32)
+    return a.r_type == kF32 ? launch_rows<G, NV, kVec, kF32, kF32>(a, s)
+                            : launch_rows<G, NV, kVec, kF32, kBf16>(a, s);
+  return a.r_type == kF32 ? launch_rows<G, NV, kVec, kBf16, kF32>(a, s)
+                          : launch_rows<G, NV, kVec, kBf16, kBf16>(a, s);
+}
+
+template <bool kVec>
+hipError_t launch_sized(const NormArgs& a, hipStream_t s) {
+  const int64_t H = a.H;
+  // Few rows leave most of the chip idle, so a row takes more lanes.
+  const bool few = a.T <= 512;
+  if (!few && H <= 512) return launch_types<64, 1, kVec>(a, s);
+  if (!few && H <= 1024) return launch_types<64, 2, kVec>(a, s);
+  if (H <= 2048) return launch_types<256, 1, kVec>(a, s);
+  if (!few && H <= 4096) return launch_types<256, 2, kVec>(a, s);
+  if (!few && H <= 8192) return launch_types<256, 4, kVec>(a, s);
+  if (H <= 8192) return launch_types<1024, 1, kVec>(a, s);
+  if constexpr (kVec) {
+    if (H > kMaxRow) return launch_types<1024, 4, kVec>(a, s);
+  }
+  return launch_types<1024, 2, kVec>(a, s);
+}
+
+bool vec_ok(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+}  // namespace
+
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
+  if (a.H <= kMaxVecRow) {
+    const bool vec = a.H % 8 == 0 && vec_ok(a.y) && vec_ok(a.residual) && vec_ok(a.gate) &&
+                     vec_ok(a.post_weight) && vec_ok(a.post_bias) && vec_ok(a.pre_weight) &&
+                     vec_ok(a.pre_bias) && vec_ok(a.residual_out) &&
+                     ((uintptr_t)a.n & (a.n_type == kInt8 ? 7 : 15)) == 0;
+    if (vec) return launch_sized<true>(a, s);
+    if (a.H <= kMaxRow) return launch_sized<false>(a, s);
+  }
+  norm_general_kernel<<<dim3((unsigned)(a.T < kMaxBlocks ? a.T : kMaxBlocks)), kGenThreads, 0,
+                        s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_rows(const void* x, int x_type, int64_t x_shard, int64_t x_pitch,
+                                int64_t P, int64_t T, int64_t K, int8_t* q, int64_t q_pitch,
+                                float* scale, hipStream_t s) {
+  const int64_t rows = P * T;
+  if (K <= kMaxRow && rows < (int64_t(1) << 31)) {
+    const CodeArgs c = {x, x_shard, x_pitch, P, T, K, q, q_pitch, scale};
+    const int64_t unit = x_type == kF32 ? 4 : 8;   // elements in 16 bytes
+    if (K % 8 == 0 && x_shard % unit == 0 && x_pitch % unit == 0 && vec_ok(x) &&
+        q_pitch % 8 == 0 && ((uintptr_t)q & 7) == 0)
+      return x_type == kF32 ? launch_codes_sized<true, kF32>(c, s)
+                            : launch_codes_sized<true, kBf16>(c, s);
+    return x_type == kF32 ? launch_codes_sized<false, kF32>(c, s)
+                          : launch_codes_sized<false, kBf16>(c, s);
+  }
+  rows_general_kernel<<<dim3((unsigned)(rows < kMaxBlocks ? rows : kMaxBlocks)), kGenThreads, 0,
+                        s>>>(x, x_type, x_shard, x_pitch, rows, T, K, q, q_pitch, scale);
+  return hipGetLastError();
+}
+
+}  // namespace btq
