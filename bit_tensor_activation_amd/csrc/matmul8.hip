@@ -245,7 +245,7 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
   const rsrc_t rw = make_rsrc(g.w + (p * g.N + n0) * g.K, (uint32_t)(nrows * K));
   const rsrc_t ra = make_rsrc(g.a + p * g.a_shard + t0 * g.a_pitch,
                               (uint32_t)((trows - 1) * pitch + K));
-  const int lrow = tid >> 3, chunk = ((tid & 7) ^ (lrow & 7)) * 16;
+  const int lrow = tid >> 3, chunk = ((tid & 7) ^ (lrow >> 1 & 7)) * 16;
   uint32_t off[kLoads];
 #pragma unroll
   for (int i = 0; i < 2 * MN; ++i)
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
   const int frow = (lane & 31) * kStep;
   // operand i of a slice
   auto read = [&](int step, int slice, int i) {
-    const int pos = ((2 * slice + (lane >> 5)) ^ (lane & 7)) * 16;
+    const int pos = ((2 * slice + (lane >> 5)) ^ (lane >> 1 & 7)) * 16;
     const int8_t* from = lds + (step & 1) * kStage + frow + pos;
     if (i < MN)
       fw[slice & 1][i] = *(const v4i*)(from + (wn + 32 * i) * kStep);
