@@ -123,54 +123,71 @@ __device__ __forceinline__ void stage_scales(const MatmulArgs& g, int64_t p, int
   }
 }
 
-// A 32x32 product: lane l holds the token l%32 and, in acc[4g + j], channel
-// 8g + 4(l/32) + j. `row` is the token's element offset in the block, kOOB for
-// one that does not exist; n the product's first channel in the block.
-// kVec: N is a multiple of 8 and y of 16 bytes.
-template <bool kVec, bool kBf>
-__device__ __forceinline__ void store_tile(const v16i& acc, const OutTile& o, uint32_t row,
-                                           float sa, int n) {
-  constexpr uint32_t sz = kBf ? 2 : 4;
-  const int h = (threadIdx.x >> 5) & 1;
-  const bool ok = row != kOOB;
+// 32 tokens x 32*MN channels of one wave: scaled, rounded, turned in LDS and
+// stored by rows. A product's lane l holds the token l%32 and, in acc[4g + j],
+// channel 8g + 4(l/32) + j: stored as they are, rows would go out in pieces of
+// 16 bytes. Through LDS (the wave's own `turn`, rows padded by 16 bytes, so
+// that the writes, 32 rows at a time, spread over the banks) a store covers
+// runs of 64*MN bytes of bf16.
+// t, n: the first token and channel within the block; rows, cols: those of the
+// block that exist. kVec: N is a multiple of 8 and y of 16 bytes.
+template <int MN, bool kBf>
+constexpr int kTurnRow = 32 * MN * (kBf ? 2 : 4) + 16;
+template <int MN, bool kBf>
+constexpr int kTurnBytes = 32 * kTurnRow<MN, kBf>;
+
+template <int MN, bool kVec, bool kBf>
+__device__ __forceinline__ void store_rows(const v16i* const (&acc)[MN], const OutTile& o,
+                                           int8_t* turn, float sa, int t, int n, int rows, int N) {
+  constexpr int sz = kBf ? 2 : 4, kRow = kTurnRow<MN, kBf>;
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  int8_t* to = turn + (lane & 31) * kRow;
 #pragma unroll
-  for (int gp = 0; gp < 2; ++gp) {
-    float f[8];
+  for (int i = 0; i < MN; ++i)
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int at = n + 8 * (2 * gp + q) + 4 * h;
-      const v4f w = *(const v4f*)(o.sw + at), b = *(const v4f*)(o.bias + at);
+    for (int g = 0; g < 4; ++g) {
+      const int c = 32 * i + 8 * g + 4 * h;
+      const v4f w = *(const v4f*)(o.sw + n + c), b = *(const v4f*)(o.bias + n + c);
+      v4f f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[4 * q + j] = scaled(acc[8 * gp + 4 * q + j], sa, w[j], b[j]);
-        if constexpr (!kVec) {
-          const uint32_t to = ok && at + j < o.cols ? (row + (uint32_t)(at + j)) * sz : kOOB;
-          if constexpr (kBf)
-            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)f32_to_bf16(f[4 * q + j]), o.y, to, 0,
-                                                  0);
-          else
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[4 * q + j]), o.y, to, 0, 0);
-        }
+      for (int j = 0; j < 4; ++j) f[j] = scaled((*acc[i])[4 * g + j], sa, w[j], b[j]);
+      if constexpr (kBf) {
+        typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+        *(v2u*)(to + c * 2) = v2u{f32_to_bf16x2(f[0], f[1]), f32_to_bf16x2(f[2], f[3])};
+      } else {
+        *(v4f*)(to + c * 4) = f;
       }
-      if constexpr (kVec && !kBf)
-        __builtin_amdgcn_raw_buffer_store_b128(
-            __builtin_bit_cast(v4i, v4f{f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]}), o.y,
-            ok && at < o.cols ? (row + (uint32_t)at) * sz : kOOB, 0, 0);
     }
-    if constexpr (kVec && kBf) {
-      // the halves of the wave trade 4 channels, so that each lane stores 8
-      // neighbouring ones
-      const uint32_t x0 = f32_to_bf16x2(f[0], f[1]), x1 = f32_to_bf16x2(f[2], f[3]);
-      const uint32_t y0 = f32_to_bf16x2(f[4], f[5]), y1 = f32_to_bf16x2(f[6], f[7]);
-      const auto p0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
-      const auto p1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-      const int at = n + 16 * gp + 8 * h;
-      __builtin_amdgcn_raw_buffer_store_b128(v4i{(int)p0[0], (int)p1[0], (int)p0[1], (int)p1[1]},
-                                             o.y,
-                                             ok && at < o.cols ? (row + (uint32_t)at) * sz : kOOB,
-                                             0, 0);
+  wave_lds_sync();
+  if constexpr (kVec) {
+    constexpr int kLanes = 32 * MN * sz / 16;   // that share a row
+    constexpr int kPass = 64 / kLanes;          // rows a pass
+    const int c = lane % kLanes * (16 / sz);
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += kPass) {
+      const int r = r0 + lane / kLanes;
+      const v4i v = *(const v4i*)(turn + r * kRow + c * sz);
+      const bool ok = t + r < rows && n + c < o.cols;
+      __builtin_amdgcn_raw_buffer_store_b128(
+          v, o.y, ok ? (uint32_t)((t + r) * N + n + c) * (uint32_t)sz : kOOB, 0, 0);
+    }
+  } else {
+    constexpr int kCols = MN < 2 ? 32 : 64;   // a pass: 64 columns of a row, or 32 of two
+#pragma unroll 4
+    for (int e = 0; e < 32 * 32 * MN; e += 64) {
+      const int at = e + lane, r = at / kCols / (32 * MN / kCols),
+                c = at % kCols + at / kCols % (32 * MN / kCols) * kCols;
+      const bool ok = t + r < rows && n + c < o.cols;
+      const uint32_t off = ok ? (uint32_t)((t + r) * N + n + c) * (uint32_t)sz : kOOB;
+      if constexpr (kBf)
+        __builtin_amdgcn_raw_buffer_store_b16(*(const uint16_t*)(turn + r * kRow + c * sz), o.y,
+                                              off, 0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b32(*(const uint32_t*)(turn + r * kRow + c * sz), o.y,
+                                              off, 0, 0);
     }
   }
+  wave_lds_sync();
 }
 
 // ---- tile kernel: K a multiple of 16, rows on 16-byte boundaries ----
@@ -330,22 +347,18 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
   if (step + 1 < steps) body(step++, yes, no);
   body(step, no, no);
 
+  lds_barrier();   // the other waves are done with the operands
   const OutTile o = {out_rsrc<kBf>(g, p, t0, n0, trows, nrows), l_sw, l_bias, nrows};
-  float sa[MT];
-  uint32_t row[MT];
+  static_assert(4 * kTurnBytes<MN, kBf> <= 2 * kStage, "the turn fits the operands' LDS");
+  int8_t* turn = lds + wave * kTurnBytes<MN, kBf>;
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
-    const int t = wt + 32 * j + (lane & 31);
-    sa[j] = l_sa[t];
-    row[j] = t < trows ? (uint32_t)(t * (int)g.N) : kOOB;
+    const v16i* part[MN];
+#pragma unroll
+    for (int i = 0; i < MN; ++i) part[i] = &acc[i][j];
+    store_rows<MN, kVec, kBf>(part, o, turn, l_sa[wt + 32 * j + (lane & 31)], wt + 32 * j, wn,
+                              trows, (int)g.N);
   }
-#pragma unroll
-  for (int i = 0; i < MN; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      store_tile<kVec, kBf>(acc[i][j], o, row[j], sa[j], wn + 32 * i);
-      issue_fence();   // one product's registers at a time
-    }
 }
 
 constexpr int64_t kMaxBlocks = int64_t(1) << 20;
