@@ -110,19 +110,6 @@ __device__ __forceinline__ rsrc_t out_rsrc(const MatmulArgs& g, int64_t p, int64
                    (uint32_t)((rows - 1) * (int)g.N + cols) * sz);
 }
 
-// A block's scales and biases to LDS, where the epilogue reads them without
-// waiting for its own stores (vector loads and stores retire in one order).
-__device__ __forceinline__ void stage_scales(const MatmulArgs& g, int64_t p, int64_t t0,
-                                             int64_t n0, int rows, int cols, int rt, int rn,
-                                             float* sa, float* sw, float* bias) {
-  for (int i = threadIdx.x; i < rt; i += blockDim.x)
-    sa[i] = i < rows ? g.a_scale[p * g.as_shard + t0 + i] : 0.0f;
-  for (int i = threadIdx.x; i < rn; i += blockDim.x) {
-    sw[i] = i < cols ? g.w_scale[p * g.N + n0 + i] : 0.0f;
-    bias[i] = g.bias && i < cols ? g.bias[p * g.N + n0 + i] : 0.0f;
-  }
-}
-
 // 32 tokens x 32*MN channels of one wave: scaled, rounded, turned in LDS and
 // stored by rows. A product's lane l holds the token l%32 and, in acc[4g + j],
 // channel 8g + 4(l/32) + j: stored as they are, rows would go out in pieces of
@@ -136,10 +123,46 @@ constexpr int kTurnRow = 32 * MN * (kBf ? 2 : 4) + 16;
 template <int MN, bool kBf>
 constexpr int kTurnBytes = 32 * kTurnRow<MN, kBf>;
 
+// 4 channels c.. of one token to its turned row.
+template <bool kBf>
+__device__ __forceinline__ void store_turn(int8_t* row, int c, v4i sum, float sa, v4f w, v4f b) {
+  v4f f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = scaled(sum[j], sa, w[j], b[j]);
+  if constexpr (kBf) {
+    typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+    *(v2u*)(row + c * 2) = v2u{f32_to_bf16x2(f[0], f[1]), f32_to_bf16x2(f[2], f[3])};
+  } else {
+    *(v4f*)(row + c * 4) = f;
+  }
+}
+
+// `count` turned rows from LDS to y, by kThreads threads.
+template <int kThreads, int MN, bool kVec, bool kBf>
+__device__ __forceinline__ void store_turned(int thread, int count, const int8_t* turn,
+                                             const OutTile& o, int t, int n, int rows, int N) {
+  constexpr int sz = kBf ? 2 : 4, kRow = kTurnRow<MN, kBf>;
+  constexpr int kRun = kVec ? 16 / sz : 1;         // elements of a store
+  constexpr int kStores = 32 * MN / kRun;          // of a row
+#pragma unroll 4
+  for (int e = thread; e < count * kStores; e += kThreads) {
+    const int r = e / kStores, c = e % kStores * kRun;
+    const int8_t* from = turn + r * kRow + c * sz;
+    const bool ok = t + r < rows && n + c < o.cols;
+    const uint32_t off = ok ? (uint32_t)((t + r) * N + n + c) * (uint32_t)sz : kOOB;
+    if constexpr (kVec)
+      __builtin_amdgcn_raw_buffer_store_b128(*(const v4i*)from, o.y, off, 0, 0);
+    else if constexpr (kBf)
+      __builtin_amdgcn_raw_buffer_store_b16(*(const uint16_t*)from, o.y, off, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b32(*(const uint32_t*)from, o.y, off, 0, 0);
+  }
+}
+
 template <int MN, bool kVec, bool kBf>
 __device__ __forceinline__ void store_rows(const v16i* const (&acc)[MN], const OutTile& o,
                                            int8_t* turn, float sa, int t, int n, int rows, int N) {
-  constexpr int sz = kBf ? 2 : 4, kRow = kTurnRow<MN, kBf>;
+  constexpr int kRow = kTurnRow<MN, kBf>;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   int8_t* to = turn + (lane & 31) * kRow;
 #pragma unroll
@@ -148,45 +171,11 @@ __device__ __forceinline__ void store_rows(const v16i* const (&acc)[MN], const O
     for (int g = 0; g < 4; ++g) {
       const int c = 32 * i + 8 * g + 4 * h;
       const v4f w = *(const v4f*)(o.sw + n + c), b = *(const v4f*)(o.bias + n + c);
-      v4f f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = scaled((*acc[i])[4 * g + j], sa, w[j], b[j]);
-      if constexpr (kBf) {
-        typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-        *(v2u*)(to + c * 2) = v2u{f32_to_bf16x2(f[0], f[1]), f32_to_bf16x2(f[2], f[3])};
-      } else {
-        *(v4f*)(to + c * 4) = f;
-      }
+      const v16i& x = *acc[i];
+      store_turn<kBf>(to, c, v4i{x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]}, sa, w, b);
     }
   wave_lds_sync();
-  if constexpr (kVec) {
-    constexpr int kLanes = 32 * MN * sz / 16;   // that share a row
-    constexpr int kPass = 64 / kLanes;          // rows a pass
-    const int c = lane % kLanes * (16 / sz);
-#pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += kPass) {
-      const int r = r0 + lane / kLanes;
-      const v4i v = *(const v4i*)(turn + r * kRow + c * sz);
-      const bool ok = t + r < rows && n + c < o.cols;
-      __builtin_amdgcn_raw_buffer_store_b128(
-          v, o.y, ok ? (uint32_t)((t + r) * N + n + c) * (uint32_t)sz : kOOB, 0, 0);
-    }
-  } else {
-    constexpr int kCols = MN < 2 ? 32 : 64;   // a pass: 64 columns of a row, or 32 of two
-#pragma unroll 4
-    for (int e = 0; e < 32 * 32 * MN; e += 64) {
-      const int at = e + lane, r = at / kCols / (32 * MN / kCols),
-                c = at % kCols + at / kCols % (32 * MN / kCols) * kCols;
-      const bool ok = t + r < rows && n + c < o.cols;
-      const uint32_t off = ok ? (uint32_t)((t + r) * N + n + c) * (uint32_t)sz : kOOB;
-      if constexpr (kBf)
-        __builtin_amdgcn_raw_buffer_store_b16(*(const uint16_t*)(turn + r * kRow + c * sz), o.y,
-                                              off, 0, 0);
-      else
-        __builtin_amdgcn_raw_buffer_store_b32(*(const uint32_t*)(turn + r * kRow + c * sz), o.y,
-                                              off, 0, 0);
-    }
-  }
+  store_turned<64, MN, kVec, kBf>(lane, 32, turn, o, t, n, rows, N);
   wave_lds_sync();
 }
 
@@ -204,19 +193,30 @@ __device__ __forceinline__ void store_rows(const v16i* const (&acc)[MN], const O
 // step after the next, and its products hide the first reads of the next step.
 constexpr int kStep = 128;
 
-// 16 bytes a lane from rsrc[off + soff] straight to LDS: lane i of the wave to
-// byte to + 16*i. `to`, an LDS address, is the same in all lanes. Written as
-// assembly because the compiler, which cannot tell the two steps' buffers
-// apart, would wait for these loads before every later LDS read; the kernel
-// orders them itself, with wait_loads and a barrier before the first read.
+// kBytes (4 or 16) a lane from rsrc[off + soff] straight to LDS: lane i of the
+// wave to byte to + kBytes*i. `to`, an LDS address, is the same in all lanes.
+// Written as assembly because the compiler, which cannot tell the steps'
+// buffers apart, would wait for these loads before every later LDS read; the
+// kernel orders them itself, with wait_loads and a barrier before the first
+// read.
+template <int kBytes>
 __device__ __forceinline__ void load_to_lds(rsrc_t r, uint32_t to, uint32_t off, uint32_t soff) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %1, %2, %3 offen lds"
-      :
-      : "s"(to), "v"(off), "s"(r), "s"(soff)
-      : "m0", "memory");
+  if constexpr (kBytes == 16)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, %3 offen lds"
+        :
+        : "s"(to), "v"(off), "s"(r), "s"(soff)
+        : "m0", "memory");
+  else
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dword %1, %2, %3 offen lds"
+        :
+        : "s"(to), "v"(off), "s"(r), "s"(soff)
+        : "m0", "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
@@ -228,156 +228,273 @@ template <int kLoads, bool kLds>
 __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt((kLoads & 15) | (kLoads >> 4) << 14 | 7 << 4 | (kLds ? 0 : 15) << 8);
 }
+// A block's share of the product: RN channels x RT tokens of shard p, and the
+// loads of its operands, 256 threads together, into S buffers of LDS.
+template <int RN, int RT, int S>
+struct Block {
+  static constexpr int kLoads = (RN + RT) / 32, kStage = (RN + RT) * kStep;
+  struct Lds {
+    __align__(1024) int8_t operands[S * kStage];
+    // whole loads of 64
+    __align__(16) float sa[(RT + 63) / 64 * 64], sw[(RN + 63) / 64 * 64], bias[(RN + 63) / 64 * 64];
+  };
+  int p, nrows, trows, K, chunk, wave;
+  int64_t n0, t0;
+  rsrc_t rw, ra;
+  uint32_t to, off[kLoads];
 
-template <int MN, int MT, bool kVec, bool kBf>
+  __device__ __forceinline__ Block(const MatmulArgs& g, int tiles_t, int tiles_n, int tiles,
+                                   Lds& lds) {
+    // Each XCD takes one run of tiles, and walks it 4 tiles of channels by
+    // many of tokens, so the blocks that run together share operands in its L2.
+    const int b = blockIdx.x, xcd = b % kXcds;
+    const int tile = xcd * (tiles / kXcds) + min(xcd, tiles % kXcds) + b / kXcds;
+    const int per_p = tiles_t * tiles_n;
+    p = tile / per_p;
+    int in = tile % per_p;
+    const int group = in / (4 * tiles_t);
+    in -= group * 4 * tiles_t;
+    const int height = min(4, tiles_n - group * 4);
+    n0 = (int64_t)(group * 4 + in % height) * RN;
+    t0 = (int64_t)(in / height) * RT;
+    nrows = (int)min((int64_t)RN, g.N - n0);
+    trows = (int)min((int64_t)RT, g.T - t0);
+    K = (int)g.K;
+    const int pitch = (int)g.a_pitch, tid = threadIdx.x, row = tid >> 3;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    rw = make_rsrc(g.w + (p * g.N + n0) * g.K, (uint32_t)(nrows * K));
+    ra = make_rsrc(g.a + p * g.a_shard + t0 * g.a_pitch, (uint32_t)((trows - 1) * pitch + K));
+    chunk = ((tid & 7) ^ (row >> 1 & 7)) * 16;
+#pragma unroll
+    for (int i = 0; i < RN / 32; ++i)
+      off[i] = (uint32_t)(min(row + 32 * i, nrows - 1) * K + chunk);
+#pragma unroll
+    for (int i = 0; i < RT / 32; ++i)
+      off[RN / 32 + i] = (uint32_t)(min(row + 32 * i, trows - 1) * pitch + chunk);
+    to = lds_address(lds.operands) + wave * 1024;
+    // The scales and biases go to LDS first, where the epilogue reads them
+    // without waiting for its own stores (vector loads and stores retire in
+    // one order). One wave loads 64 of them at a time.
+    stage(g.a_scale + p * g.as_shard + t0, trows, lds.sa, RT);
+    stage(g.w_scale + p * g.N + n0, nrows, lds.sw, RN);
+    if (g.bias)
+      stage(g.bias + p * g.N + n0, nrows, lds.bias, RN);
+    else
+      for (int i = tid; i < RN; i += 256) lds.bias[i] = 0.0f;
+  }
+  __device__ __forceinline__ void stage(const float* from, int n, float* dst, int size) const {
+    const rsrc_t r = make_rsrc(from, (uint32_t)n * 4u);
+    for (int i = wave * 64; i < size; i += 256)
+      load_to_lds<4>(r, lds_address(dst + i), (uint32_t)(i + (threadIdx.x & 63)) * 4u, 0);
+  }
+  // Load i of a step into buffer `buf`. Past the end of a row (and for the
+  // steps past the last, which keep the counts of loads in flight the same)
+  // the address is out of range: nothing is read.
+  __device__ __forceinline__ void fetch(int step, int buf, int i) const {
+    const bool in_row = step * kStep + chunk < K;
+    load_to_lds<16>(i < RN / 32 ? rw : ra, to + buf * kStage + i * 32 * kStep,
+                    in_row ? off[i] : kOOB, step * kStep);
+  }
+  __device__ __forceinline__ int steps() const { return (K + kStep - 1) / kStep; }
+  // Operand rows row..row+31 of slice `slice` in buffer `buf`: this lane's 16
+  // bytes. Channels come first, tokens from row RN.
+  static __device__ __forceinline__ v4i read(const Lds& lds, int buf, int slice, int row) {
+    const int lane = threadIdx.x & 63;
+    const int pos = ((2 * slice + (lane >> 5)) ^ (lane >> 1 & 7)) * 16;
+    return *(const v4i*)(lds.operands + buf * kStage + (lane & 31) * kStep + pos + row * kStep);
+  }
+};
+
+template <int WN, int WT, int MN, int MT, int S, bool kVec, bool kBf>
 __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
     MatmulArgs g, int tiles_t, int tiles_n, int tiles) {
-  constexpr int RN = 64 * MN, RT = 64 * MT, kLoads = 2 * MN + 2 * MT;
-  constexpr int kStage = (RN + RT) * kStep;
-  __shared__ __align__(1024) int8_t lds[2 * kStage];
-  __shared__ __align__(16) float l_sa[RT], l_sw[RN], l_bias[RN];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = (wave >> 1) * 32 * MN, wt = (wave & 1) * 32 * MT;
-
-  // Each XCD takes one run of tiles, and walks it 4 tiles of channels by many
-  // of tokens, so the blocks that run together share operands in its L2.
-  int tile;
-  {
-    const int b = blockIdx.x, xcd = b % kXcds, slot = b / kXcds;
-    const int each = tiles / kXcds, more = tiles % kXcds;
-    tile = xcd * each + min(xcd, more) + slot;
-  }
-  const int per_p = tiles_t * tiles_n;
-  const int p = tile / per_p;
-  int in = tile % per_p;
-  const int group = in / (4 * tiles_t);
-  in -= group * 4 * tiles_t;
-  const int height = min(4, tiles_n - group * 4);
-  const int64_t n0 = (int64_t)(group * 4 + in % height) * RN;
-  const int64_t t0 = (int64_t)(in / height) * RT;
-
-  const int nrows = (int)min((int64_t)RN, g.N - n0), trows = (int)min((int64_t)RT, g.T - t0);
-  const int K = (int)g.K, pitch = (int)g.a_pitch;
-  const rsrc_t rw = make_rsrc(g.w + (p * g.N + n0) * g.K, (uint32_t)(nrows * K));
-  const rsrc_t ra = make_rsrc(g.a + p * g.a_shard + t0 * g.a_pitch,
-                              (uint32_t)((trows - 1) * pitch + K));
-  const int lrow = tid >> 3, chunk = ((tid & 7) ^ (lrow >> 1 & 7)) * 16;
-  uint32_t off[kLoads];
-#pragma unroll
-  for (int i = 0; i < 2 * MN; ++i)
-    off[i] = (uint32_t)(min(lrow + 32 * i, nrows - 1) * K + chunk);
-#pragma unroll
-  for (int i = 0; i < 2 * MT; ++i)
-    off[2 * MN + i] = (uint32_t)(min(lrow + 32 * i, trows - 1) * pitch + chunk);
-
-  const int steps = (K + kStep - 1) / kStep;
-  const uint32_t to = lds_address(lds) + wave * 1024;
-  // load i of a step
-  auto fetch = [&](int step, int i) {
-    const bool in_row = step * kStep + chunk < K;
-    load_to_lds(i < 2 * MN ? rw : ra, to + (step & 1) * kStage + i * 32 * kStep,
-                in_row ? off[i] : kOOB, step * kStep);
-  };
+  static_assert(WN * WT == 4, "4 waves");
+  constexpr int RN = 32 * MN * WN, RT = 32 * MT * WT;
+  using B = Block<RN, RT, S>;
+  constexpr int kLoads = B::kLoads;
+  __shared__ typename B::Lds lds;
+  const B b(g, tiles_t, tiles_n, tiles, lds);
+  const int wn = b.wave / WT * 32 * MN, wt = b.wave % WT * 32 * MT;
   v4i fw[2][MN], fa[2][MT];
-  const int frow = (lane & 31) * kStep;
   // operand i of a slice
-  auto read = [&](int step, int slice, int i) {
-    const int pos = ((2 * slice + (lane >> 5)) ^ (lane >> 1 & 7)) * 16;
-    const int8_t* from = lds + (step & 1) * kStage + frow + pos;
+  auto read = [&](int buf, int slice, int i) {
     if (i < MN)
-      fw[slice & 1][i] = *(const v4i*)(from + (wn + 32 * i) * kStep);
+      fw[slice & 1][i] = B::read(lds, buf, slice, wn + 32 * i);
     else
-      fa[slice & 1][i - MN] = *(const v4i*)(from + (RN + wt + 32 * (i - MN)) * kStep);
+      fa[slice & 1][i - MN] = B::read(lds, buf, slice, RN + wt + 32 * (i - MN));
   };
   v16i acc[MN][MT] = {};
   // The products of a slice, in turn with the reads of the slice after it and
   // loads d0..d1 of step `ds`. The fences keep this order.
-  auto slice = [&](int set, auto has_read, int rstep, int rslice, auto has_load, int ds, int d0,
-                   int d1) {
+  auto slice = [&](int set, int rbuf, int rslice, int ds, int dbuf, int d0, int d1) {
     constexpr int kM = MN * MT, kR = MN + MT;
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
       acc[m / MT][m % MT] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
           fw[set][m / MT], fa[set][m % MT], acc[m / MT][m % MT], 0, 0, 0);
-      if constexpr (decltype(has_read)::value) {
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
-          if (r * kM / kR / 2 == m || (r * kM / kR / 2 >= kM && m == kM - 1))
-            read(rstep, rslice, r);
-      }
-      if constexpr (decltype(has_load)::value) {
+      for (int r = 0; r < kR; ++r)
+        if (min(r * kM / kR / 2, kM - 1) == m) read(rbuf, rslice, r);
 #pragma unroll
-        for (int d = 0; d < kLoads; ++d)
-          if (d >= d0 && d < d1 && (d - d0) * kM / (d1 - d0) == m) fetch(ds, d);
-      }
+      for (int d = 0; d < kLoads; ++d)
+        if (d >= d0 && d < d1 && (d - d0) * kM / (d1 - d0) == m) b.fetch(ds, dbuf, d);
       issue_fence();
     }
   };
-  constexpr std::true_type yes;
-  constexpr std::false_type no;
-  constexpr int kEarly = kLoads / 2;   // loads that go out right after the barrier
-  // One step; next, next2: the steps after it exist.
-  auto body = [&](int step, auto next, auto next2) {
-    slice(0, yes, step, 1, next, step + 1, kEarly, kLoads);
-    slice(1, yes, step, 2, no, 0, 0, 1);
-    slice(0, yes, step, 3, no, 0, 0, 1);
-    if constexpr (decltype(next)::value) {
-      wait_loads<0, true>();
-      __builtin_amdgcn_s_barrier();
-      issue_fence();
-    }
-    slice(1, next, step + 1, 0, next2, step + 2, 0, kEarly);
-  };
-
+  // half of a step's loads go out right after the barrier that frees their
+  // buffer, the other half a slice later: together they would hold up the
+  // products that follow
+  constexpr int kEarly = kLoads / 2;
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) fetch(0, i);
-  stage_scales(g, p, t0, n0, trows, nrows, RT, RN, l_sa, l_sw, l_bias);
-  wait_loads<0, true>();
+  for (int q = 0; q < S; ++q)
+#pragma unroll
+    for (int i = 0; i < (q == S - 1 ? kEarly : kLoads); ++i) b.fetch(q, q, i);
+  wait_loads<(S - 2) * kLoads + kEarly, true>();
   __builtin_amdgcn_s_barrier();
   issue_fence();
-  if (steps > 1) {
-#pragma unroll
-    for (int i = 0; i < kEarly; ++i) fetch(1, i);
-  }
 #pragma unroll
   for (int i = 0; i < MN + MT; ++i) read(0, 0, i);
-  int step = 0;
-  for (; step + 2 < steps; ++step) body(step, yes, yes);
-  if (step + 1 < steps) body(step++, yes, no);
-  body(step, no, no);
+  const int steps = b.steps();
+  int buf = 0;
+  for (int step = 0; step < steps; ++step) {
+    const int next = S == 2 ? buf ^ 1 : buf + 1 == S ? 0 : buf + 1;
+    const int last = S == 2 ? next : buf == 0 ? S - 1 : buf - 1;   // buffer of step + S - 1
+    slice(0, buf, 1, step + S - 1, last, kEarly, kLoads);
+    slice(1, buf, 2, 0, 0, 0, 0);
+    slice(0, buf, 3, 0, 0, 0, 0);
+    wait_loads<(S - 2) * kLoads, true>();   // the next step is in LDS
+    __builtin_amdgcn_s_barrier();           // for all waves, and this buffer is free
+    issue_fence();
+    slice(1, next, 0, step + S, buf, 0, kEarly);
+    buf = next;
+  }
 
-  lds_barrier();   // the other waves are done with the operands
-  const OutTile o = {out_rsrc<kBf>(g, p, t0, n0, trows, nrows), l_sw, l_bias, nrows};
-  static_assert(4 * kTurnBytes<MN, kBf> <= 2 * kStage, "the turn fits the operands' LDS");
-  int8_t* turn = lds + wave * kTurnBytes<MN, kBf>;
+  wait_loads<0, true>();   // no load may land in what is written next
+  lds_barrier();
+  const OutTile o = {out_rsrc<kBf>(g, b.p, b.t0, b.n0, b.trows, b.nrows), lds.sw, lds.bias,
+                     b.nrows};
+  static_assert(4 * kTurnBytes<MN, kBf> <= sizeof(lds.operands), "the turn fits");
+  int8_t* turn = lds.operands + b.wave * kTurnBytes<MN, kBf>;
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const v16i* part[MN];
 #pragma unroll
     for (int i = 0; i < MN; ++i) part[i] = &acc[i][j];
-    store_rows<MN, kVec, kBf>(part, o, turn, l_sa[wt + 32 * j + (lane & 31)], wt + 32 * j, wn,
-                              trows, (int)g.N);
+    store_rows<MN, kVec, kBf>(part, o, turn, lds.sa[wt + 32 * j + (threadIdx.x & 31)],
+                              wt + 32 * j, wn, b.trows, (int)g.N);
   }
+}
+
+// ---- few tokens or few tiles: the waves of a block split k ----
+//
+// The product then costs less than reading the weights, and what counts is
+// bytes in flight on every CU. The block is 32*MN channels x 32*MT tokens, so
+// that few channels still make many blocks; its four waves share the loads as
+// above and each multiplies one of a step's four slices. Their int32 sums are
+// added through LDS at the end, exact in any order.
+template <int MN, int MT, int S, bool kVec, bool kBf>
+__global__ __launch_bounds__(256, 2) void matmul_split_kernel(MatmulArgs g, int tiles_t,
+                                                              int tiles_n, int tiles) {
+  constexpr int RN = 32 * MN, RT = 32 * MT;
+  using B = Block<RN, RT, S>;
+  constexpr int kLoads = B::kLoads;
+  __shared__ typename B::Lds lds;
+  const B b(g, tiles_t, tiles_n, tiles, lds);
+#pragma unroll
+  for (int q = 0; q < S - 1; ++q)
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) b.fetch(q, q, i);
+  v16i acc[MN][MT] = {};
+  const int steps = b.steps();
+  int buf = 0;
+  for (int step = 0; step < steps; ++step) {
+    wait_loads<(S - 2) * kLoads, false>();   // this step is in LDS
+    __builtin_amdgcn_s_barrier();            // for all waves, and the last step's buffer is free
+    issue_fence();
+    v4i fw[MN], fa[MT];
+#pragma unroll
+    for (int i = 0; i < MN; ++i) fw[i] = B::read(lds, buf, b.wave, 32 * i);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fa[i] = B::read(lds, buf, b.wave, RN + 32 * i);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) b.fetch(step + S - 1, buf == 0 ? S - 1 : buf - 1, i);
+#pragma unroll
+    for (int i = 0; i < MN; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[i], fa[j], acc[i][j], 0, 0, 0);
+    issue_fence();
+    buf = buf + 1 == S ? 0 : buf + 1;
+  }
+  wait_loads<0, true>();   // no load may land in what is written next
+  lds_barrier();
+  const OutTile o = {out_rsrc<kBf>(g, b.p, b.t0, b.n0, b.trows, b.nrows), lds.sw, lds.bias,
+                     b.nrows};
+  // wave v finishes the channels 8v .. 8v+7 of every product: acc[4v .. 4v+3]
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  constexpr int kSums = 4 * MN * MT * 4 * 64 * 16;
+  static_assert(kSums + MT * kTurnBytes<MN, kBf> <= sizeof(lds.operands), "the sums fit");
+  v4i* sums = (v4i*)lds.operands;
+  int8_t* turn = lds.operands + kSums;
+#pragma unroll
+  for (int i = 0; i < MN; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        sums[((b.wave * MN * MT + i * MT + j) * 4 + v) * 64 + lane] =
+            v4i{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
+                acc[i][j][4 * v + 3]};
+  lds_barrier();
+#pragma unroll
+  for (int i = 0; i < MN; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      v4i sum = sums[((i * MT + j) * 4 + b.wave) * 64 + lane];
+#pragma unroll
+      for (int q = 1; q < 4; ++q)
+        sum += sums[((q * MN * MT + i * MT + j) * 4 + b.wave) * 64 + lane];
+      const int t = 32 * j + (lane & 31), c = 32 * i + 8 * b.wave + 4 * h;
+      const float sa = lds.sa[t];
+      const v4f w = *(const v4f*)(o.sw + c), bias = *(const v4f*)(o.bias + c);
+      store_turn<kBf>(turn + t * kTurnRow<MN, kBf>, c, sum, sa, w, bias);
+    }
+  lds_barrier();
+  store_turned<256, MN, kVec, kBf>((int)threadIdx.x, RT, turn, o, 0, 0, b.trows, (int)g.N);
 }
 
 constexpr int64_t kMaxBlocks = int64_t(1) << 20;
 
-template <int MN, int MT>
-hipError_t launch_tiles(const MatmulArgs& a, hipStream_t s) {
-  const int64_t tt = (a.T + 64 * MT - 1) / (64 * MT), tn = (a.N + 64 * MN - 1) / (64 * MN);
-  const dim3 grid((unsigned)(a.P * tt * tn));
+// A kernel over RN x RT tiles; kernel(vec, bf16, grid, tiles of t, of n, of all).
+template <int RN, int RT, typename F>
+hipError_t launch_tiled(const MatmulArgs& a, F kernel) {
+  const int64_t tt = (a.T + RT - 1) / RT, tn = (a.N + RN - 1) / RN, n = a.P * tt * tn;
   const bool bf = a.y_type == kBf16, vec = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
-  const int itt = (int)tt, itn = (int)tn, n = (int)(a.P * tt * tn);
-  if (vec && bf)
-    matmul_tile_kernel<MN, MT, true, true><<<grid, 256, 0, s>>>(a, itt, itn, n);
-  else if (vec)
-    matmul_tile_kernel<MN, MT, true, false><<<grid, 256, 0, s>>>(a, itt, itn, n);
-  else if (bf)
-    matmul_tile_kernel<MN, MT, false, true><<<grid, 256, 0, s>>>(a, itt, itn, n);
+  const auto run = [&](auto v, auto b) { kernel(v, b, dim3((unsigned)n), (int)tt, (int)tn, (int)n); };
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+  if (vec)
+    bf ? run(yes, yes) : run(yes, no);
   else
-    matmul_tile_kernel<MN, MT, false, false><<<grid, 256, 0, s>>>(a, itt, itn, n);
+    bf ? run(no, yes) : run(no, no);
   return hipGetLastError();
+}
+
+template <int WN, int WT, int MN, int MT, int S>
+hipError_t launch_tiles(const MatmulArgs& a, hipStream_t s) {
+  return launch_tiled<32 * MN * WN, 32 * MT * WT>(
+      a, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
+        matmul_tile_kernel<WN, WT, MN, MT, S, decltype(v)::value, decltype(b)::value>
+            <<<grid, 256, 0, s>>>(a, tt, tn, n);
+      });
+}
+
+template <int MN, int MT, int S>
+hipError_t launch_split(const MatmulArgs& a, hipStream_t s) {
+  return launch_tiled<32 * MN, 32 * MT>(a, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
+    matmul_split_kernel<MN, MT, S, decltype(v)::value, decltype(b)::value>
+        <<<grid, 256, 0, s>>>(a, tt, tn, n);
+  });
 }
 
 // Direct 16-byte loads need every row on a 16-byte boundary; a block's rows of
@@ -388,13 +505,73 @@ bool rows_aligned(const MatmulArgs& a) {
          a.a_pitch < (int64_t(1) << 22) && a.N < (int64_t(1) << 20);
 }
 
+// The tile for a product of more than 64 tokens: the one whose blocks, in
+// rounds over the chip's 256 CUs, cost least. A cost is the time of a round
+// with `few` (at most 256) or `full` (512, two a CU) blocks in units of a round
+// of 256 x 256 tiles, measured at K=4096: T=64 .. 4096, N=4096 .. 8192, P=1 and
+// 8. One tile for all sizes loses up to 5x (T=128 N=4096 K=4096: 8.3 us with
+// 32 x 64 tiles, 41.5 us with 256 x 256; T=8192 N=8192 K=8192: 450 us with
+// 256 x 256, 560 us with 128 x 128).
+enum Tile { k256x256, k128x128, k128x64, k64x64, k32x64, k32x32, kTiles };
+
+Tile choose_tile(const MatmulArgs& a) {
+  struct {
+    int n, t;
+    float few, full;
+  } const tiles[kTiles] = {{256, 256, 1.0f, 2.0f},  {128, 128, 0.37f, 0.62f},
+                           {128, 64, 0.26f, 0.42f}, {64, 64, 0.17f, 0.30f},
+                           {32, 64, 0.13f, 0.22f},  {32, 32, 0.11f, 0.16f}};
+  Tile best = k256x256;
+  float least = 0.0f;
+  for (int i = 0; i < kTiles; ++i) {
+    const int64_t blocks =
+        a.P * ((a.T + tiles[i].t - 1) / tiles[i].t) * ((a.N + tiles[i].n - 1) / tiles[i].n);
+    float cost = blocks <= 256 ? tiles[i].few : (float)((blocks + 511) / 512) * tiles[i].full;
+    if (i == k256x256) {
+      cost = (float)((blocks + 255) / 256);
+      // With short sums a block mostly waits for its first loads and its
+      // stores, which a second block on the CU covers: at P=8 T=2048 N=4096
+      // 256 x 256 and 128 x 128 tiles take 52.8 and 46.9 us for K=256, 61.2
+      // and 63.0 us for K=512.
+      if (a.K <= 256) cost *= 1.4f;
+    }
+    if (i == 0 || cost < least) best = (Tile)i, least = cost;
+  }
+  return best;
+}
+
 }  // namespace
 
 hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
-  const int64_t t128 = (a.T + 127) / 128, n128 = (a.N + 127) / 128;
-  if (rows_aligned(a) && a.P * t128 * n128 <= kMaxBlocks) {
-    if (a.P * ((t128 + 1) / 2) * ((n128 + 1) / 2) >= 256) return launch_tiles<4, 4>(a, s);
-    return launch_tiles<2, 2>(a, s);
+  const int64_t n32 = a.P * ((a.N + 31) / 32), t32 = (a.T + 31) / 32;
+  if (rows_aligned(a) && n32 * t32 <= kMaxBlocks * 8) {
+    const int64_t n128 = a.P * ((a.N + 127) / 128), n64 = a.P * ((a.N + 63) / 64);
+    // Few tokens: the weights are read once, and the tile only has to keep
+    // every CU loading. 128 channels a block share the activations best; with
+    // fewer than two such blocks a CU, smaller ones fill the chip (T=64 N=1024
+    // P=8 K=8192: 16.2 us with 32 channels, 28.2 with 128). For up to 32 tokens
+    // and long k, 64 channels by split waves read more steadily than 128 (T=16
+    // N=8192 P=8 K=4096: 54.7 against 63.2 us; K=1024: 15.1 against 13.5).
+    if (a.T <= 32) {
+      if (n128 >= 512 && a.K <= 2048) return launch_tiles<4, 1, 1, 1, 3>(a, s);
+      if (n64 >= 512) return launch_split<2, 1, 6>(a, s);
+      return launch_split<1, 1, 6>(a, s);
+    }
+    if (a.T <= 64) {
+      if (n128 >= 512) return launch_tiles<4, 1, 1, 2, 3>(a, s);
+      if (n32 >= 256) return launch_split<1, 2, 6>(a, s);
+      return launch_split<1, 1, 6>(a, s);
+    }
+    switch (choose_tile(a)) {
+      case k256x256: return launch_tiles<2, 2, 4, 4, 2>(a, s);
+      case k128x128:   // one block a CU: more steps in flight
+        return n128 * ((a.T + 127) / 128) <= 256 ? launch_tiles<2, 2, 2, 2, 4>(a, s)
+                                                 : launch_tiles<2, 2, 2, 2, 2>(a, s);
+      case k128x64: return launch_tiles<4, 1, 1, 2, 3>(a, s);
+      case k64x64: return launch_split<2, 2, 6>(a, s);
+      case k32x64: return launch_split<1, 2, 6>(a, s);
+      default: return launch_split<1, 1, 6>(a, s);
+    }
   }
   const int64_t tt = (a.T + kGenTile - 1) / kGenTile, tn = (a.N + kGenTile - 1) / kGenTile;
   const int64_t tiles = a.P * tt * tn;
