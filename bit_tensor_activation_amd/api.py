@@ -365,28 +365,37 @@ def btq_decompress_reduce_per_shard(packed: torch.Tensor, outliers: torch.Tensor
 _T = {torch.float32: _lib.BTQ_T_F32, torch.bfloat16: _lib.BTQ_T_BF16, torch.int16: _lib.BTQ_T_BF16,
       torch.int8: _lib.BTQ_T_INT8}
 _VALUES = (torch.float32, torch.bfloat16, torch.int16)
+_F32, _I8 = (torch.float32,), (torch.int8,)
 _NORMS = {"none": _lib.BTQ_NORM_NONE, "rms": _lib.BTQ_NORM_RMS, "layer": _lib.BTQ_NORM_LAYER}
 
 
-def _opt(t: Optional[torch.Tensor], name: str, dtypes, shape, dev) -> Optional[int]:
-    """Data pointer of an optional contiguous tensor."""
-    if t is None:
-        return None
+def _at(t: torch.Tensor, name: str, dtypes, shape, dev) -> int:
+    """Data pointer of a contiguous tensor, checked."""
     # the quick form of _need: its messages only when something is wrong
-    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.device != dev:
+    if (t.dtype not in dtypes or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != dev.index):
         _need(t, name, dtypes, shape, dev)
-    return t.data_ptr() if t.numel() else None
+    return t.data_ptr()
 
 
-def _rows(x: torch.Tensor, name: str, dtypes, dev):
+def _stream_of(dev: torch.device, stream):
+    """_launch, with the quick way to torch's current stream: these calls are
+    short enough for the host's part of them to count."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index), _HERE
+    return _launch(dev, stream)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _rows(x: torch.Tensor, name: str, dtypes):
     """(P or None, T, K, shard stride, row pitch) of rows [T,K] or [P,T,K] whose
     last dimension is contiguous."""
     if x.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {x.dtype}, expected one of {dtypes}")
     if x.dim() not in (2, 3):
         raise ValueError(f"{name}: shape {tuple(x.shape)}, expected [T,K] or [P,T,K]")
-    if x.device != dev:
-        raise ValueError(f"{name}: on {x.device}, expected {dev}")
     if x.stride(-1) != 1 and x.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if x.dim() == 2:
@@ -403,18 +412,18 @@ def btq_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     dimension. For weights [P,N,K] the rows are the output channels.
     """
     dev = _device(x)
-    P, T, K, shard, pitch = _rows(x, "x", _VALUES, dev)
+    P, T, K, shard, pitch = _rows(x, "x", _VALUES)
     shape = tuple(x.shape)
-    sh, ctx = _launch(dev, stream)
+    sh, ctx = _stream_of(dev, stream)
     with ctx:
         if q is None:
             q = torch.empty(shape, dtype=torch.int8, device=dev)
         if scale is None:
             scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         st = _lib.load().btq_quantize_rows(
-            _ptr(x), _T[x.dtype], shard, pitch, 1 if P is None else P, T, K,
-            _opt(q, "q", (torch.int8,), shape, dev),
-            _opt(scale, "scale", (torch.float32,), shape[:-1], dev), sh)
+            x.data_ptr(), _T[x.dtype], shard, pitch, 1 if P is None else P, T, K,
+            _at(q, "q", _I8, shape, dev),
+            _at(scale, "scale", _F32, shape[:-1], dev), sh)
     _lib.check(st, "btq_quantize_rows")
     return q, scale
 
@@ -426,13 +435,13 @@ def _product_args(x_p, T, K, w, w_scale, bias, y, bf16, y_like, dev):
     P, N = w.shape[0], w.shape[1]
     if x_p is not None and x_p != P:
         raise ValueError(f"w: {P} shards, the activations have {x_p}")
-    wp = _opt(w, "w", (torch.int8,), (P, N, K), dev)
-    sp = _opt(w_scale, "w_scale", (torch.float32,), (P, N), dev)
-    bp = _opt(bias, "bias", (torch.float32,), (P, N), dev)
+    wp = _at(w, "w", _I8, (P, N, K), dev)
+    sp = _at(w_scale, "w_scale", _F32, (P, N), dev)
+    bp = None if bias is None else _at(bias, "bias", _F32, (P, N), dev)
     if y is None:
         dt = torch.float32 if not bf16 else y_like
         y = torch.empty((P, T, N), dtype=dt, device=dev)
-    return P, N, wp, sp, bp, y, _opt(y, "y", _VALUES, (P, T, N), dev)
+    return P, N, wp, sp, bp, y, _at(y, "y", _VALUES, (P, T, N), dev)
 
 
 def btq_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
@@ -448,20 +457,20 @@ def btq_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
     torch.bfloat16 or int16.
     """
     dev = _device(a)
-    x_p, T, K, shard, pitch = _rows(a, "a", (torch.int8,), dev)
-    sh, ctx = _launch(dev, stream)
+    x_p, T, K, shard, pitch = _rows(a, "a", _I8)
+    sh, ctx = _stream_of(dev, stream)
     with ctx:
         P, N, wp, sp, bp, y, yp = _product_args(x_p, T, K, w, w_scale, bias, y, bf16, torch.int16,
                                                 dev)
-        asp = _opt(a_scale, "a_scale", (torch.float32,), (T,) if x_p is None else (P, T), dev)
-        st = _lib.load().btq_int8_matmul(_ptr(a), shard, pitch, asp, 0 if x_p is None else T, wp,
+        asp = _at(a_scale, "a_scale", _F32, (T,) if x_p is None else (P, T), dev)
+        st = _lib.load().btq_int8_matmul(a.data_ptr(), shard, pitch, asp, 0 if x_p is None else T, wp,
                                          sp, bp, P, T, N, K, yp, _T[y.dtype], sh)
     _lib.check(st, "btq_int8_matmul")
     return y
 
 
 def btq_int8_linear_workspace_bytes(P: int, T: int, K: int) -> int:
-    return int(_lib.load().btq_int8_linear_workspace_bytes(P, T, K))
+    return _lib.load().btq_int8_linear_workspace_bytes(P, T, K)
 
 
 def btq_int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -475,17 +484,17 @@ def btq_int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     of bf16 (int16 bits for float32 x).
     """
     dev = _device(x)
-    x_p, T, K, shard, pitch = _rows(x, "x", _VALUES, dev)
+    x_p, T, K, shard, pitch = _rows(x, "x", _VALUES)
     like = torch.bfloat16 if x.dtype == torch.bfloat16 else torch.int16
-    sh, ctx = _launch(dev, stream)
+    sh, ctx = _stream_of(dev, stream)
     with ctx:
         P, N, wp, sp, bp, y, yp = _product_args(x_p, T, K, w, w_scale, bias, y, bf16, like, dev)
         if workspace is None:
             workspace = torch.empty(btq_int8_linear_workspace_bytes(P, T, K), dtype=torch.uint8,
                                     device=dev)
         st = _lib.load().btq_int8_linear(
-            _ptr(x), _T[x.dtype], shard, pitch, wp, sp, bp, P, T, N, K, yp, _T[y.dtype],
-            _ptr(workspace), workspace.numel() * workspace.element_size(), sh)
+            x.data_ptr(), _T[x.dtype], shard, pitch, wp, sp, bp, P, T, N, K, yp, _T[y.dtype],
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), sh)
     _lib.check(st, "btq_int8_linear")
     return y
 
@@ -515,28 +524,27 @@ def btq_block_norm(y: Optional[torch.Tensor], residual: torch.Tensor, post: str 
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError(f"post and pre must be among {sorted(_NORMS)}")
     shape = T, H = residual.shape
-    rp = _opt(residual, "residual", _VALUES, shape, dev)
-    yp = _opt(y, "y", _VALUES, shape, dev)
-    f32 = (torch.float32,)
-    pw, pb = _opt(post_weight, "post_weight", f32, (H,), dev), _opt(post_bias, "post_bias", f32,
-                                                                  (H,), dev)
-    nw, nb = _opt(pre_weight, "pre_weight", f32, (H,), dev), _opt(pre_bias, "pre_bias", f32, (H,),
-                                                                dev)
+    rp = _at(residual, "residual", _VALUES, shape, dev)
+    yp = None if y is None else _at(y, "y", _VALUES, shape, dev)
+    pw, pb, nw, nb = [
+        None if t is None else _at(t, name, _F32, (H,), dev)
+        for name, t in (("post_weight", post_weight), ("post_bias", post_bias),
+                        ("pre_weight", pre_weight), ("pre_bias", pre_bias))]
     gp, gt, gr = None, 0, 1
     if gate is not None:
         gr = gate.shape[0] if gate.dim() == 2 else 0
-        gp, gt = _opt(gate, "gate", _VALUES, (gr, H), dev), _T[gate.dtype]
-    sh, ctx = _launch(dev, stream)
+        gp, gt = _at(gate, "gate", _VALUES, (gr, H), dev), _T[gate.dtype]
+    sh, ctx = _stream_of(dev, stream)
     with ctx:
         if residual_out is None:
             residual_out = torch.empty_like(residual)
-        op = _opt(residual_out, "residual_out", (residual.dtype,), shape, dev)
+        op = _at(residual_out, "residual_out", (residual.dtype,), shape, dev)
         if n is None:
             n = torch.empty(shape, dtype=residual.dtype if n_dtype is None else n_dtype, device=dev)
-        np_ = _opt(n, "n", _VALUES + (torch.int8,), shape, dev)
+        np_ = _at(n, "n", _VALUES + (torch.int8,), shape, dev)
         if n.dtype == torch.int8 and n_scale is None:
             n_scale = torch.empty((T,), dtype=torch.float32, device=dev)
-        sp = _opt(n_scale, "n_scale", f32, (T,), dev)
+        sp = None if n_scale is None else _at(n_scale, "n_scale", _F32, (T,), dev)
         st = _lib.load().btq_block_norm(
             yp, 0 if y is None else _T[y.dtype], rp, _T[residual.dtype], T, H, _NORMS[post], pw,
             pb, eps if post_eps is None else post_eps, gp, gt, gr, alpha, _NORMS[pre], nw, nb, eps,
