@@ -40,8 +40,9 @@ __device__ __forceinline__ float scaled(int sum, float sa, float sw, float b) {
 
 // ---- general kernel: any size, stride and alignment ----
 //
-// 64 tokens x 64 channels a block, 4 waves of 32x32, 64 bytes of k a step
-// through LDS (rows padded to 80 bytes).
+// For k below 16, and rows or strides too large for 32-bit offsets: 64 tokens x
+// 64 channels a block, 4 waves of 32x32, 64 bytes of k a step through LDS (rows
+// padded to 80 bytes).
 constexpr int kGenTile = 64, kGenK = 64, kGenRow = 80;
 
 __global__ __launch_bounds__(256) void matmul_general_kernel(MatmulArgs g, int64_t tiles_t,
@@ -137,7 +138,10 @@ __device__ __forceinline__ void store_turn(int8_t* row, int c, v4i sum, float sa
   }
 }
 
-// `count` turned rows from LDS to y, by kThreads threads.
+// `count` turned rows from LDS to y, by kThreads threads. Stored with the
+// streaming hint: y does not push the operands out of the caches (P=8 T=2048
+// N=4096: K=512 71.0 -> 63.5 us; with btq_compress_pack reading y next, K=2048
+// 194.5 -> 191.3 us for both).
 template <int kThreads, int MN, bool kVec, bool kBf>
 __device__ __forceinline__ void store_turned(int thread, int count, const int8_t* turn,
                                              const OutTile& o, int t, int n, int rows, int N) {
@@ -151,7 +155,7 @@ __device__ __forceinline__ void store_turned(int thread, int count, const int8_t
     const bool ok = t + r < rows && n + c < o.cols;
     const uint32_t off = ok ? (uint32_t)((t + r) * N + n + c) * (uint32_t)sz : kOOB;
     if constexpr (kVec)
-      __builtin_amdgcn_raw_buffer_store_b128(*(const v4i*)from, o.y, off, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(*(const v4i*)from, o.y, off, 0, kStream);
     else if constexpr (kBf)
       __builtin_amdgcn_raw_buffer_store_b16(*(const uint16_t*)from, o.y, off, 0, 0);
     else
@@ -198,7 +202,7 @@ constexpr int kStep = 128;
 // Written as assembly because the compiler, which cannot tell the steps'
 // buffers apart, would wait for these loads before every later LDS read; the
 // kernel orders them itself, with wait_loads and a barrier before the first
-// read.
+// read. (m0 is reserved and nothing else in these kernels uses it.)
 template <int kBytes>
 __device__ __forceinline__ void load_to_lds(rsrc_t r, uint32_t to, uint32_t off, uint32_t soff) {
   if constexpr (kBytes == 16)
@@ -208,7 +212,7 @@ __device__ __forceinline__ void load_to_lds(rsrc_t r, uint32_t to, uint32_t off,
         "buffer_load_dwordx4 %1, %2, %3 offen lds"
         :
         : "s"(to), "v"(off), "s"(r), "s"(soff)
-        : "m0", "memory");
+        : "memory");
   else
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
@@ -216,7 +220,7 @@ __device__ __forceinline__ void load_to_lds(rsrc_t r, uint32_t to, uint32_t off,
         "buffer_load_dword %1, %2, %3 offen lds"
         :
         : "s"(to), "v"(off), "s"(r), "s"(soff)
-        : "m0", "memory");
+        : "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
@@ -240,6 +244,7 @@ struct Block {
   };
   int p, nrows, trows, K, chunk, wave;
   int64_t n0, t0;
+  const int8_t *w, *a;      // the block's first rows
   rsrc_t rw, ra;
   uint32_t to, off[kLoads];
 
@@ -262,8 +267,10 @@ struct Block {
     K = (int)g.K;
     const int pitch = (int)g.a_pitch, tid = threadIdx.x, row = tid >> 3;
     wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    rw = make_rsrc(g.w + (p * g.N + n0) * g.K, (uint32_t)(nrows * K));
-    ra = make_rsrc(g.a + p * g.a_shard + t0 * g.a_pitch, (uint32_t)((trows - 1) * pitch + K));
+    w = g.w + (p * g.N + n0) * g.K;
+    a = g.a + p * g.a_shard + t0 * g.a_pitch;
+    rw = make_rsrc(w, (uint32_t)(nrows * K));
+    ra = make_rsrc(a, (uint32_t)((trows - 1) * pitch + K));
     chunk = ((tid & 7) ^ (row >> 1 & 7)) * 16;
 #pragma unroll
     for (int i = 0; i < RN / 32; ++i)
@@ -295,6 +302,25 @@ struct Block {
     load_to_lds<16>(i < RN / 32 ? rw : ra, to + buf * kStage + i * 32 * kStep,
                     in_row ? off[i] : kOOB, step * kStep);
   }
+  // The same load to registers, for rows on any byte: 16 bytes that end inside
+  // the row, shifted down to where they belong.
+  __device__ __forceinline__ v4i load(int step, int i) const {
+    const int8_t* from = i < RN / 32 ? w : a;
+    const int k = step * kStep;
+    v4i v;
+    if (k + kStep <= K) {
+      __builtin_memcpy(&v, from + (off[i] + (uint32_t)k), 16);
+      return v;
+    }
+    const int past = max(k + chunk + 16 - K, 0);   // bytes of the chunk past the row
+    if (past >= 16) return v4i{0, 0, 0, 0};
+    __builtin_memcpy(&v, from + (off[i] + (uint32_t)(k - past)), 16);
+    const unsigned __int128 bits = __builtin_bit_cast(unsigned __int128, v) >> (8 * past);
+    return __builtin_bit_cast(v4i, bits);
+  }
+  static __device__ __forceinline__ void put(Lds& lds, int buf, int i, v4i v) {
+    *(v4i*)(lds.operands + buf * kStage + i * 32 * kStep + threadIdx.x * 16) = v;
+  }
   __device__ __forceinline__ int steps() const { return (K + kStep - 1) / kStep; }
   // Operand rows row..row+31 of slice `slice` in buffer `buf`: this lane's 16
   // bytes. Channels come first, tokens from row RN.
@@ -305,10 +331,13 @@ struct Block {
   }
 };
 
-template <int WN, int WT, int MN, int MT, int S, bool kVec, bool kBf>
+//
+// kDirect: K and every row on 16 bytes. Otherwise (S = 2) the next step's
+// operands wait in registers while this one is multiplied.
+template <int WN, int WT, int MN, int MT, int S, bool kDirect, bool kVec, bool kBf>
 __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
     MatmulArgs g, int tiles_t, int tiles_n, int tiles) {
-  static_assert(WN * WT == 4, "4 waves");
+  static_assert(WN * WT == 4 && (kDirect || S == 2), "4 waves");
   constexpr int RN = 32 * MN * WN, RT = 32 * MT * WT;
   using B = Block<RN, RT, S>;
   constexpr int kLoads = B::kLoads;
@@ -337,36 +366,61 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
         if (min(r * kM / kR / 2, kM - 1) == m) read(rbuf, rslice, r);
 #pragma unroll
       for (int d = 0; d < kLoads; ++d)
-        if (d >= d0 && d < d1 && (d - d0) * kM / (d1 - d0) == m) b.fetch(ds, dbuf, d);
+        if (kDirect && d >= d0 && d < d1 && (d - d0) * kM / (d1 - d0) == m) b.fetch(ds, dbuf, d);
       issue_fence();
     }
   };
-  // half of a step's loads go out right after the barrier that frees their
-  // buffer, the other half a slice later: together they would hold up the
-  // products that follow
-  constexpr int kEarly = kLoads / 2;
-#pragma unroll
-  for (int q = 0; q < S; ++q)
-#pragma unroll
-    for (int i = 0; i < (q == S - 1 ? kEarly : kLoads); ++i) b.fetch(q, q, i);
-  wait_loads<(S - 2) * kLoads + kEarly, true>();
-  __builtin_amdgcn_s_barrier();
-  issue_fence();
-#pragma unroll
-  for (int i = 0; i < MN + MT; ++i) read(0, 0, i);
   const int steps = b.steps();
   int buf = 0;
-  for (int step = 0; step < steps; ++step) {
-    const int next = S == 2 ? buf ^ 1 : buf + 1 == S ? 0 : buf + 1;
-    const int last = S == 2 ? next : buf == 0 ? S - 1 : buf - 1;   // buffer of step + S - 1
-    slice(0, buf, 1, step + S - 1, last, kEarly, kLoads);
-    slice(1, buf, 2, 0, 0, 0, 0);
-    slice(0, buf, 3, 0, 0, 0, 0);
-    wait_loads<(S - 2) * kLoads, true>();   // the next step is in LDS
-    __builtin_amdgcn_s_barrier();           // for all waves, and this buffer is free
+  if constexpr (kDirect) {
+    // half of a step's loads go out right after the barrier that frees their
+    // buffer, the other half a slice later: together they would hold up the
+    // products that follow
+    constexpr int kEarly = kLoads / 2;
+#pragma unroll
+    for (int q = 0; q < S; ++q)
+#pragma unroll
+      for (int i = 0; i < (q == S - 1 ? kEarly : kLoads); ++i) b.fetch(q, q, i);
+    wait_loads<(S - 2) * kLoads + kEarly, true>();
+    __builtin_amdgcn_s_barrier();
     issue_fence();
-    slice(1, next, 0, step + S, buf, 0, kEarly);
-    buf = next;
+#pragma unroll
+    for (int i = 0; i < MN + MT; ++i) read(0, 0, i);
+    for (int step = 0; step < steps; ++step) {
+      const int next = S == 2 ? buf ^ 1 : buf + 1 == S ? 0 : buf + 1;
+      const int last = S == 2 ? next : buf == 0 ? S - 1 : buf - 1;   // buffer of step + S - 1
+      slice(0, buf, 1, step + S - 1, last, kEarly, kLoads);
+      slice(1, buf, 2, 0, 0, 0, 0);
+      slice(0, buf, 3, 0, 0, 0, 0);
+      wait_loads<(S - 2) * kLoads, true>();   // the next step is in LDS
+      __builtin_amdgcn_s_barrier();           // for all waves, and this buffer is free
+      issue_fence();
+      slice(1, next, 0, step + S, buf, 0, kEarly);
+      buf = next;
+    }
+  } else {
+    v4i next_rows[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) next_rows[i] = b.load(0, i);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) B::put(lds, 0, i, next_rows[i]);
+    wait_loads<0, true>();   // also the scales
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < MN + MT; ++i) read(0, 0, i);
+    for (int step = 0; step < steps; ++step, buf ^= 1) {
+      if (step + 1 < steps) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) next_rows[i] = b.load(step + 1, i);
+      }
+      slice(0, buf, 1, 0, 0, 0, 0);
+      slice(1, buf, 2, 0, 0, 0, 0);
+      slice(0, buf, 3, 0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) B::put(lds, buf ^ 1, i, next_rows[i]);
+      lds_barrier();
+      slice(1, buf ^ 1, 0, 0, 0, 0, 0);
+    }
   }
 
   wait_loads<0, true>();   // no load may land in what is written next
@@ -392,7 +446,7 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
 // that few channels still make many blocks; its four waves share the loads as
 // above and each multiplies one of a step's four slices. Their int32 sums are
 // added through LDS at the end, exact in any order.
-template <int MN, int MT, int S, bool kVec, bool kBf>
+template <int MN, int MT, int S, bool kDirect, bool kVec, bool kBf>
 __global__ __launch_bounds__(256, 2) void matmul_split_kernel(MatmulArgs g, int tiles_t,
                                                               int tiles_n, int tiles) {
   constexpr int RN = 32 * MN, RT = 32 * MT;
@@ -400,31 +454,58 @@ __global__ __launch_bounds__(256, 2) void matmul_split_kernel(MatmulArgs g, int 
   constexpr int kLoads = B::kLoads;
   __shared__ typename B::Lds lds;
   const B b(g, tiles_t, tiles_n, tiles, lds);
-#pragma unroll
-  for (int q = 0; q < S - 1; ++q)
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) b.fetch(q, q, i);
   v16i acc[MN][MT] = {};
-  const int steps = b.steps();
-  int buf = 0;
-  for (int step = 0; step < steps; ++step) {
-    wait_loads<(S - 2) * kLoads, false>();   // this step is in LDS
-    __builtin_amdgcn_s_barrier();            // for all waves, and the last step's buffer is free
-    issue_fence();
-    v4i fw[MN], fa[MT];
+  v4i fw[MN], fa[MT];
+  auto read = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < MN; ++i) fw[i] = B::read(lds, buf, b.wave, 32 * i);
 #pragma unroll
     for (int i = 0; i < MT; ++i) fa[i] = B::read(lds, buf, b.wave, RN + 32 * i);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) b.fetch(step + S - 1, buf == 0 ? S - 1 : buf - 1, i);
+  };
+  auto multiply = [&]() {
 #pragma unroll
     for (int i = 0; i < MN; ++i)
 #pragma unroll
       for (int j = 0; j < MT; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[i], fa[j], acc[i][j], 0, 0, 0);
-    issue_fence();
-    buf = buf + 1 == S ? 0 : buf + 1;
+  };
+  const int steps = b.steps();
+  int buf = 0;
+  if constexpr (kDirect) {
+#pragma unroll
+    for (int q = 0; q < S - 1; ++q)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) b.fetch(q, q, i);
+    for (int step = 0; step < steps; ++step) {
+      wait_loads<(S - 2) * kLoads, false>();   // this step is in LDS
+      __builtin_amdgcn_s_barrier();            // for all waves, and the last step's buffer is free
+      issue_fence();
+      read(buf);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) b.fetch(step + S - 1, buf == 0 ? S - 1 : buf - 1, i);
+      multiply();
+      issue_fence();
+      buf = buf + 1 == S ? 0 : buf + 1;
+    }
+  } else {
+    // two steps on their way in registers, two in LDS
+    v4i rows[2][kLoads];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) rows[q][i] = b.load(q, i);
+    for (int step = 0; step < steps; step += 2) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) B::put(lds, q, i, rows[q][i]);
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) rows[q][i] = b.load(step + 2 + q, i);
+        read(q);
+        multiply();   // of zeros where the row has ended
+      }
+    }
   }
   wait_loads<0, true>();   // no load may land in what is written next
   lds_barrier();
@@ -480,29 +561,34 @@ hipError_t launch_tiled(const MatmulArgs& a, F kernel) {
   return hipGetLastError();
 }
 
-template <int WN, int WT, int MN, int MT, int S>
+template <int WN, int WT, int MN, int MT, int S, bool kDirect = true>
 hipError_t launch_tiles(const MatmulArgs& a, hipStream_t s) {
   return launch_tiled<32 * MN * WN, 32 * MT * WT>(
       a, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
-        matmul_tile_kernel<WN, WT, MN, MT, S, decltype(v)::value, decltype(b)::value>
+        matmul_tile_kernel<WN, WT, MN, MT, S, kDirect, decltype(v)::value, decltype(b)::value>
             <<<grid, 256, 0, s>>>(a, tt, tn, n);
       });
 }
 
-template <int MN, int MT, int S>
+template <int MN, int MT, int S, bool kDirect = true>
 hipError_t launch_split(const MatmulArgs& a, hipStream_t s) {
   return launch_tiled<32 * MN, 32 * MT>(a, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
-    matmul_split_kernel<MN, MT, S, decltype(v)::value, decltype(b)::value>
+    matmul_split_kernel<MN, MT, S, kDirect, decltype(v)::value, decltype(b)::value>
         <<<grid, 256, 0, s>>>(a, tt, tn, n);
   });
 }
 
-// Direct 16-byte loads need every row on a 16-byte boundary; a block's rows of
-// a, w and y must each span less than 2^31 bytes.
+// A block's rows of a, w and y must each span less than 2^31 bytes (there are
+// 256 of them at most), and its blocks must fit a grid.
+bool spans_ok(const MatmulArgs& a) {
+  const int64_t blocks = a.P * ((a.N + 31) / 32) * ((a.T + 31) / 32);
+  return a.a_pitch < (int64_t(1) << 22) && a.N < (int64_t(1) << 20) && blocks < kMaxBlocks * 8;
+}
+
+// Direct 16-byte loads need every row on a 16-byte boundary.
 bool rows_aligned(const MatmulArgs& a) {
   return a.K % 16 == 0 && a.a_pitch % 16 == 0 && a.a_shard % 16 == 0 &&
-         ((uintptr_t)a.a & 15) == 0 && ((uintptr_t)a.w & 15) == 0 &&
-         a.a_pitch < (int64_t(1) << 22) && a.N < (int64_t(1) << 20);
+         ((uintptr_t)a.a & 15) == 0 && ((uintptr_t)a.w & 15) == 0;
 }
 
 // The tile for a product of more than 64 tokens: the one whose blocks, in
@@ -531,9 +617,9 @@ Tile choose_tile(const MatmulArgs& a) {
       cost = (float)((blocks + 255) / 256);
       // With short sums a block mostly waits for its first loads and its
       // stores, which a second block on the CU covers: at P=8 T=2048 N=4096
-      // 256 x 256 and 128 x 128 tiles take 52.8 and 46.9 us for K=256, 61.2
-      // and 63.0 us for K=512.
-      if (a.K <= 256) cost *= 1.4f;
+      // 256 x 256 and 128 x 128 tiles take 55.3 and 51.8 us for K=256, 67.2
+      // and 64.6 us for K=512, 88.8 and 94.2 us for K=1024.
+      cost *= a.K <= 512 ? 1.3f : a.K <= 1024 ? 1.15f : 1.0f;
     }
     if (i == 0 || cost < least) best = (Tile)i, least = cost;
   }
@@ -543,8 +629,8 @@ Tile choose_tile(const MatmulArgs& a) {
 }  // namespace
 
 hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
-  const int64_t n32 = a.P * ((a.N + 31) / 32), t32 = (a.T + 31) / 32;
-  if (rows_aligned(a) && n32 * t32 <= kMaxBlocks * 8) {
+  if (spans_ok(a) && rows_aligned(a)) {
+    const int64_t n32 = a.P * ((a.N + 31) / 32);
     const int64_t n128 = a.P * ((a.N + 127) / 128), n64 = a.P * ((a.N + 63) / 64);
     // Few tokens: the weights are read once, and the tile only has to keep
     // every CU loading. 128 channels a block share the activations best; with
@@ -572,6 +658,15 @@ hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
       case k32x64: return launch_split<1, 2, 6>(a, s);
       default: return launch_split<1, 1, 6>(a, s);
     }
+  }
+  // Rows on any byte: 128 x 128 tiles, or 32 x 32 where those leave half of the
+  // CUs idle or most of a tile's tokens are missing (K=4095 N=4096: T=512 46.5
+  // against 53.3 us, T=256 45.5 against 30.4; N=8192 P=8: T=64 K=4094 95.9
+  // against 129.9, T=16 K=1023 25.0 against 19.3).
+  if (spans_ok(a) && a.K >= 16) {
+    const int64_t b128 = a.P * ((a.N + 127) / 128) * ((a.T + 127) / 128);
+    return a.T > 32 && b128 >= 128 ? launch_tiles<2, 2, 2, 2, 2, false>(a, s)
+                                   : launch_split<1, 1, 3, false>(a, s);
   }
   const int64_t tt = (a.T + kGenTile - 1) / kGenTile, tn = (a.N + kGenTile - 1) / kGenTile;
   const int64_t tiles = a.P * tt * tn;

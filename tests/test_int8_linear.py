@@ -238,6 +238,39 @@ def test_int8_matmul(P, T, N, K):
     assert_product(y, np.repeat(a[:1], P, 0), np.repeat(sa[:1], P, 0), w, sw, b, "shared rows")
 
 
+LARGE = [  # P, T, N, K: what takes each tile size, whole and ragged, aligned and not
+    (8, 2048, 2048, 1040), (4, 2000, 4088, 2064), (3, 1500, 3001, 1168), (1, 4096, 4096, 1152),
+    (2, 2048, 4096, 300), (8, 1024, 2048, 512), (1, 1000, 4104, 1296), (8, 250, 1016, 2048),
+    (1, 512, 4096, 2048), (1, 300, 4100, 784), (8, 100, 1024, 1024), (1, 256, 4096, 4096),
+    (1, 90, 4096, 1024), (8, 60, 8192, 528), (8, 33, 8190, 400), (8, 30, 8192, 2176),
+    (8, 7, 8200, 656), (4, 50, 4096, 1024), (1, 1024, 4095, 2047), (3, 2047, 1023, 513),
+    (8, 64, 2047, 1001), (2, 500, 900, 18)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P,T,N,K", LARGE)
+def test_int8_matmul_large(P, T, N, K):
+    # the sums in float64 on the GPU: exact below 2^53, whatever their order
+    say(f"case: int8_matmul P={P} T={T} N={N} K={K}")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(K)
+    a = torch.randint(-128, 128, (P, T, K), device=DEV, generator=g, dtype=torch.int8)
+    w = torch.randint(-128, 128, (P, N, K), device=DEV, generator=g, dtype=torch.int8)
+    sa, sw = torch.rand((P, T), device=DEV, generator=g), torch.rand((P, N), device=DEV,
+                                                                     generator=g)
+    bias = torch.randn((P, N), device=DEV, generator=g)
+    for b in (None, bias):
+        for bf16 in (True, False):
+            y = B.btq_int8_matmul(a, sa, w, sw, bias=b, bf16=bf16)
+            for p in range(P):
+                acc = a[p].double() @ w[p].double().t().contiguous()
+                want = acc.float() * sa[p][:, None] * sw[p][None, :]
+                if b is not None:
+                    want = want + b[p][None, :]
+                got = y[p].view(torch.bfloat16) if bf16 else y[p]
+                assert torch.equal(got, want.to(got.dtype)), (p, bf16, b is not None)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 16, 40, 300])
 def test_int8_matmul_largest_sums(T):
