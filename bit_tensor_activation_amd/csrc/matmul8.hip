@@ -203,9 +203,19 @@ constexpr int kStep = 128;
 // buffers apart, would wait for these loads before every later LDS read; the
 // kernel orders them itself, with wait_loads and a barrier before the first
 // read. (m0 is reserved and nothing else in these kernels uses it.)
-template <int kBytes>
+// kNt: with the streaming hint.
+template <int kBytes, bool kNt = false>
 __device__ __forceinline__ void load_to_lds(rsrc_t r, uint32_t to, uint32_t off, uint32_t soff) {
-  if constexpr (kBytes == 16)
+  static_assert(kBytes == 16 || (kBytes == 4 && !kNt));
+  if constexpr (kNt)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, %3 offen nt lds"
+        :
+        : "s"(to), "v"(off), "s"(r), "s"(soff)
+        : "memory");
+  else if constexpr (kBytes == 16)
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
         "s_nop 0\n\t"
@@ -234,7 +244,8 @@ __device__ __forceinline__ void wait_loads() {
 }
 // A block's share of the product: RN channels x RT tokens of shard p, and the
 // loads of its operands, 256 threads together, into S buffers of LDS.
-template <int RN, int RT, int S>
+// kNt: the channels' loads stream past the caches.
+template <int RN, int RT, int S, bool kNt>
 struct Block {
   static constexpr int kLoads = (RN + RT) / 32, kStage = (RN + RT) * kStep;
   struct Lds {
@@ -299,8 +310,11 @@ struct Block {
   // the address is out of range: nothing is read.
   __device__ __forceinline__ void fetch(int step, int buf, int i) const {
     const bool in_row = step * kStep + chunk < K;
-    load_to_lds<16>(i < RN / 32 ? rw : ra, to + buf * kStage + i * 32 * kStep,
-                    in_row ? off[i] : kOOB, step * kStep);
+    const uint32_t at = to + buf * kStage + i * 32 * kStep, from = in_row ? off[i] : kOOB;
+    if (i < RN / 32)
+      load_to_lds<16, kNt>(rw, at, from, step * kStep);
+    else
+      load_to_lds<16>(ra, at, from, step * kStep);
   }
   // The same load to registers, for rows on any byte: 16 bytes that end inside
   // the row, shifted down to where they belong.
@@ -332,14 +346,17 @@ struct Block {
 };
 
 //
-// kDirect: K and every row on 16 bytes. Otherwise (S = 2) the next step's
-// operands wait in registers while this one is multiplied.
-template <int WN, int WT, int MN, int MT, int S, bool kDirect, bool kVec, bool kBf>
+// kLoad: kDirect or kDirectNt where K and every row lie on 16 bytes. kAnyByte
+// (S = 2): the next step's operands wait in registers while this one is
+// multiplied.
+enum Load { kDirect, kDirectNt, kAnyByte };
+
+template <int WN, int WT, int MN, int MT, int S, Load kLoad, bool kVec, bool kBf>
 __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
     MatmulArgs g, int tiles_t, int tiles_n, int tiles) {
-  static_assert(WN * WT == 4 && (kDirect || S == 2), "4 waves");
+  static_assert(WN * WT == 4 && (kLoad != kAnyByte || S == 2));
   constexpr int RN = 32 * MN * WN, RT = 32 * MT * WT;
-  using B = Block<RN, RT, S>;
+  using B = Block<RN, RT, S, kLoad == kDirectNt>;
   constexpr int kLoads = B::kLoads;
   __shared__ typename B::Lds lds;
   const B b(g, tiles_t, tiles_n, tiles, lds);
@@ -366,13 +383,13 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
         if (min(r * kM / kR / 2, kM - 1) == m) read(rbuf, rslice, r);
 #pragma unroll
       for (int d = 0; d < kLoads; ++d)
-        if (kDirect && d >= d0 && d < d1 && (d - d0) * kM / (d1 - d0) == m) b.fetch(ds, dbuf, d);
+        if (kLoad != kAnyByte && d >= d0 && d < d1 && (d - d0) * kM / (d1 - d0) == m) b.fetch(ds, dbuf, d);
       issue_fence();
     }
   };
   const int steps = b.steps();
   int buf = 0;
-  if constexpr (kDirect) {
+  if constexpr (kLoad != kAnyByte) {
     // half of a step's loads go out right after the barrier that frees their
     // buffer, the other half a slice later: together they would hold up the
     // products that follow
@@ -446,11 +463,11 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
 // that few channels still make many blocks; its four waves share the loads as
 // above and each multiplies one of a step's four slices. Their int32 sums are
 // added through LDS at the end, exact in any order.
-template <int MN, int MT, int S, bool kDirect, bool kVec, bool kBf>
+template <int MN, int MT, int S, Load kLoad, bool kVec, bool kBf>
 __global__ __launch_bounds__(256, 2) void matmul_split_kernel(MatmulArgs g, int tiles_t,
                                                               int tiles_n, int tiles) {
   constexpr int RN = 32 * MN, RT = 32 * MT;
-  using B = Block<RN, RT, S>;
+  using B = Block<RN, RT, S, kLoad == kDirectNt>;
   constexpr int kLoads = B::kLoads;
   __shared__ typename B::Lds lds;
   const B b(g, tiles_t, tiles_n, tiles, lds);
@@ -471,7 +488,7 @@ __global__ __launch_bounds__(256, 2) void matmul_split_kernel(MatmulArgs g, int 
   };
   const int steps = b.steps();
   int buf = 0;
-  if constexpr (kDirect) {
+  if constexpr (kLoad != kAnyByte) {
 #pragma unroll
     for (int q = 0; q < S - 1; ++q)
 #pragma unroll
@@ -561,19 +578,19 @@ hipError_t launch_tiled(const MatmulArgs& a, F kernel) {
   return hipGetLastError();
 }
 
-template <int WN, int WT, int MN, int MT, int S, bool kDirect = true>
+template <int WN, int WT, int MN, int MT, int S, Load kLoad = kDirect>
 hipError_t launch_tiles(const MatmulArgs& a, hipStream_t s) {
   return launch_tiled<32 * MN * WN, 32 * MT * WT>(
       a, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
-        matmul_tile_kernel<WN, WT, MN, MT, S, kDirect, decltype(v)::value, decltype(b)::value>
+        matmul_tile_kernel<WN, WT, MN, MT, S, kLoad, decltype(v)::value, decltype(b)::value>
             <<<grid, 256, 0, s>>>(a, tt, tn, n);
       });
 }
 
-template <int MN, int MT, int S, bool kDirect = true>
+template <int MN, int MT, int S, Load kLoad = kDirect>
 hipError_t launch_split(const MatmulArgs& a, hipStream_t s) {
   return launch_tiled<32 * MN, 32 * MT>(a, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
-    matmul_split_kernel<MN, MT, S, kDirect, decltype(v)::value, decltype(b)::value>
+    matmul_split_kernel<MN, MT, S, kLoad, decltype(v)::value, decltype(b)::value>
         <<<grid, 256, 0, s>>>(a, tt, tn, n);
   });
 }
@@ -634,17 +651,29 @@ hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
     const int64_t n128 = a.P * ((a.N + 127) / 128), n64 = a.P * ((a.N + 63) / 64);
     // Few tokens: the weights are read once, and the tile only has to keep
     // every CU loading. 128 channels a block share the activations best; with
-    // fewer than two such blocks a CU, smaller ones fill the chip (T=64 N=1024
-    // P=8 K=8192: 16.2 us with 32 channels, 28.2 with 128). For up to 32 tokens
+    // fewer than one such block a CU, smaller ones fill the chip (T=64 P=8 K=8192
+    // N=1024: 15.7 us with 32 channels, 27.9 with 128; P=4 N=8192 K=4096: 29.0
+    // and 24.4; P=2 N=8192 K=8192: 29.1 with 32, 25.9 with 64, 33.8 with 128). For up to 32 tokens
     // and long k, 64 channels by split waves read more steadily than 128 (T=16
     // N=8192 P=8 K=4096: 54.7 against 63.2 us; K=1024: 15.1 against 13.5).
+    // Weights as large as the 256 MB last-level cache cannot be there from an
+    // earlier call and are not kept for a later one: loaded with the streaming
+    // hint (N=8192 P=8 K=4096: T=64 63.8 -> 58.0 us, T=16 55.2 -> 48.9). Half
+    // of that lost by it (N=8192 P=4 K=4096, found there again: 24.4 -> 33.5).
+    const bool nt = a.P * a.N * a.K >= (int64_t(1) << 28);
     if (a.T <= 32) {
-      if (n128 >= 512 && a.K <= 2048) return launch_tiles<4, 1, 1, 1, 3>(a, s);
-      if (n64 >= 512) return launch_split<2, 1, 6>(a, s);
+      if (n128 >= 512 && a.K <= 2048)
+        return nt ? launch_tiles<4, 1, 1, 1, 3, kDirectNt>(a, s)
+                  : launch_tiles<4, 1, 1, 1, 3>(a, s);
+      if (n64 >= 512)
+        return nt ? launch_split<2, 1, 6, kDirectNt>(a, s) : launch_split<2, 1, 6>(a, s);
       return launch_split<1, 1, 6>(a, s);
     }
     if (a.T <= 64) {
-      if (n128 >= 512) return launch_tiles<4, 1, 1, 2, 3>(a, s);
+      if (n128 >= 256)
+        return nt ? launch_tiles<4, 1, 1, 2, 3, kDirectNt>(a, s)
+                  : launch_tiles<4, 1, 1, 2, 3>(a, s);
+      if (n64 >= 256) return launch_split<2, 2, 6>(a, s);
       if (n32 >= 256) return launch_split<1, 2, 6>(a, s);
       return launch_split<1, 1, 6>(a, s);
     }
@@ -665,8 +694,8 @@ hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
   // against 129.9, T=16 K=1023 25.0 against 19.3).
   if (spans_ok(a) && a.K >= 16) {
     const int64_t b128 = a.P * ((a.N + 127) / 128) * ((a.T + 127) / 128);
-    return a.T > 32 && b128 >= 128 ? launch_tiles<2, 2, 2, 2, 2, false>(a, s)
-                                   : launch_split<1, 1, 3, false>(a, s);
+    return a.T > 32 && b128 >= 128 ? launch_tiles<2, 2, 2, 2, 2, kAnyByte>(a, s)
+                                   : launch_split<1, 1, 3, kAnyByte>(a, s);
   }
   const int64_t tt = (a.T + kGenTile - 1) / kGenTile, tn = (a.N + kGenTile - 1) / kGenTile;
   const int64_t tiles = a.P * tt * tn;
