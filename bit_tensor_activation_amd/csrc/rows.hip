@@ -137,88 +137,104 @@ __global__ __launch_bounds__(kGenThreads) void rows_general_kernel(
 // read once and written once; each statistic is a sum over registers, a
 // shuffle and (G > 64) one LDS exchange. A layer norm takes its variance from
 // the deviations in a second sum, so a large mean costs no precision.
-// kVec: element runs of 8 a lane, read and written as 16-byte vectors. Else
-// lanes take neighbouring elements, one at a time (odd H, odd addresses).
-// Every row access goes through a buffer descriptor over the row: what lies
-// past H loads as 0 and is not stored.
+// A lane takes runs of 8 elements. Every access goes through a buffer
+// descriptor over the row, which is checked dword by dword: what lies past the
+// row loads as 0 and is not stored. That needs rows on 4 bytes (kAligned), not
+// on the 16 of the vectors. Else (bf16 rows of odd H, codes of H not a multiple
+// of 4) bf16 loads read the dwords the row lies in, shift by its odd half and
+// clear what belongs to the next row (never past the dword of the row's last
+// element), and stores go by address, at any byte.
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-template <int G, int NV, bool kVec>
+// A row of `n` elements of `size` bytes.
+template <bool kAligned>
+struct Row {
+  char* p;
+  uint32_t skip;   // bytes of the first dword before the row
+  rsrc_t r;
+  __device__ __forceinline__ Row(const void* base, int64_t first, int n, int size) {
+    p = (char*)base + first * size;
+    skip = kAligned ? 0 : (uint32_t)(uintptr_t)p & 3;
+    r = make_rsrc(p - skip, kAligned ? (uint32_t)(n * size) : (skip + n * size + 3) & ~3u);
+  }
+};
+
+template <int G, int NV, bool kAligned>
 struct RowMap {
+  using R = Row<kAligned>;
   static constexpr int E = 8 * NV;
   int i;   // lane of the row's group
-  __device__ __forceinline__ int at(int v, int j) const {
-    return kVec ? (v * G + i) * 8 + j : (v * 8 + j) * G + i;
-  }
-  // raw words of 8 elements: 8 for fp32, 4 (or 8 halves, one a word) for bf16
+  int H;
+  __device__ __forceinline__ int at(int v, int j) const { return (v * G + i) * 8 + j; }
+  // raw words of 8 elements: 8 for fp32 (always on 4 bytes), 4 for bf16
   template <int kType>
-  __device__ __forceinline__ void load(rsrc_t r, int v, uint32_t (&w)[8]) const {
-    if constexpr (!kVec) {
+  __device__ __forceinline__ void load(const R& r, int v, uint32_t (&w)[8]) const {
+    constexpr int kWords = kType == kF32 ? 8 : 4;
+    const int h = at(v, 0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w[j] = kType == kF32
-                   ? __builtin_amdgcn_raw_buffer_load_b32(r, (uint32_t)at(v, j) * 4u, 0, 0)
-                   : (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                         r, (uint32_t)at(v, j) * 2u, 0, 0);
-    } else if constexpr (kType == kF32) {
-      const v4u a = __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)at(v, 0) * 4u, 0, 0);
-      const v4u b = __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)at(v, 0) * 4u + 16u, 0, 0);
+    for (int q = 0; q < kWords / 4; ++q) {
+      const v4u a =
+          __builtin_amdgcn_raw_buffer_load_b128(r.r, (uint32_t)(h * kWords / 2 + 16 * q), 0, 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = a[j], w[4 + j] = b[j];
-    } else {
-      const v4u a = __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)at(v, 0) * 2u, 0, 0);
+      for (int j = 0; j < 4; ++j) w[4 * q + j] = a[j];
+    }
+    if constexpr (!kAligned && kType == kBf16) {
+      w[4] = __builtin_amdgcn_raw_buffer_load_b32(r.r, (uint32_t)(h * 2 + 16), 0, 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = a[j];
+      for (int j = 0; j < 4; ++j) {
+        w[j] = __builtin_amdgcn_alignbyte(w[j + 1], w[j], r.skip);
+        if (h + 2 * j + 1 >= H) w[j] &= h + 2 * j >= H ? 0u : 0xffffu;
+      }
     }
   }
   template <int kType>
   static __device__ __forceinline__ float value(const uint32_t (&w)[8], int j) {
     if constexpr (kType == kF32) return __uint_as_float(w[j]);
-    if constexpr (!kVec) return bf16_to_f32(w[j]);
     return j & 1 ? __uint_as_float(w[j / 2] & 0xffff0000u) : __uint_as_float(w[j / 2] << 16);
   }
-  template <int kType>
-  __device__ __forceinline__ void store(rsrc_t r, int v, const float (&f)[8]) const {
-    if constexpr (!kVec) {
+  // 8 elements of kSize bytes, packed in w
+  template <int kSize>
+  __device__ __forceinline__ void put(const R& r, int v, const uint32_t* w) const {
+    const int h = at(v, 0);
+    if constexpr (kAligned || kSize == 4) {
+      const uint32_t off = (uint32_t)(h * kSize);
+      if constexpr (kSize == 1) {
+        __builtin_amdgcn_raw_buffer_store_b64(v2u{w[0], w[1]}, r.r, off, 0, 0);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (kType == kF32)
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[j]), r, (uint32_t)at(v, j) * 4u,
-                                                0, 0);
-        else
-          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)f32_to_bf16(f[j]), r,
-                                                (uint32_t)at(v, j) * 2u, 0, 0);
+        for (int q = 0; q < kSize / 2; ++q)
+          __builtin_amdgcn_raw_buffer_store_b128(
+              v4u{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]}, r.r, off + 16u * q, 0, 0);
       }
-    } else if constexpr (kType == kF32) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        __builtin_amdgcn_raw_buffer_store_b128(
-            v4u{__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]),
-                __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3])},
-            r, (uint32_t)at(v, 0) * 4u + 16u * h, 0, 0);
+    } else if (h + 8 <= H) {
+      __builtin_memcpy(r.p + (int64_t)h * kSize, w, 8 * kSize);
     } else {
-      __builtin_amdgcn_raw_buffer_store_b128(
-          v4u{f32_to_bf16x2(f[0], f[1]), f32_to_bf16x2(f[2], f[3]), f32_to_bf16x2(f[4], f[5]),
-              f32_to_bf16x2(f[6], f[7])},
-          r, (uint32_t)at(v, 0) * 2u, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (h + j < H) {
+          if constexpr (kSize == 2)
+            ((uint16_t*)r.p)[h + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+          if constexpr (kSize == 1) r.p[h + j] = (char)(w[j / 4] >> (8 * (j & 3)));
+        }
     }
   }
-  __device__ __forceinline__ void store_codes(rsrc_t r, int v, const float (&f)[8],
+  template <int kType>
+  __device__ __forceinline__ void store(const R& r, int v, const float (&f)[8]) const {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < (kType == kF32 ? 8 : 4); ++j)
+      w[j] = kType == kF32 ? __float_as_uint(f[j]) : f32_to_bf16x2(f[2 * j & 7], f[2 * j + 1 & 7]);
+    put<kType == kF32 ? 4 : 2>(r, v, w);
+  }
+  __device__ __forceinline__ void store_codes(const R& r, int v, const float (&f)[8],
                                               float mul) const {
     uint32_t c[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) c[j] = code_bits(f[j], mul);
-    if constexpr (kVec) {
-      __builtin_amdgcn_raw_buffer_store_b64(
-          v2u{c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
-              c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24},
-          r, (uint32_t)at(v, 0), 0, 0);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)c[j], r, (uint32_t)at(v, j), 0, 0);
-    }
+    const uint32_t w[2] = {c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
+                           c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
+    put<1>(r, v, w);
   }
 };
 
@@ -249,8 +265,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x, uint32_t* slot) {
 }
 
 // Statistics of the row in v: its mean (layer) and 1/sqrt(var + eps).
-template <int G, int NV, bool kVec>
-__device__ __forceinline__ void row_stats(const RowMap<G, NV, kVec>& m, const float (&v)[8 * NV],
+template <int G, int NV, bool kAligned>
+__device__ __forceinline__ void row_stats(const RowMap<G, NV, kAligned>& m, const float (&v)[8 * NV],
                                           int H, bool layer, float eps, uint32_t* slot,
                                           float* mean, float* rstd) {
   const float inv_h = 1.0f / (float)H;
@@ -274,13 +290,13 @@ __device__ __forceinline__ void row_stats(const RowMap<G, NV, kVec>& m, const fl
 }
 
 // f = norm of 8 elements of the row.
-template <int G, int NV, bool kVec>
-__device__ __forceinline__ void row_norm(const RowMap<G, NV, kVec>& m, int v, float (&f)[8],
+template <int G, int NV, bool kAligned>
+__device__ __forceinline__ void row_norm(const RowMap<G, NV, kAligned>& m, int v, float (&f)[8],
                                          float mean, float rstd, const float* weight,
-                                         const float* bias, uint32_t bytes) {
+                                         const float* bias) {
   uint32_t w[8];
   if (weight) {
-    m.template load<kF32>(make_rsrc(weight, bytes), v, w);
+    m.template load<kF32>(Row<kAligned>(weight, 0, m.H, 4), v, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd * __uint_as_float(w[j]);
   } else {
@@ -288,23 +304,22 @@ __device__ __forceinline__ void row_norm(const RowMap<G, NV, kVec>& m, int v, fl
     for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean) * rstd;
   }
   if (bias) {
-    m.template load<kF32>(make_rsrc(bias, bytes), v, w);
+    m.template load<kF32>(Row<kAligned>(bias, 0, m.H, 4), v, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] += __uint_as_float(w[j]);
   }
 }
 
-template <int G, int NV, bool kVec, int kY, int kR>
+template <int G, int NV, bool kAligned, int kY, int kR>
 __global__ __launch_bounds__(G == 64 ? 256 : G) void norm_row_kernel(NormArgs a) {
   constexpr int E = 8 * NV;
   constexpr int kRows = G == 64 ? 4 : 1;   // rows of a block
   // 5 exchanges a row, in two sets: a wave may enter the next row's while
   // another still reads this one's, but never the one after that
   __shared__ uint32_t lds[2][5 * 16];
-  RowMap<G, NV, kVec> m;
+  RowMap<G, NV, kAligned> m;
   m.i = threadIdx.x % G;
-  const int H = (int)a.H;
-  const uint32_t h32 = (uint32_t)H * 4u;
+  const int H = m.H = (int)a.H;
   int set = 0;
   const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / G);
   for (int64_t t = (int64_t)blockIdx.x * kRows + sub; t < a.T;
@@ -312,11 +327,11 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void norm_row_kernel(NormArgs a)
     uint32_t* slot = lds[set];
     const int64_t row = t * H;
     constexpr int ysz = kY == kF32 ? 4 : 2, rsz = kR == kF32 ? 4 : 2;
-    const rsrc_t rr = make_rsrc((const char*)a.residual + row * rsz, (uint32_t)H * rsz);
+    const Row<kAligned> rr(a.residual, row, H, rsz);
     float u[E];
     uint32_t res[NV][8];
     if (a.y) {
-      const rsrc_t ry = make_rsrc((const char*)a.y + row * ysz, (uint32_t)H * ysz);
+      const Row<kAligned> ry(a.y, row, H, ysz);
       uint32_t yw[NV][8];
 #pragma unroll
       for (int v = 0; v < NV; ++v) m.template load<kY>(ry, v, yw[v]);
@@ -327,15 +342,13 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void norm_row_kernel(NormArgs a)
       float mean = 0.0f, rstd = 1.0f;
       if (a.post != kNone)
         row_stats(m, u, H, a.post == kLayer, a.post_eps, slot, &mean, &rstd);
-      const rsrc_t rg = make_rsrc(
-          (const char*)a.gate + t / a.gate_each * H * (a.gate_type == kF32 ? 4 : 2),
-          (uint32_t)H * (a.gate_type == kF32 ? 4u : 2u));
+      const Row<kAligned> rg(a.gate, t / a.gate_each * H, H, a.gate_type == kF32 ? 4 : 2);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = u[v * 8 + j];
-        if (a.post != kNone) row_norm(m, v, f, mean, rstd, a.post_weight, a.post_bias, h32);
+        if (a.post != kNone) row_norm(m, v, f, mean, rstd, a.post_weight, a.post_bias);
         if (a.gate) {
           uint32_t w[8];
           if (a.gate_type == kF32) {
@@ -359,7 +372,7 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void norm_row_kernel(NormArgs a)
       for (int e = 0; e < E; ++e) u[e] = m.template value<kR>(res[e / 8], e % 8);
     }
     if (a.residual_out) {
-      const rsrc_t ro = make_rsrc((char*)a.residual_out + row * rsz, (uint32_t)H * rsz);
+      const Row<kAligned> ro(a.residual_out, row, H, rsz);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float f[8];
@@ -377,13 +390,12 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void norm_row_kernel(NormArgs a)
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = u[v * 8 + j];
-        row_norm(m, v, f, mean, rstd, a.pre_weight, a.pre_bias, h32);
+        row_norm(m, v, f, mean, rstd, a.pre_weight, a.pre_bias);
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[v * 8 + j] = f[j];
       }
     }
-    const int nsz = a.n_type == kF32 ? 4 : a.n_type == kBf16 ? 2 : 1;
-    const rsrc_t rn = make_rsrc((char*)a.n + row * nsz, (uint32_t)(H * nsz));
+    const Row<kAligned> rn(a.n, row, H, a.n_type == kF32 ? 4 : a.n_type == kBf16 ? 2 : 1);
     RowScale rs = {1.0f, 0.0f};
     if (a.n_type == kInt8) {
       uint32_t big = 0;
@@ -409,20 +421,21 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void norm_row_kernel(NormArgs a)
 }
 
 // 8-bit codes of a row: the largest |x| from the bits, then the codes.
-template <int G, int NV, bool kVec, int kX>
+template <int G, int NV, bool kAligned, int kX>
 __global__ __launch_bounds__(G == 64 ? 256 : G) void rows_code_kernel(
     const void* __restrict__ x, int64_t x_shard, int64_t x_pitch, uint32_t rows, uint32_t T, int K,
     int8_t* __restrict__ q, int64_t q_pitch, float* __restrict__ scale) {
   constexpr uint32_t kRows = G == 64 ? 4 : 1;
   constexpr int sz = kX == kF32 ? 4 : 2;
   __shared__ uint32_t lds[2][16];   // two rows' exchanges, as in norm_row_kernel
-  RowMap<G, NV, kVec> m;
+  RowMap<G, NV, kAligned> m;
   m.i = threadIdx.x % G;
+  m.H = K;
   int set = 0;
   const uint32_t sub = (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x / G);
   for (uint32_t row = blockIdx.x * kRows + sub; row < rows; row += gridDim.x * kRows, set ^= 1) {
     const int64_t base = (int64_t)(row / T) * x_shard + (int64_t)(row % T) * x_pitch;
-    const rsrc_t rx = make_rsrc((const char*)x + base * sz, (uint32_t)K * sz);
+    const Row<kAligned> rx(x, base, K, sz);
     uint32_t w[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) m.template load<kX>(rx, v, w[v]);
@@ -434,7 +447,7 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void rows_code_kernel(
         big = max(big, __float_as_uint(m.template value<kX>(w[v], j)) & 0x7fffffffu);
     const RowScale rs = row_scale(row_max<G>(big, lds[set]));
     if (m.i == 0) scale[row] = rs.scale;
-    const rsrc_t rq = make_rsrc(q + row * q_pitch, (uint32_t)K);
+    const Row<kAligned> rq(q, row * q_pitch, K, 1);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float f[8];
@@ -446,9 +459,8 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void rows_code_kernel(
 }
 
 constexpr int64_t kMaxBlocks = int64_t(1) << 20;
-// The longest rows that stay in registers: 16 elements a lane of 1024, and
-// for a norm read by vectors 32 (element by element that spills).
-constexpr int64_t kMaxRow = 16384, kMaxVecRow = 32768;
+// The longest rows that stay in registers: 32 elements a lane of 1024.
+constexpr int64_t kMaxRow = 32768;
 
 struct CodeArgs {
   const void* x;
@@ -458,76 +470,79 @@ struct CodeArgs {
   float* scale;
 };
 
-template <int G, int NV, bool kVec, int kX>
+template <int G, int NV, bool kAligned, int kX>
 hipError_t launch_codes(const CodeArgs& c, hipStream_t s) {
   constexpr int per = G == 64 ? 4 : 1;
   const int64_t rows = c.P * c.T, blocks = (rows + per - 1) / per;
-  rows_code_kernel<G, NV, kVec, kX>
+  rows_code_kernel<G, NV, kAligned, kX>
       <<<dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), G == 64 ? 256 : G, 0, s>>>(
           c.x, c.x_shard, c.x_pitch, (uint32_t)rows, (uint32_t)c.T, (int)c.K, c.q, c.q_pitch,
           c.scale);
   return hipGetLastError();
 }
 
-template <bool kVec, int kX>
+template <bool kAligned, int kX>
 hipError_t launch_codes_sized(const CodeArgs& c, hipStream_t s) {
-  const bool few = c.P * c.T <= 512;
-  if (!few && c.K <= 512) return launch_codes<64, 1, kVec, kX>(c, s);
-  if (!few && c.K <= 1024) return launch_codes<64, 2, kVec, kX>(c, s);
-  if (c.K <= 2048) return launch_codes<256, 1, kVec, kX>(c, s);
-  if (!few && c.K <= 4096) return launch_codes<256, 2, kVec, kX>(c, s);
-  if (!few && c.K <= 8192) return launch_codes<256, 4, kVec, kX>(c, s);
-  if (c.K <= 8192) return launch_codes<1024, 1, kVec, kX>(c, s);
-  return launch_codes<1024, 2, kVec, kX>(c, s);
+  if (c.K <= 512) return launch_codes<64, 1, kAligned, kX>(c, s);
+  if (c.K <= 1024) return launch_codes<64, 2, kAligned, kX>(c, s);
+  if (c.K <= 2048) return launch_codes<256, 1, kAligned, kX>(c, s);
+  if (c.K <= 4096) return launch_codes<256, 2, kAligned, kX>(c, s);
+  if (c.K <= 8192) return launch_codes<256, 4, kAligned, kX>(c, s);
+  if (c.K <= 16384) return launch_codes<1024, 2, kAligned, kX>(c, s);
+  return launch_codes<1024, 4, kAligned, kX>(c, s);
 }
 
-template <int G, int NV, bool kVec, int kY, int kR>
+template <int G, int NV, bool kAligned, int kY, int kR>
 hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
   constexpr int rows = G == 64 ? 4 : 1;
   const int64_t blocks = (a.T + rows - 1) / rows;
-  norm_row_kernel<G, NV, kVec, kY, kR>
+  norm_row_kernel<G, NV, kAligned, kY, kR>
       <<<dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), G == 64 ? 256 : G, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <int G, int NV, bool kVec>
+template <int G, int NV, bool kAligned>
 hipError_t launch_types(const NormArgs& a, hipStream_t s) {
   if (a.y_type == kF32)
-    return a.r_type == kF32 ? launch_rows<G, NV, kVec, kF32, kF32>(a, s)
-                            : launch_rows<G, NV, kVec, kF32, kBf16>(a, s);
-  return a.r_type == kF32 ? launch_rows<G, NV, kVec, kBf16, kF32>(a, s)
-                          : launch_rows<G, NV, kVec, kBf16, kBf16>(a, s);
+    return a.r_type == kF32 ? launch_rows<G, NV, kAligned, kF32, kF32>(a, s)
+                            : launch_rows<G, NV, kAligned, kF32, kBf16>(a, s);
+  return a.r_type == kF32 ? launch_rows<G, NV, kAligned, kBf16, kF32>(a, s)
+                          : launch_rows<G, NV, kAligned, kBf16, kBf16>(a, s);
 }
 
-template <bool kVec>
+template <bool kAligned>
 hipError_t launch_sized(const NormArgs& a, hipStream_t s) {
   const int64_t H = a.H;
-  // Few rows leave most of the chip idle, so a row takes more lanes.
-  const bool few = a.T <= 512;
-  if (!few && H <= 512) return launch_types<64, 1, kVec>(a, s);
-  if (!few && H <= 1024) return launch_types<64, 2, kVec>(a, s);
-  if (H <= 2048) return launch_types<256, 1, kVec>(a, s);
-  if (!few && H <= 4096) return launch_types<256, 2, kVec>(a, s);
-  if (!few && H <= 8192) return launch_types<256, 4, kVec>(a, s);
-  if (H <= 8192) return launch_types<1024, 1, kVec>(a, s);
-  if constexpr (kVec) {
-    if (H > kMaxRow) return launch_types<1024, 4, kVec>(a, s);
+  if (H <= 512) return launch_types<64, 1, kAligned>(a, s);
+  if (H <= 1024) return launch_types<64, 2, kAligned>(a, s);
+  if (H <= 2048) return launch_types<256, 1, kAligned>(a, s);
+  if (H <= 4096) return launch_types<256, 2, kAligned>(a, s);
+  // few rows leave most of the chip idle, so a row takes more lanes (H=8192:
+  // T=64 5.1 against 6.3 us, T=256 7.4 against 8.7, T=1024 24.2 against 17.8)
+  if (H <= 8192 && a.T > 256) return launch_types<256, 4, kAligned>(a, s);
+  if (H <= 8192) return launch_types<1024, 1, kAligned>(a, s);
+  if constexpr (kAligned) {
+    if (H > 16384) return launch_types<1024, 4, kAligned>(a, s);
   }
-  return launch_types<1024, 2, kVec>(a, s);
+  return launch_types<1024, 2, kAligned>(a, s);
 }
 
-bool vec_ok(const void* p) { return ((uintptr_t)p & 15) == 0; }
+// Rows of `pitch` elements start on 4 bytes.
+bool on4(const void* p, int64_t pitch, int type) {
+  const int64_t size = type == kF32 ? 4 : type == kBf16 ? 2 : 1;
+  return ((uintptr_t)p & 3) == 0 && pitch * size % 4 == 0;
+}
 
 }  // namespace
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
-  if (a.H <= kMaxVecRow) {
-    const bool vec = a.H % 8 == 0 && vec_ok(a.y) && vec_ok(a.residual) && vec_ok(a.gate) &&
-                     vec_ok(a.post_weight) && vec_ok(a.post_bias) && vec_ok(a.pre_weight) &&
-                     vec_ok(a.pre_bias) && vec_ok(a.residual_out) &&
-                     ((uintptr_t)a.n & (a.n_type == kInt8 ? 7 : 15)) == 0;
-    if (vec) return launch_sized<true>(a, s);
-    if (a.H <= kMaxRow) return launch_sized<false>(a, s);
+  if (a.H <= kMaxRow) {
+    // (fp32 tensors are on 4 bytes)
+    const bool aligned = on4(a.y, a.H, a.y_type) && on4(a.residual, a.H, a.r_type) &&
+                         on4(a.gate, a.gate ? a.H : 0, a.gate_type) &&
+                         on4(a.residual_out, a.H, a.r_type) && on4(a.n, a.n ? a.H : 0, a.n_type);
+    if (aligned) return launch_sized<true>(a, s);
+    if (a.H <= kMaxRow / 2) return launch_sized<false>(a, s);
   }
   norm_general_kernel<<<dim3((unsigned)(a.T < kMaxBlocks ? a.T : kMaxBlocks)), kGenThreads, 0,
                         s>>>(a);
@@ -540,9 +555,8 @@ hipError_t launch_quantize_rows(const void* x, int x_type, int64_t x_shard, int6
   const int64_t rows = P * T;
   if (K <= kMaxRow && rows < (int64_t(1) << 31)) {
     const CodeArgs c = {x, x_shard, x_pitch, P, T, K, q, q_pitch, scale};
-    const int64_t unit = x_type == kF32 ? 4 : 8;   // elements in 16 bytes
-    if (K % 8 == 0 && x_shard % unit == 0 && x_pitch % unit == 0 && vec_ok(x) &&
-        q_pitch % 8 == 0 && ((uintptr_t)q & 7) == 0)
+    if (on4(x, x_shard, x_type) && on4(x, x_pitch, x_type) && (x_type == kF32 || K % 2 == 0) &&
+        on4(q, q_pitch, kInt8) && K % 4 == 0)
       return x_type == kF32 ? launch_codes_sized<true, kF32>(c, s)
                             : launch_codes_sized<true, kBf16>(c, s);
     return x_type == kF32 ? launch_codes_sized<false, kF32>(c, s)
