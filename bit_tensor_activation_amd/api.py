@@ -366,27 +366,39 @@ _T = {torch.float32: _lib.BTQ_T_F32, torch.bfloat16: _lib.BTQ_T_BF16, torch.int1
       torch.int8: _lib.BTQ_T_INT8}
 _VALUES = (torch.float32, torch.bfloat16, torch.int16)
 _F32, _I8 = (torch.float32,), (torch.int8,)
+_NORM_OUT = _VALUES + _I8
 _NORMS = {"none": _lib.BTQ_NORM_NONE, "rms": _lib.BTQ_NORM_RMS, "layer": _lib.BTQ_NORM_LAYER}
 
 
-def _at(t: torch.Tensor, name: str, dtypes, shape, dev) -> int:
+# The calls below can be shorter on the GPU than the host's part of them, so
+# they check tensors by the quick way first (the device by its index, messages
+# only when something is wrong) and enter a stream's context only to allocate.
+
+def _index(x: torch.Tensor) -> int:
+    idx = x.get_device()
+    if idx < 0:
+        _device(x)
+    return idx
+
+
+def _at(t: torch.Tensor, name: str, dtypes, shape, idx: int) -> int:
     """Data pointer of a contiguous tensor, checked."""
-    # the quick form of _need: its messages only when something is wrong
-    if (t.dtype not in dtypes or t.shape != shape or not t.is_contiguous()
-            or t.get_device() != dev.index):
-        _need(t, name, dtypes, shape, dev)
+    if (t.dtype in dtypes and t.shape == shape and t.get_device() == idx
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, dtypes, shape, torch.device("cuda", idx))
     return t.data_ptr()
 
 
-def _stream_of(dev: torch.device, stream):
-    """_launch, with the quick way to torch's current stream: these calls are
-    short enough for the host's part of them to count."""
+def _stream_of(idx: int, stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index), _HERE
-    return _launch(dev, stream)
+        return torch._C._cuda_getCurrentRawStream(idx), None
+    return _launch(torch.device("cuda", idx), stream)
 
 
-_HERE = contextlib.nullcontext()
+def _empty(shape, dtype, idx: int, ctx) -> torch.Tensor:
+    with ctx or contextlib.nullcontext():
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", idx))
 
 
 def _rows(x: torch.Tensor, name: str, dtypes):
@@ -411,37 +423,34 @@ def btq_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     the others with any strides. q has x's shape and scale lacks its last
     dimension. For weights [P,N,K] the rows are the output channels.
     """
-    dev = _device(x)
+    idx = _index(x)
     P, T, K, shard, pitch = _rows(x, "x", _VALUES)
     shape = tuple(x.shape)
-    sh, ctx = _stream_of(dev, stream)
-    with ctx:
-        if q is None:
-            q = torch.empty(shape, dtype=torch.int8, device=dev)
-        if scale is None:
-            scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-        st = _lib.load().btq_quantize_rows(
-            x.data_ptr(), _T[x.dtype], shard, pitch, 1 if P is None else P, T, K,
-            _at(q, "q", _I8, shape, dev),
-            _at(scale, "scale", _F32, shape[:-1], dev), sh)
+    sh, ctx = _stream_of(idx, stream)
+    if q is None:
+        q = _empty(shape, torch.int8, idx, ctx)
+    if scale is None:
+        scale = _empty(shape[:-1], torch.float32, idx, ctx)
+    st = _lib.load().btq_quantize_rows(
+        x.data_ptr(), _T[x.dtype], shard, pitch, 1 if P is None else P, T, K,
+        _at(q, "q", _I8, shape, idx), _at(scale, "scale", _F32, shape[:-1], idx), sh)
     _lib.check(st, "btq_quantize_rows")
     return q, scale
 
 
-def _product_args(x_p, T, K, w, w_scale, bias, y, bf16, y_like, dev):
-    """Shape checks shared by the products; allocates y if needed."""
+def _product_args(x_p, T, K, w, w_scale, bias, y, dtype, idx, ctx):
+    """Checks shared by the products; allocates y of `dtype` if there is none."""
     if w.dim() != 3:
         raise ValueError(f"w: shape {tuple(w.shape)}, expected [P,N,K]")
-    P, N = w.shape[0], w.shape[1]
+    P, N, _ = w.shape
     if x_p is not None and x_p != P:
         raise ValueError(f"w: {P} shards, the activations have {x_p}")
-    wp = _at(w, "w", _I8, (P, N, K), dev)
-    sp = _at(w_scale, "w_scale", _F32, (P, N), dev)
-    bp = None if bias is None else _at(bias, "bias", _F32, (P, N), dev)
+    wp = _at(w, "w", _I8, (P, N, K), idx)
+    sp = _at(w_scale, "w_scale", _F32, (P, N), idx)
+    bp = None if bias is None else _at(bias, "bias", _F32, (P, N), idx)
     if y is None:
-        dt = torch.float32 if not bf16 else y_like
-        y = torch.empty((P, T, N), dtype=dt, device=dev)
-    return P, N, wp, sp, bp, y, _at(y, "y", _VALUES, (P, T, N), dev)
+        y = _empty((P, T, N), dtype, idx, ctx)
+    return P, N, wp, sp, bp, y, _at(y, "y", _VALUES, (P, T, N), idx)
 
 
 def btq_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
@@ -456,15 +465,14 @@ def btq_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
     is bf16 bits (int16), or float32 when not bf16; a given y may be float32,
     torch.bfloat16 or int16.
     """
-    dev = _device(a)
+    idx = _index(a)
     x_p, T, K, shard, pitch = _rows(a, "a", _I8)
-    sh, ctx = _stream_of(dev, stream)
-    with ctx:
-        P, N, wp, sp, bp, y, yp = _product_args(x_p, T, K, w, w_scale, bias, y, bf16, torch.int16,
-                                                dev)
-        asp = _at(a_scale, "a_scale", _F32, (T,) if x_p is None else (P, T), dev)
-        st = _lib.load().btq_int8_matmul(a.data_ptr(), shard, pitch, asp, 0 if x_p is None else T, wp,
-                                         sp, bp, P, T, N, K, yp, _T[y.dtype], sh)
+    sh, ctx = _stream_of(idx, stream)
+    P, N, wp, sp, bp, y, yp = _product_args(x_p, T, K, w, w_scale, bias, y,
+                                            torch.int16 if bf16 else torch.float32, idx, ctx)
+    asp = _at(a_scale, "a_scale", _F32, (T,) if x_p is None else (P, T), idx)
+    st = _lib.load().btq_int8_matmul(a.data_ptr(), shard, pitch, asp, 0 if x_p is None else T, wp,
+                                     sp, bp, P, T, N, K, yp, _T[y.dtype], sh)
     _lib.check(st, "btq_int8_matmul")
     return y
 
@@ -483,18 +491,19 @@ def btq_int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     y [P,T,N] as in btq_int8_matmul; without `y` a bf16 result has x's form
     of bf16 (int16 bits for float32 x).
     """
-    dev = _device(x)
+    idx = _index(x)
     x_p, T, K, shard, pitch = _rows(x, "x", _VALUES)
-    like = torch.bfloat16 if x.dtype == torch.bfloat16 else torch.int16
-    sh, ctx = _stream_of(dev, stream)
-    with ctx:
-        P, N, wp, sp, bp, y, yp = _product_args(x_p, T, K, w, w_scale, bias, y, bf16, like, dev)
-        if workspace is None:
-            workspace = torch.empty(btq_int8_linear_workspace_bytes(P, T, K), dtype=torch.uint8,
-                                    device=dev)
-        st = _lib.load().btq_int8_linear(
-            x.data_ptr(), _T[x.dtype], shard, pitch, wp, sp, bp, P, T, N, K, yp, _T[y.dtype],
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), sh)
+    sh, ctx = _stream_of(idx, stream)
+    dtype = (torch.float32 if not bf16 else
+             torch.bfloat16 if x.dtype == torch.bfloat16 else torch.int16)
+    P, N, wp, sp, bp, y, yp = _product_args(x_p, T, K, w, w_scale, bias, y, dtype, idx, ctx)
+    if workspace is None:
+        workspace = _empty(btq_int8_linear_workspace_bytes(P, T, K), torch.uint8, idx, ctx)
+    elif workspace.get_device() != idx or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous and on {x.device}")
+    st = _lib.load().btq_int8_linear(
+        x.data_ptr(), _T[x.dtype], shard, pitch, wp, sp, bp, P, T, N, K, yp, _T[y.dtype],
+        workspace.data_ptr(), workspace.nbytes, sh)
     _lib.check(st, "btq_int8_linear")
     return y
 
@@ -518,39 +527,48 @@ def btq_block_norm(y: Optional[torch.Tensor], residual: torch.Tensor, post: str 
     n: n_dtype (by default the residual's type; float32, bf16 or int8).
     Returns (residual_out, n), and n_scale [T] as a third for int8 n.
     """
-    dev = _device(residual)
+    idx = _index(residual)
     if residual.dim() != 2:
         raise ValueError(f"residual: shape {tuple(residual.shape)}, expected [T,H]")
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError(f"post and pre must be among {sorted(_NORMS)}")
     shape = T, H = residual.shape
-    rp = _at(residual, "residual", _VALUES, shape, dev)
-    yp = None if y is None else _at(y, "y", _VALUES, shape, dev)
-    pw, pb, nw, nb = [
-        None if t is None else _at(t, name, _F32, (H,), dev)
-        for name, t in (("post_weight", post_weight), ("post_bias", post_bias),
-                        ("pre_weight", pre_weight), ("pre_bias", pre_bias))]
-    gp, gt, gr = None, 0, 1
+    r_dtype = residual.dtype
+    rp = _at(residual, "residual", _VALUES, shape, idx)
+    yp = yt = pw = pb = nw = nb = gp = gt = sp = None
+    gr = 1
+    if y is not None:
+        yp, yt = _at(y, "y", _VALUES, shape, idx), _T[y.dtype]
+    if post_weight is not None:
+        pw = _at(post_weight, "post_weight", _F32, (H,), idx)
+    if post_bias is not None:
+        pb = _at(post_bias, "post_bias", _F32, (H,), idx)
+    if pre_weight is not None:
+        nw = _at(pre_weight, "pre_weight", _F32, (H,), idx)
+    if pre_bias is not None:
+        nb = _at(pre_bias, "pre_bias", _F32, (H,), idx)
     if gate is not None:
         gr = gate.shape[0] if gate.dim() == 2 else 0
-        gp, gt = _at(gate, "gate", _VALUES, (gr, H), dev), _T[gate.dtype]
-    sh, ctx = _stream_of(dev, stream)
-    with ctx:
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
-        op = _at(residual_out, "residual_out", (residual.dtype,), shape, dev)
-        if n is None:
-            n = torch.empty(shape, dtype=residual.dtype if n_dtype is None else n_dtype, device=dev)
-        np_ = _at(n, "n", _VALUES + (torch.int8,), shape, dev)
-        if n.dtype == torch.int8 and n_scale is None:
-            n_scale = torch.empty((T,), dtype=torch.float32, device=dev)
-        sp = None if n_scale is None else _at(n_scale, "n_scale", _F32, (T,), dev)
-        st = _lib.load().btq_block_norm(
-            yp, 0 if y is None else _T[y.dtype], rp, _T[residual.dtype], T, H, _NORMS[post], pw,
-            pb, eps if post_eps is None else post_eps, gp, gt, gr, alpha, _NORMS[pre], nw, nb, eps,
-            op, np_, _T[n.dtype], sp, sh)
-    _lib.check(st, "btq_block_norm")
-    return (residual_out, n, n_scale) if n.dtype == torch.int8 else (residual_out, n)
+        gp, gt = _at(gate, "gate", _VALUES, (gr, H), idx), _T[gate.dtype]
+    sh, ctx = _stream_of(idx, stream)
+    if residual_out is None:
+        residual_out = _empty(shape, r_dtype, idx, ctx)
+    op = _at(residual_out, "residual_out", (r_dtype,), shape, idx)
+    if n is None:
+        n = _empty(shape, n_dtype or r_dtype, idx, ctx)
+    np_ = _at(n, "n", _NORM_OUT, shape, idx)
+    int8 = n.dtype == torch.int8
+    if int8 and n_scale is None:
+        n_scale = _empty((T,), torch.float32, idx, ctx)
+    if n_scale is not None:
+        sp = _at(n_scale, "n_scale", _F32, (T,), idx)
+    st = _lib.load().btq_block_norm(
+        yp, yt or 0, rp, _T[r_dtype], T, H, _NORMS[post], pw, pb,
+        eps if post_eps is None else post_eps, gp, gt or 0, gr, alpha, _NORMS[pre], nw, nb, eps,
+        op, np_, _T[n.dtype], sp, sh)
+    if st:
+        _lib.check(st, "btq_block_norm")
+    return (residual_out, n, n_scale) if int8 else (residual_out, n)
 
 
 def btq_status_str(status: int) -> str:
