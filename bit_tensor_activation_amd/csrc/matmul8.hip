@@ -608,22 +608,29 @@ bool rows_aligned(const MatmulArgs& a) {
          ((uintptr_t)a.a & 15) == 0 && ((uintptr_t)a.w & 15) == 0;
 }
 
-// The tile for a product of more than 64 tokens: the one whose blocks, in
-// rounds over the chip's 256 CUs, cost least. A cost is the time of a round
-// with `few` (at most 256) or `full` (512, two a CU) blocks in units of a round
-// of 256 x 256 tiles, measured at K=4096: T=64 .. 4096, N=4096 .. 8192, P=1 and
-// 8. One tile for all sizes loses up to 5x (T=128 N=4096 K=4096: 8.3 us with
-// 32 x 64 tiles, 41.5 us with 256 x 256; T=8192 N=8192 K=8192: 450 us with
-// 256 x 256, 560 us with 128 x 128).
+// The tile whose blocks, in rounds over the chip's 256 CUs, cost least. A cost
+// is the time of a round with `few` (at most 256) or `full` (512, two a CU)
+// blocks in units of a round of 256 x 256 tiles, measured at K=4096: T=64 ..
+// 4096, N=4096 .. 8192, P=1 and 8. One tile for all sizes loses up to 5x (T=128
+// N=4096 K=4096: 8.3 us with 32 x 64 tiles, 41.5 us with 256 x 256; T=8192
+// N=8192 K=8192: 450 us with 256 x 256, 560 us with 128 x 128). Rows on any
+// byte cost more for each load, so large tiles pay sooner (K=4095 N=4096 T=256:
+// 22 us with 32 x 64, 46 with 128 x 128; 8192 x 8192: 742 with 256 x 256, 881
+// with 128 x 128, 1199 with 128 x 64).
 enum Tile { k256x256, k128x128, k128x64, k64x64, k32x64, k32x32, kTiles };
 
-Tile choose_tile(const MatmulArgs& a) {
-  struct {
+Tile choose_tile(const MatmulArgs& a, bool direct) {
+  struct Cost {
     int n, t;
     float few, full;
-  } const tiles[kTiles] = {{256, 256, 1.0f, 2.0f},  {128, 128, 0.37f, 0.62f},
-                           {128, 64, 0.26f, 0.42f}, {64, 64, 0.17f, 0.30f},
-                           {32, 64, 0.13f, 0.22f},  {32, 32, 0.11f, 0.16f}};
+  };
+  constexpr Cost direct_cost[kTiles] = {{256, 256, 1.0f, 2.0f},  {128, 128, 0.37f, 0.62f},
+                                        {128, 64, 0.26f, 0.42f}, {64, 64, 0.17f, 0.30f},
+                                        {32, 64, 0.13f, 0.22f},  {32, 32, 0.11f, 0.16f}};
+  constexpr Cost any_cost[kTiles] = {{256, 256, 1.0f, 2.0f},  {128, 128, 0.50f, 0.59f},
+                                     {128, 64, 0.39f, 0.43f}, {64, 64, 9.0f, 9.0f},   // not built
+                                     {32, 64, 0.15f, 0.24f},  {32, 32, 0.10f, 0.15f}};
+  const Cost* tiles = direct ? direct_cost : any_cost;
   Tile best = k256x256;
   float least = 0.0f;
   for (int i = 0; i < kTiles; ++i) {
@@ -677,7 +684,7 @@ hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
       if (n32 >= 256) return launch_split<1, 2, 6>(a, s);
       return launch_split<1, 1, 6>(a, s);
     }
-    switch (choose_tile(a)) {
+    switch (choose_tile(a, true)) {
       case k256x256: return launch_tiles<2, 2, 4, 4, 2>(a, s);
       case k128x128:   // one block a CU: more steps in flight
         return n128 * ((a.T + 127) / 128) <= 256 ? launch_tiles<2, 2, 2, 2, 4>(a, s)
@@ -688,14 +695,14 @@ hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
       default: return launch_split<1, 1, 6>(a, s);
     }
   }
-  // Rows on any byte: 128 x 128 tiles, or 32 x 32 where those leave half of the
-  // CUs idle or most of a tile's tokens are missing (K=4095 N=4096: T=512 46.5
-  // against 53.3 us, T=256 45.5 against 30.4; N=8192 P=8: T=64 K=4094 95.9
-  // against 129.9, T=16 K=1023 25.0 against 19.3).
-  if (spans_ok(a) && a.K >= 16) {
-    const int64_t b128 = a.P * ((a.N + 127) / 128) * ((a.T + 127) / 128);
-    return a.T > 32 && b128 >= 128 ? launch_tiles<2, 2, 2, 2, 2, kAnyByte>(a, s)
-                                   : launch_split<1, 1, 3, kAnyByte>(a, s);
+  if (spans_ok(a) && a.K >= 16) {   // rows on any byte
+    switch (choose_tile(a, false)) {
+      case k256x256: return launch_tiles<2, 2, 4, 4, 2, kAnyByte>(a, s);
+      case k128x128: return launch_tiles<2, 2, 2, 2, 2, kAnyByte>(a, s);
+      case k128x64: return launch_tiles<4, 1, 1, 2, 2, kAnyByte>(a, s);
+      case k32x64: return launch_split<1, 2, 4, kAnyByte>(a, s);
+      default: return launch_split<1, 1, 3, kAnyByte>(a, s);
+    }
   }
   const int64_t tt = (a.T + kGenTile - 1) / kGenTile, tn = (a.N + kGenTile - 1) / kGenTile;
   const int64_t tiles = a.P * tt * tn;

@@ -245,7 +245,8 @@ LARGE = [  # P, T, N, K: what takes each tile size, whole and ragged, aligned an
     (1, 90, 4096, 1024), (8, 60, 8192, 528), (8, 33, 8190, 400), (8, 30, 8192, 2176),
     (8, 7, 8200, 656), (4, 50, 4096, 1024), (1, 1024, 4095, 2047), (3, 2047, 1023, 513),
     (8, 64, 2047, 1001), (2, 500, 900, 18), (2, 60, 8192, 1040), (8, 16, 8200, 4112),
-    (8, 64, 8192, 4096), (9, 10, 16384, 2048)]
+    (8, 64, 8192, 4096), (9, 10, 16384, 2048), (8, 2048, 2048, 2043), (1, 1024, 4096, 1021),
+    (8, 300, 999, 1001), (1, 256, 4096, 1030), (2, 100, 1000, 1029), (1, 2, 4095, 4095)]
 
 
 @pytest.mark.gpu
