@@ -193,7 +193,9 @@ struct RowMap {
     if constexpr (kType == kF32) return __uint_as_float(w[j]);
     return j & 1 ? __uint_as_float(w[j / 2] & 0xffff0000u) : __uint_as_float(w[j / 2] << 16);
   }
-  // 8 elements of kSize bytes, packed in w
+  // 8 elements of kSize bytes, packed in w. The streaming hint leaves the caches
+  // to what is read (norm T=16384 H=8192: 255 -> 238 us, T=512: 11.4 -> 9.8);
+  // on the loads it costs where the data is in the cache.
   template <int kSize>
   __device__ __forceinline__ void put(const R& r, int v, const uint32_t* w) const {
     const int h = at(v, 0);
@@ -205,7 +207,7 @@ struct RowMap {
 #pragma unroll
         for (int q = 0; q < kSize / 2; ++q)
           __builtin_amdgcn_raw_buffer_store_b128(
-              v4u{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]}, r.r, off + 16u * q, 0, 0);
+              v4u{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]}, r.r, off + 16u * q, 0, kStream);
       }
     } else if (h + 8 <= H) {
       __builtin_memcpy(r.p + (int64_t)h * kSize, w, 8 * kSize);
