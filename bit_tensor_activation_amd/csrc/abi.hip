@@ -388,11 +388,13 @@ int btq_int8_linear(const void* x, int x_type, int64_t x_shard, int64_t x_pitch,
   const int64_t rows = x_shard == 0 ? 1 : P;   // shards of activations
   int8_t* q = (int8_t*)workspace;
   float* scale = (float*)(q + P * T * pitch);
+  const btq::MatmulArgs m = {q, rows == 1 ? 0 : T * pitch, pitch, scale, rows == 1 ? 0 : T,
+                             w, w_scale, bias, P, T, N, K, y, y_type};
+  if (btq::small_linear_ok(x, x_type, x_shard, x_pitch, m))
+    return hip_status(btq::launch_small_linear(x, x_shard, x_pitch, m, (hipStream_t)stream));
   st = hip_status(btq::launch_quantize_rows(x, x_type, x_shard, x_pitch, rows, T, K, q, pitch,
                                             scale, (hipStream_t)stream));
   if (st != BTQ_OK) return st;
-  const btq::MatmulArgs m = {q, rows == 1 ? 0 : T * pitch, pitch, scale, rows == 1 ? 0 : T,
-                             w, w_scale, bias, P, T, N, K, y, y_type};
   return hip_status(btq::launch_int8_matmul(m, (hipStream_t)stream));
 }
 

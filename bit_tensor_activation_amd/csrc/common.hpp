@@ -123,6 +123,26 @@ __device__ __forceinline__ TileGeom tile_geom(const int32_t* __restrict__ cmap, 
   return g;
 }
 
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kCtrl, 0xf, 0xf, true);
+}
+
+// x combined over the 64 lanes, in all of them: neighbours in 4, halves of 8,
+// halves of 16, then rows of 16 and halves of the wave by swaps. A few cycles a
+// step, where a shuffle through LDS takes over a hundred.
+template <typename F>
+__device__ __forceinline__ uint32_t wave_combine(uint32_t x, F f) {
+  x = f(x, dpp<0xb1>(x));    // quad_perm 1,0,3,2
+  x = f(x, dpp<0x4e>(x));    // quad_perm 2,3,0,1
+  x = f(x, dpp<0x141>(x));   // row_half_mirror
+  x = f(x, dpp<0x140>(x));   // row_mirror
+  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = f(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return f(b[0], b[1]);
+}
+
 // ---- values of the calls around the codec ----
 enum ValueType { kF32 = 0, kBf16 = 1, kInt8 = 2 };   // btq_type
 
@@ -239,6 +259,14 @@ struct MatmulArgs {
   int y_type;
 };
 hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s);
+
+// btq_int8_linear in one launch, for products so small that launches count.
+// small_linear_ok: whether the sizes and x (bf16, row strides in elements) suit
+// it; m.a and m.a_scale are not used.
+bool small_linear_ok(const void* x, int x_type, int64_t x_shard, int64_t x_pitch,
+                     const MatmulArgs& m);
+hipError_t launch_small_linear(const void* x, int64_t x_shard, int64_t x_pitch,
+                               const MatmulArgs& m, hipStream_t s);
 
 struct NormArgs {
   const void* y;            // null: no block output

@@ -244,10 +244,12 @@ __device__ __forceinline__ void wait_loads() {
 }
 // A block's share of the product: RN channels x RT tokens of shard p, and the
 // loads of its operands, 256 threads together, into S buffers of LDS.
-// kNt: the channels' loads stream past the caches.
-template <int RN, int RT, int S, bool kNt>
+// kNt: the channels' loads stream past the caches. kCodes: the block makes the
+// tokens' codes and scales itself; only the channels are loaded.
+template <int RN, int RT, int S, bool kNt, bool kCodes = false>
 struct Block {
-  static constexpr int kLoads = (RN + RT) / 32, kStage = (RN + RT) * kStep;
+  static constexpr int kTokens = kCodes ? 0 : RT;   // rows of tokens in a step
+  static constexpr int kLoads = (RN + kTokens) / 32, kStage = (RN + kTokens) * kStep;
   struct Lds {
     __align__(1024) int8_t operands[S * kStage];
     // whole loads of 64
@@ -279,21 +281,23 @@ struct Block {
     const int pitch = (int)g.a_pitch, tid = threadIdx.x, row = tid >> 3;
     wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     w = g.w + (p * g.N + n0) * g.K;
-    a = g.a + p * g.a_shard + t0 * g.a_pitch;
     rw = make_rsrc(w, (uint32_t)(nrows * K));
-    ra = make_rsrc(a, (uint32_t)((trows - 1) * pitch + K));
+    if constexpr (!kCodes) {
+      a = g.a + p * g.a_shard + t0 * g.a_pitch;
+      ra = make_rsrc(a, (uint32_t)((trows - 1) * pitch + K));
+    }
     chunk = ((tid & 7) ^ (row >> 1 & 7)) * 16;
 #pragma unroll
     for (int i = 0; i < RN / 32; ++i)
       off[i] = (uint32_t)(min(row + 32 * i, nrows - 1) * K + chunk);
 #pragma unroll
-    for (int i = 0; i < RT / 32; ++i)
+    for (int i = 0; i < kTokens / 32; ++i)
       off[RN / 32 + i] = (uint32_t)(min(row + 32 * i, trows - 1) * pitch + chunk);
     to = lds_address(lds.operands) + wave * 1024;
     // The scales and biases go to LDS first, where the epilogue reads them
     // without waiting for its own stores (vector loads and stores retire in
     // one order). One wave loads 64 of them at a time.
-    stage(g.a_scale + p * g.as_shard + t0, trows, lds.sa, RT);
+    if constexpr (!kCodes) stage(g.a_scale + p * g.as_shard + t0, trows, lds.sa, RT);
     stage(g.w_scale + p * g.N + n0, nrows, lds.sw, RN);
     if (g.bias)
       stage(g.bias + p * g.N + n0, nrows, lds.bias, RN);
@@ -456,6 +460,48 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
   }
 }
 
+// The end of the kernels whose waves split k: sums added through LDS, scaled
+// and stored.
+template <int MN, int MT, bool kVec, bool kBf, typename B>
+__device__ __forceinline__ void finish_split(const MatmulArgs& g, const B& b,
+                                             typename B::Lds& lds, const v16i (&acc)[MN][MT]) {
+  wait_loads<0, true>();   // no load may land in what is written next
+  lds_barrier();
+  const OutTile o = {out_rsrc<kBf>(g, b.p, b.t0, b.n0, b.trows, b.nrows), lds.sw, lds.bias,
+                     b.nrows};
+  // wave v finishes the channels 8v .. 8v+7 of every product: acc[4v .. 4v+3]
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  constexpr int kSums = 4 * MN * MT * 4 * 64 * 16;
+  static_assert(kSums + MT * kTurnBytes<MN, kBf> <= sizeof(lds.operands), "the sums fit");
+  v4i* sums = (v4i*)lds.operands;
+  int8_t* turn = lds.operands + kSums;
+#pragma unroll
+  for (int i = 0; i < MN; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        sums[((b.wave * MN * MT + i * MT + j) * 4 + v) * 64 + lane] =
+            v4i{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
+                acc[i][j][4 * v + 3]};
+  lds_barrier();
+#pragma unroll
+  for (int i = 0; i < MN; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      v4i sum = sums[((i * MT + j) * 4 + b.wave) * 64 + lane];
+#pragma unroll
+      for (int q = 1; q < 4; ++q)
+        sum += sums[((q * MN * MT + i * MT + j) * 4 + b.wave) * 64 + lane];
+      const int t = 32 * j + (lane & 31), c = 32 * i + 8 * b.wave + 4 * h;
+      const float sa = lds.sa[t];
+      const v4f w = *(const v4f*)(o.sw + c), bias = *(const v4f*)(o.bias + c);
+      store_turn<kBf>(turn + t * kTurnRow<MN, kBf>, c, sum, sa, w, bias);
+    }
+  lds_barrier();
+  store_turned<256, MN, kVec, kBf>((int)threadIdx.x, 32 * MT, turn, o, 0, 0, b.trows, (int)g.N);
+}
+
 // ---- few tokens or few tiles: the waves of a block split k ----
 //
 // The product then costs less than reading the weights, and what counts is
@@ -505,60 +551,138 @@ __global__ __launch_bounds__(256, 2) void matmul_split_kernel(MatmulArgs g, int 
       buf = buf + 1 == S ? 0 : buf + 1;
     }
   } else {
-    // two steps on their way in registers, two in LDS
-    v4i rows[2][kLoads];
+    // steps on their way in registers, and as many in LDS
+    constexpr int kDeep = MN * MT == 1 ? 4 : 2;
+    v4i rows[kDeep][kLoads];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < kDeep; ++q)
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) rows[q][i] = b.load(q, i);
-    for (int step = 0; step < steps; step += 2) {
+    for (int step = 0; step < steps; step += kDeep) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < kDeep; ++q) {
+        if (step + q >= steps) break;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) B::put(lds, q, i, rows[q][i]);
         lds_barrier();
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) rows[q][i] = b.load(step + 2 + q, i);
+        for (int i = 0; i < kLoads; ++i) rows[q][i] = b.load(step + kDeep + q, i);
         read(q);
-        multiply();   // of zeros where the row has ended
+        multiply();
       }
     }
   }
-  wait_loads<0, true>();   // no load may land in what is written next
-  lds_barrier();
-  const OutTile o = {out_rsrc<kBf>(g, b.p, b.t0, b.n0, b.trows, b.nrows), lds.sw, lds.bias,
-                     b.nrows};
-  // wave v finishes the channels 8v .. 8v+7 of every product: acc[4v .. 4v+3]
-  const int lane = threadIdx.x & 63, h = lane >> 5;
-  constexpr int kSums = 4 * MN * MT * 4 * 64 * 16;
-  static_assert(kSums + MT * kTurnBytes<MN, kBf> <= sizeof(lds.operands), "the sums fit");
-  v4i* sums = (v4i*)lds.operands;
-  int8_t* turn = lds.operands + kSums;
+  finish_split<MN, MT, kVec, kBf>(g, b, lds, acc);
+}
+
+// ---- activations quantized by the block: one launch for a small linear layer ----
+//
+// For calls that the second launch and the codes' way through memory would
+// lengthen most: 32 channels x kTokens tokens a block, waves splitting k as
+// above. A wave reads 16/NVEC rows of x, all at once (NVEC vectors of 8 a lane),
+// takes their largest values and leaves codes and scales in LDS, while the first
+// steps of the weights land. Every block of channels quantizes its tokens
+// again, from L2; with at most two blocks a CU that costs less than the launch
+// (P=8 T=1 N=1024 K=1024: 4.1 us against 5.7 for the two kernels in a graph;
+// P=3 T=77 N=999 K=1000: 7.6 against 9.1, and 10.0 against 12.9 called from
+// Python; only 32 rows of short k lose, T=32 N=4096 K=512: 6.1 against 5.5 in a
+// graph).
+template <Load kLoad, int NVEC, bool kBf>
+__global__ __launch_bounds__(256, 2) void linear_small_kernel(MatmulArgs g, const uint16_t* x,
+                                                              int64_t x_shard, int64_t x_pitch,
+                                                              int tiles_t, int tiles_n, int tiles) {
+  constexpr int kRows = 16 / NVEC, kTokens = 4 * kRows, S = 6;
+  constexpr int kCodeRow = NVEC * 512 + 16;   // 16: rows start in different banks
+  using B = Block<32, kTokens, S, false, true>;
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+  typedef unsigned short v2h __attribute__((ext_vector_type(2)));
+  __shared__ typename B::Lds lds;
+  __shared__ __align__(16) int8_t codes[kTokens * kCodeRow];
+  const B b(g, tiles_t, tiles_n, tiles, lds);
+  const int lane = threadIdx.x & 63;
+  v4i raw[kRows][NVEC];
 #pragma unroll
-  for (int i = 0; i < MN; ++i)
+  for (int r = 0; r < kRows; ++r) {
+    if (4 * r + b.wave >= b.trows) break;
+    const int64_t t = b.t0 + 4 * r + b.wave;
+    const rsrc_t rx = make_rsrc(x + b.p * x_shard + t * x_pitch, (uint32_t)b.K * 2u);
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
+    for (int v = 0; v < NVEC; ++v)
+      raw[r][v] = __builtin_bit_cast(
+          v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, (uint32_t)(v * 64 + lane) * 16u, 0, 0));
+  }
+  issue_fence();
+  constexpr int kDeep = 4;   // steps on their way in registers (kAnyByte)
+  v4i rows[kDeep];
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        sums[((b.wave * MN * MT + i * MT + j) * 4 + v) * 64 + lane] =
-            v4i{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
-                acc[i][j][4 * v + 3]};
-  lds_barrier();
+  for (int q = 0; q < (kLoad == kAnyByte ? kDeep : S - 1); ++q) {
+    if constexpr (kLoad == kAnyByte)
+      rows[q] = b.load(q, 0);
+    else
+      b.fetch(q, q, 0);
+  }
 #pragma unroll
-  for (int i = 0; i < MN; ++i)
+  for (int r = 0; r < kRows; ++r) {
+    if (4 * r + b.wave >= b.trows) break;
+    v2h big = {0, 0};
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      v4i sum = sums[((i * MT + j) * 4 + b.wave) * 64 + lane];
+    for (int v = 0; v < NVEC; ++v)
 #pragma unroll
-      for (int q = 1; q < 4; ++q)
-        sum += sums[((q * MN * MT + i * MT + j) * 4 + b.wave) * 64 + lane];
-      const int t = 32 * j + (lane & 31), c = 32 * i + 8 * b.wave + 4 * h;
-      const float sa = lds.sa[t];
-      const v4f w = *(const v4f*)(o.sw + c), bias = *(const v4f*)(o.bias + c);
-      store_turn<kBf>(turn + t * kTurnRow<MN, kBf>, c, sum, sa, w, bias);
+      for (int j = 0; j < 4; ++j)
+        big = __builtin_elementwise_max(
+            big, __builtin_bit_cast(v2h, (uint32_t)raw[r][v][j] & 0x7fff7fffu));
+    const uint32_t most = wave_combine((uint32_t)max(big[0], big[1]) << 16,
+                                       [](uint32_t p, uint32_t q) { return max(p, q); });
+    const RowScale rs = row_scale(most);
+    const int t = 4 * r + b.wave;
+    if (lane == 0) lds.sa[t] = rs.scale;
+#pragma unroll
+    for (int v = 0; v < NVEC; ++v) {
+      uint32_t c[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t d = (uint32_t)raw[r][v][j];
+        c[2 * j] = code_bits(__uint_as_float(d << 16), rs.mul);
+        c[2 * j + 1] = code_bits(__uint_as_float(d & 0xffff0000u), rs.mul);
+      }
+      *(v2u*)(codes + t * kCodeRow + (v * 64 + lane) * 8) =
+          v2u{c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
+              c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24};
     }
+  }
   lds_barrier();
-  store_turned<256, MN, kVec, kBf>((int)threadIdx.x, RT, turn, o, 0, 0, b.trows, (int)g.N);
+  const int8_t* code = codes + min(lane & 31, b.trows - 1) * kCodeRow + b.wave * 32 +
+                       (lane >> 5) * 16;
+  v16i acc[1][1] = {};
+  auto multiply = [&](int buf, int step) {
+    acc[0][0] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+        B::read(lds, buf, b.wave, 0), *(const v4i*)(code + step * kStep), acc[0][0], 0, 0, 0);
+  };
+  const int steps = b.steps();
+  if constexpr (kLoad == kAnyByte) {
+    for (int step = 0; step < steps; step += kDeep) {
+#pragma unroll
+      for (int q = 0; q < kDeep; ++q) {
+        if (step + q >= steps) break;   // codes end with the row
+        B::put(lds, q, 0, rows[q]);
+        lds_barrier();
+        rows[q] = b.load(step + kDeep + q, 0);
+        multiply(q, step + q);
+      }
+    }
+  } else {
+    int buf = 0;
+    for (int step = 0; step < steps; ++step) {
+      wait_loads<S - 2, false>();
+      __builtin_amdgcn_s_barrier();
+      issue_fence();
+      b.fetch(step + S - 1, buf == 0 ? S - 1 : buf - 1, 0);
+      multiply(buf, step);
+      issue_fence();
+      buf = buf + 1 == S ? 0 : buf + 1;
+    }
+  }
+  finish_split<1, 1, false, kBf>(g, b, lds, acc);
 }
 
 constexpr int64_t kMaxBlocks = int64_t(1) << 20;
@@ -650,6 +774,34 @@ Tile choose_tile(const MatmulArgs& a, bool direct) {
   return best;
 }
 
+// Vectors of 8 a lane for rows of K, and the tokens of a block.
+int small_vectors(int64_t K) { return K <= 1024 ? 2 : K <= 2048 ? 4 : K <= 4096 ? 8 : 16; }
+
+template <Load kLoad, int NVEC>
+hipError_t launch_small(const void* x, int64_t x_shard, int64_t x_pitch, const MatmulArgs& m,
+                        hipStream_t s) {
+  constexpr int kTokens = 64 / NVEC;
+  const int64_t tt = (m.T + kTokens - 1) / kTokens, tn = (m.N + 31) / 32, n = m.P * tt * tn;
+  if (m.y_type == kBf16)
+    linear_small_kernel<kLoad, NVEC, true><<<dim3((unsigned)n), 256, 0, s>>>(
+        m, (const uint16_t*)x, x_shard, x_pitch, (int)tt, (int)tn, (int)n);
+  else
+    linear_small_kernel<kLoad, NVEC, false><<<dim3((unsigned)n), 256, 0, s>>>(
+        m, (const uint16_t*)x, x_shard, x_pitch, (int)tt, (int)tn, (int)n);
+  return hipGetLastError();
+}
+
+template <Load kLoad>
+hipError_t launch_small_rows(const void* x, int64_t x_shard, int64_t x_pitch, const MatmulArgs& m,
+                             hipStream_t s) {
+  switch (small_vectors(m.K)) {
+    case 2: return launch_small<kLoad, 2>(x, x_shard, x_pitch, m, s);
+    case 4: return launch_small<kLoad, 4>(x, x_shard, x_pitch, m, s);
+    case 8: return launch_small<kLoad, 8>(x, x_shard, x_pitch, m, s);
+    default: return launch_small<kLoad, 16>(x, x_shard, x_pitch, m, s);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
@@ -701,7 +853,7 @@ hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
       case k128x128: return launch_tiles<2, 2, 2, 2, 2, kAnyByte>(a, s);
       case k128x64: return launch_tiles<4, 1, 1, 2, 2, kAnyByte>(a, s);
       case k32x64: return launch_split<1, 2, 4, kAnyByte>(a, s);
-      default: return launch_split<1, 1, 3, kAnyByte>(a, s);
+      default: return launch_split<1, 1, 4, kAnyByte>(a, s);
     }
   }
   const int64_t tt = (a.T + kGenTile - 1) / kGenTile, tn = (a.N + kGenTile - 1) / kGenTile;
@@ -709,6 +861,22 @@ hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
   matmul_general_kernel<<<dim3((unsigned)(tiles < kMaxBlocks ? tiles : kMaxBlocks)), 256, 0, s>>>(
       a, tt, tn, tiles);
   return hipGetLastError();
+}
+
+bool small_linear_ok(const void* x, int x_type, int64_t x_shard, int64_t x_pitch,
+                     const MatmulArgs& m) {
+  if (x_type != kBf16 || m.K < 16 || m.K > 8192 || m.K % 2 || m.N >= (int64_t(1) << 20))
+    return false;
+  if (((uintptr_t)x & 3) || x_shard % 2 || x_pitch % 2) return false;   // rows on 4 bytes
+  const int64_t tokens = 64 / small_vectors(m.K);
+  return m.P * ((m.N + 31) / 32) * ((m.T + tokens - 1) / tokens) <= 512;
+}
+
+hipError_t launch_small_linear(const void* x, int64_t x_shard, int64_t x_pitch,
+                               const MatmulArgs& m, hipStream_t s) {
+  return m.K % 16 == 0 && ((uintptr_t)m.w & 15) == 0
+             ? launch_small_rows<kDirect>(x, x_shard, x_pitch, m, s)
+             : launch_small_rows<kAnyByte>(x, x_shard, x_pitch, m, s);
 }
 
 }  // namespace btq

@@ -240,26 +240,6 @@ struct RowMap {
   }
 };
 
-template <int kCtrl>
-__device__ __forceinline__ uint32_t dpp(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kCtrl, 0xf, 0xf, true);
-}
-
-// x combined over the 64 lanes, in all of them: neighbours in 4, halves of 8,
-// halves of 16, then rows of 16 and halves of the wave by swaps. A few cycles a
-// step, where a shuffle through LDS takes over a hundred.
-template <typename F>
-__device__ __forceinline__ uint32_t wave_combine(uint32_t x, F f) {
-  x = f(x, dpp<0xb1>(x));    // quad_perm 1,0,3,2
-  x = f(x, dpp<0x4e>(x));    // quad_perm 2,3,0,1
-  x = f(x, dpp<0x141>(x));   // row_half_mirror
-  x = f(x, dpp<0x140>(x));   // row_mirror
-  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-  x = f(a[0], a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  return f(b[0], b[1]);
-}
-
 // One value a lane combined over the G lanes of a row; all lanes get it.
 // `slot` is LDS that no other exchange in flight uses.
 template <int G, typename F>

@@ -420,7 +420,7 @@ int btq_int8_matmul(const int8_t *a, int64_t a_shard, int64_t a_pitch,
 /*
  * btq_quantize_rows on x, then btq_int8_matmul of its codes: a linear layer
  * with 8-bit weights on fp32 or bf16 activations. Bit for bit the result of
- * the two calls. workspace: device scratch of at least
+ * the two calls; small ones run in one launch. workspace: device scratch of at least
  * btq_int8_linear_workspace_bytes(P,T,K) bytes, 16-byte aligned, with no
  * initial value. x_shard == 0 quantizes one set of T rows for all shards.
  */

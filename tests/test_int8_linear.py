@@ -358,7 +358,10 @@ def test_int8_matmul_offsets_past_32_bits(T, N, K):
 @pytest.mark.gpu
 @pytest.mark.parametrize("P,T,N,K", [(1, 1, 8, 5), (8, 1, 512, 1024), (2, 1, 40, 8208), (2, 3, 64, 256),
                                      (2, 8, 320, 512), (3, 16, 48, 100), (1, 40, 96, 2048),
-                                     (2, 64, 128, 1008), (3, 77, 99, 1000), (2, 300, 256, 512)])
+                                     (2, 64, 128, 1008), (3, 77, 99, 1000), (2, 300, 256, 512),
+                                     (1, 9, 70, 4096), (2, 5, 33, 8192), (1, 3, 40, 5598),
+                                     (2, 33, 40, 2046), (1, 17, 64, 18), (8, 300, 512, 640),
+                                     (2, 4, 40, 8194)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_int8_linear_is_the_two_calls(P, T, N, K, dtype):
     say(f"case: int8_linear P={P} T={T} N={N} K={K} {dtype}")
