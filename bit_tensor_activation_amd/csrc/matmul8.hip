@@ -124,6 +124,12 @@ constexpr int kTurnRow = 32 * MN * (kBf ? 2 : 4) + 16;
 template <int MN, bool kBf>
 constexpr int kTurnBytes = 32 * kTurnRow<MN, kBf>;
 
+// The lane, counted anew: cheaper at a kernel's end than a register held
+// through its loop.
+__device__ __forceinline__ int lane_id() {
+  return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
+}
+
 // 4 channels c.. of one token to its turned row.
 template <bool kBf>
 __device__ __forceinline__ void store_turn(int8_t* row, int c, v4i sum, float sa, v4f w, v4f b) {
@@ -167,7 +173,7 @@ template <int MN, bool kVec, bool kBf>
 __device__ __forceinline__ void store_rows(const v16i* const (&acc)[MN], const OutTile& o,
                                            int8_t* turn, float sa, int t, int n, int rows, int N) {
   constexpr int kRow = kTurnRow<MN, kBf>;
-  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int lane = lane_id(), h = lane >> 5;
   int8_t* to = turn + (lane & 31) * kRow;
 #pragma unroll
   for (int i = 0; i < MN; ++i)
@@ -320,19 +326,22 @@ struct Block {
     else
       load_to_lds<16>(ra, at, from, step * kStep);
   }
-  // The same load to registers, for rows on any byte: 16 bytes that end inside
-  // the row, shifted down to where they belong.
-  __device__ __forceinline__ v4i load(int step, int i) const {
-    const int8_t* from = i < RN / 32 ? w : a;
-    const int k = step * kStep;
+  // The same load to registers, for rows on any byte: of a step that ends
+  // inside the rows,
+  __device__ __forceinline__ v4i load_whole(int step, int i) const {
     v4i v;
-    if (k + kStep <= K) {
-      __builtin_memcpy(&v, from + (off[i] + (uint32_t)k), 16);
-      return v;
-    }
+    __builtin_memcpy(&v, (i < RN / 32 ? w : a) + (off[i] + (uint32_t)(step * kStep)), 16);
+    return v;
+  }
+  // and of any step: 16 bytes that end inside the row, shifted down to where
+  // they belong.
+  __device__ __forceinline__ v4i load(int step, int i) const {
+    const int k = step * kStep;
+    if (k + kStep <= K) return load_whole(step, i);
     const int past = max(k + chunk + 16 - K, 0);   // bytes of the chunk past the row
     if (past >= 16) return v4i{0, 0, 0, 0};
-    __builtin_memcpy(&v, from + (off[i] + (uint32_t)(k - past)), 16);
+    v4i v;
+    __builtin_memcpy(&v, (i < RN / 32 ? w : a) + (off[i] + (uint32_t)(k - past)), 16);
     const unsigned __int128 bits = __builtin_bit_cast(unsigned __int128, v) >> (8 * past);
     return __builtin_bit_cast(v4i, bits);
   }
@@ -375,8 +384,8 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
   };
   v16i acc[MN][MT] = {};
   // The products of a slice, in turn with the reads of the slice after it and
-  // loads d0..d1 of step `ds`. The fences keep this order.
-  auto slice = [&](int set, int rbuf, int rslice, int ds, int dbuf, int d0, int d1) {
+  // with also(d0) .. also(d1 - 1). The fences keep this order.
+  auto slice = [&](int set, int rbuf, int rslice, int d0, int d1, auto also) {
     constexpr int kM = MN * MT, kR = MN + MT;
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
@@ -387,10 +396,11 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
         if (min(r * kM / kR / 2, kM - 1) == m) read(rbuf, rslice, r);
 #pragma unroll
       for (int d = 0; d < kLoads; ++d)
-        if (kLoad != kAnyByte && d >= d0 && d < d1 && (d - d0) * kM / (d1 - d0) == m) b.fetch(ds, dbuf, d);
+        if (d >= d0 && d < d1 && (d - d0) * kM / (d1 - d0) == m) also(d);
       issue_fence();
     }
   };
+  const auto nothing = [](int) {};
   const int steps = b.steps();
   int buf = 0;
   if constexpr (kLoad != kAnyByte) {
@@ -410,37 +420,57 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
     for (int step = 0; step < steps; ++step) {
       const int next = S == 2 ? buf ^ 1 : buf + 1 == S ? 0 : buf + 1;
       const int last = S == 2 ? next : buf == 0 ? S - 1 : buf - 1;   // buffer of step + S - 1
-      slice(0, buf, 1, step + S - 1, last, kEarly, kLoads);
-      slice(1, buf, 2, 0, 0, 0, 0);
-      slice(0, buf, 3, 0, 0, 0, 0);
+      slice(0, buf, 1, kEarly, kLoads, [&](int d) { b.fetch(step + S - 1, last, d); });
+      slice(1, buf, 2, 0, 0, nothing);
+      slice(0, buf, 3, 0, 0, nothing);
       wait_loads<(S - 2) * kLoads, true>();   // the next step is in LDS
       __builtin_amdgcn_s_barrier();           // for all waves, and this buffer is free
       issue_fence();
-      slice(1, next, 0, step + S, buf, 0, kEarly);
+      slice(1, next, 0, 0, kEarly, [&](int d) { b.fetch(step + S, buf, d); });
       buf = next;
     }
   } else {
     v4i next_rows[kLoads];
+    if (b.K >= kStep) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) next_rows[i] = b.load(0, i);
+      for (int i = 0; i < kLoads; ++i) next_rows[i] = b.load_whole(0, i);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) B::put(lds, 0, i, next_rows[i]);
+      for (int i = 0; i < kLoads; ++i) B::put(lds, 0, i, next_rows[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        B::put(lds, 0, i, b.load(0, i));
+        issue_fence();
+      }
+    }
     wait_loads<0, true>();   // also the scales
     lds_barrier();
 #pragma unroll
     for (int i = 0; i < MN + MT; ++i) read(0, 0, i);
-    for (int step = 0; step < steps; ++step, buf ^= 1) {
-      if (step + 1 < steps) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) next_rows[i] = b.load(step + 1, i);
-      }
-      slice(0, buf, 1, 0, 0, 0, 0);
-      slice(1, buf, 2, 0, 0, 0, 0);
-      slice(0, buf, 3, 0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) B::put(lds, buf ^ 1, i, next_rows[i]);
+    // the next step's loads go out over two slices and into the other buffer
+    // over the third
+    int step = 0;
+    for (; step + 1 < b.K / kStep; ++step) {
+      const auto load = [&](int d) { next_rows[d] = b.load_whole(step + 1, d); };
+      slice(0, buf, 1, 0, kLoads / 2, load);
+      slice(1, buf, 2, kLoads / 2, kLoads, load);
+      slice(0, buf, 3, 0, kLoads, [&](int d) { B::put(lds, buf ^ 1, d, next_rows[d]); });
       lds_barrier();
-      slice(1, buf ^ 1, 0, 0, 0, 0, 0);
+      slice(1, buf ^ 1, 0, 0, 0, nothing);
+      buf ^= 1;
+    }
+    for (; step < steps; ++step) {   // the next step is the row's end, or past it
+      slice(0, buf, 1, 0, 0, nothing);
+      slice(1, buf, 2, 0, 0, nothing);
+      slice(0, buf, 3, 0, 0, nothing);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        B::put(lds, buf ^ 1, i, b.load(step + 1, i));
+        issue_fence();
+      }
+      lds_barrier();
+      slice(1, buf ^ 1, 0, 0, 0, nothing);
+      buf ^= 1;
     }
   }
 
@@ -455,7 +485,7 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
     const v16i* part[MN];
 #pragma unroll
     for (int i = 0; i < MN; ++i) part[i] = &acc[i][j];
-    store_rows<MN, kVec, kBf>(part, o, turn, lds.sa[wt + 32 * j + (threadIdx.x & 31)],
+    store_rows<MN, kVec, kBf>(part, o, turn, lds.sa[wt + 32 * j + (lane_id() & 31)],
                               wt + 32 * j, wn, b.trows, (int)g.N);
   }
 }
@@ -740,7 +770,8 @@ bool rows_aligned(const MatmulArgs& a) {
 // N=8192 K=8192: 450 us with 256 x 256, 560 us with 128 x 128). Rows on any
 // byte cost more for each load, so large tiles pay sooner (K=4095 N=4096 T=256:
 // 22 us with 32 x 64, 46 with 128 x 128; 8192 x 8192: 742 with 256 x 256, 881
-// with 128 x 128, 1199 with 128 x 64).
+// with 128 x 128, 1199 with 128 x 64; with the loads spread over the slices
+// 675 with 256 x 256).
 enum Tile { k256x256, k128x128, k128x64, k64x64, k32x64, k32x32, kTiles };
 
 Tile choose_tile(const MatmulArgs& a, bool direct) {
