@@ -154,18 +154,31 @@ __device__ __forceinline__ void store_turned(int thread, int count, const int8_t
   constexpr int sz = kBf ? 2 : 4, kRow = kTurnRow<MN, kBf>;
   constexpr int kRun = kVec ? 16 / sz : 1;         // elements of a store
   constexpr int kStores = 32 * MN / kRun;          // of a row
-#pragma unroll 4
-  for (int e = thread; e < count * kStores; e += kThreads) {
-    const int r = e / kStores, c = e % kStores * kRun;
-    const int8_t* from = turn + r * kRow + c * sz;
-    const bool ok = t + r < rows && n + c < o.cols;
-    const uint32_t off = ok ? (uint32_t)((t + r) * N + n + c) * (uint32_t)sz : kOOB;
+  const auto put = [&](const int8_t* from, uint32_t off) {
     if constexpr (kVec)
       __builtin_amdgcn_raw_buffer_store_b128(*(const v4i*)from, o.y, off, 0, kStream);
     else if constexpr (kBf)
       __builtin_amdgcn_raw_buffer_store_b16(*(const uint16_t*)from, o.y, off, 0, 0);
     else
       __builtin_amdgcn_raw_buffer_store_b32(*(const uint32_t*)from, o.y, off, 0, 0);
+  };
+  if constexpr (kThreads % kStores == 0) {   // a thread keeps its columns
+    constexpr int kPass = kThreads / kStores;
+    const int c = thread % kStores * kRun;
+    int r = thread / kStores;
+    const bool in_cols = n + c < o.cols;
+    uint32_t off = (uint32_t)((t + r) * N + n + c) * (uint32_t)sz;
+    const int8_t* from = turn + r * kRow + c * sz;
+#pragma unroll 4
+    for (; r < count; r += kPass, off += (uint32_t)(kPass * N * sz), from += kPass * kRow)
+      put(from, in_cols && t + r < rows ? off : kOOB);
+  } else {
+#pragma unroll 4
+    for (int e = thread; e < count * kStores; e += kThreads) {
+      const int r = e / kStores, c = e % kStores * kRun;
+      const bool ok = t + r < rows && n + c < o.cols;
+      put(turn + r * kRow + c * sz, ok ? (uint32_t)((t + r) * N + n + c) * (uint32_t)sz : kOOB);
+    }
   }
 }
 
