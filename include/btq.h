@@ -22,7 +22,10 @@
  * between devices is the identity: the buffers written by btq_compress_pack
  * are the ones read by btq_decompress_reduce. The other calls widen the path:
  * a bf16-output receiver, other readings of the selection step and a packed
- * row pitch.
+ * row pitch. The last group covers what stands next to the path in a
+ * transformer: the 8-bit linear layer whose partial sums the sender takes
+ * (btq_quantize_rows, btq_int8_matmul, btq_int8_linear) and the norms that
+ * read the receiver's sum (btq_block_norm).
  *
  * Conventions shared by every call
  *  - Tensor pointers are DEVICE pointers (hipMalloc'd or from PyTorch) to
@@ -80,8 +83,8 @@ extern "C" {
 
 typedef enum {
   BTQ_OK = 0,
-  BTQ_ERR_ARG = -1,        /* null pointer, or momentum outside [0,1) / NaN    */
-  BTQ_ERR_SHAPE = -2,      /* P, T, H, k or the pitch out of range              */
+  BTQ_ERR_ARG = -1,        /* null pointer, unknown option, factor out of range */
+  BTQ_ERR_SHAPE = -2,      /* a size, a stride or the pitch out of range        */
   BTQ_ERR_ALIGN = -3,      /* pointer not aligned to its element type           */
   BTQ_ERR_WORKSPACE = -4,  /* workspace smaller than the *_workspace_bytes size */
   BTQ_ERR_HIP = -5,        /* a HIP call failed (hipGetLastError, cleared)      */
@@ -408,8 +411,9 @@ int btq_quantize_rows(const void *x, int x_type, int64_t x_shard, int64_t x_pitc
  *   w        i8 [P,N,K], w_scale fp32 [P,N]  in, contiguous
  *   bias     fp32 [P,N]  in, or NULL
  *   y        fp32 or bf16 [P,T,N]  out, contiguous
- * Fast kernels run when a, w and their strides are multiples of 16 (so K is);
- * other layouts are as exact and slower.
+ * The fastest kernels run when a, w and their strides are multiples of 16 (so K
+ * is, and weights are best stored so); rows on any other byte are as exact and
+ * take up to 1.6 times as long.
  */
 int btq_int8_matmul(const int8_t *a, int64_t a_shard, int64_t a_pitch,
                     const float *a_scale, int64_t as_shard,
