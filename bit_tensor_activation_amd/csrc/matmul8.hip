@@ -202,18 +202,19 @@ __device__ __forceinline__ void store_rows(const v16i* const (&acc)[MN], const O
   wave_lds_sync();
 }
 
-// ---- tile kernel: K a multiple of 16, rows on 16-byte boundaries ----
+// ---- tile kernel ----
 //
-// A block of 4 waves (2x2) makes 64*MN channels x 64*MT tokens; a wave
-// 32*MN x 32*MT in 32x32x32 products. k goes in steps of 128 bytes, two steps
-// in LDS: one is read while the next one lands by direct loads to LDS. In LDS
-// a row's eight 16-byte chunks are permuted by c ^ (row & 7) (the loads
-// permute their addresses: a direct load writes its lanes in a line), so the
-// 8 rows that one LDS cycle serves lie in different banks.
+// A block of 4 waves (WN x WT) makes RN channels x RT tokens; a wave 32*MN x
+// 32*MT of them in 32x32x32 products. k goes in steps of 128 bytes, S of them in
+// LDS: one is read while the others land by direct loads to LDS. In LDS a row's
+// eight 16-byte chunks are permuted by c ^ (row/2 & 7) (the loads permute their
+// addresses: a direct load writes its lanes in a line), so the 16 rows that one
+// LDS cycle serves lie in different banks (two rows share the 64 banks; with
+// c ^ (row & 7) half of the reads' cycles were conflicts).
 // A step is 4 slices of 32 bytes. The next slice's operands are read while
 // the matrix cores run the present one. The barrier stands before the last
-// slice: its operands are in registers by then, so the buffer is free for the
-// step after the next, and its products hide the first reads of the next step.
+// slice: its operands are in registers by then, so the buffer is free for a
+// later step, and its products hide the first reads of the next step.
 // Large products are bound by the chip's power: 8192^3 takes 434 us, 2.5 POPS,
 // the matrix cores busy 0.71 of the cycles at 1.67 GHz; products of few tokens
 // by the weights' bytes (T=64 N=8192 P=8 K=4096: 58 us, 4.9 TB/s); short sums by
@@ -265,6 +266,7 @@ template <int kLoads, bool kLds>
 __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt((kLoads & 15) | (kLoads >> 4) << 14 | 7 << 4 | (kLds ? 0 : 15) << 8);
 }
+
 // A block's share of the product: RN channels x RT tokens of shard p, and the
 // loads of its operands, 256 threads together, into S buffers of LDS.
 // kNt: the channels' loads stream past the caches. kCodes: the block makes the
@@ -375,7 +377,6 @@ struct Block {
   }
 };
 
-//
 // kLoad: kDirect or kDirectNt where K and every row lie on 16 bytes. kAnyByte
 // (S = 2): the next step's operands wait in registers while this one is
 // multiplied.
@@ -423,7 +424,7 @@ __global__ __launch_bounds__(256, MN* MT == 16 ? 1 : 2) void matmul_tile_kernel(
   if constexpr (kLoad != kAnyByte) {
     // half of a step's loads go out right after the barrier that frees their
     // buffer, the other half a slice later: together they would hold up the
-    // products that follow
+    // products that follow (8192^3: 2319 against 2439 TOPS)
     constexpr int kEarly = kLoads / 2;
 #pragma unroll
     for (int q = 0; q < S; ++q)
