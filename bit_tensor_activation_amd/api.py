@@ -397,8 +397,10 @@ def _stream_of(idx: int, stream):
 
 
 def _empty(shape, dtype, idx: int, ctx) -> torch.Tensor:
-    with ctx or contextlib.nullcontext():
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", idx))
+    if ctx is None:
+        return torch.empty(shape, dtype=dtype, device=idx)
+    with ctx:
+        return torch.empty(shape, dtype=dtype, device=idx)
 
 
 def _rows(x: torch.Tensor, name: str, dtypes):
