@@ -123,3 +123,31 @@ def test_large_constant_rows(dt):
                                  float(np.float32(1e-6)), float(np.float32(1e-6)))
         # r' carries one rounding into n: of the row's norm, sqrt(H) at most
         within(n, n64, en + 4 * U * np.sqrt(H) * np.abs(host(w)), F32, "n")
+
+
+@pytest.mark.parametrize("H", [40000, (1 << 22) + 3])
+def test_long_rows_keep_their_sums(H):
+    # Rows past the register kernels. Near-constant values make every rounding
+    # of a running fp32 sum fall the same way: H/256 of them one after another
+    # would be off by far more than the bound, which allows the sums only the
+    # rounding of their result. n = v * rstd: var + eps, its root, the
+    # quotient and the product round once each, and so does var (half of that in
+    # rstd): 4.5 roundings, and the first order of it. A layer norm's mean
+    # rounds too: the deviations move by U*|mean|, their own rounding by U*|d|.
+    say(f"case: block norm, long rows H={H}")
+    v = (0.7 + 0.01 * rand(H, 2, H)).to(F32)
+    x = host(v)
+    _, n = B.btq_block_norm(None, v, pre="rms", n_dtype=F32)
+    want = x / np.sqrt((x * x).mean(-1, keepdims=True) + float(np.float32(1e-6)))
+    off = np.abs(host(n) - want)
+    assert (off <= 6 * U * np.abs(want)).all(), f"rms: off by {np.max(off / np.abs(want)) / U} u"
+    _, n = B.btq_block_norm(None, v, pre="layer", n_dtype=F32)
+    mean = x.mean(-1, keepdims=True)
+    d = x - mean
+    rstd = 1 / np.sqrt((d * d).mean(-1, keepdims=True) + float(np.float32(1e-6)))
+    off = np.abs(host(n) - d * rstd)
+    tol = (2 * U * np.abs(mean) + 8 * U * np.abs(d)) * rstd
+    assert (off <= tol).all(), f"layer: off by {np.max(off)}, at most {np.max(tol)} allowed"
+    # the same through the first norm, whose weights are absent
+    _, n2 = B.btq_block_norm(v, torch.zeros_like(v), post="layer", pre="none", n_dtype=F32)
+    assert torch.equal(n2, n)
