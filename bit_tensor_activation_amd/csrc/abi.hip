@@ -336,8 +336,12 @@ int check_matmul(int64_t as_shard, const int8_t* w, const float* w_scale, const 
 }
 
 // Workspace of btq_int8_linear: the codes with rows padded to 16 bytes, then
-// the scales.
+// the scales. Its bytes stay inside 2^62 too (short rows grow up to 20 times).
 int64_t code_pitch(int64_t K) { return (K + 15) / 16 * 16; }
+int64_t code_row_bytes(int64_t K) { return code_pitch(K) + (int64_t)sizeof(float); }
+int check_linear_workspace(int64_t P, int64_t T, int64_t K) {
+  return K < 1 || K > kMaxSumK ? BTQ_ERR_SHAPE : check_dims(P, T, code_row_bytes(K), 0);
+}
 
 }  // namespace
 
@@ -369,8 +373,8 @@ int btq_int8_matmul(const int8_t* a, int64_t a_shard, int64_t a_pitch, const flo
 }
 
 size_t btq_int8_linear_workspace_bytes(int64_t P, int64_t T, int64_t K) {
-  if (check_dims(P, T, K, 0) != BTQ_OK || K > kMaxSumK) return 0;
-  return (size_t)(P * T * (code_pitch(K) + (int64_t)sizeof(float)));
+  if (check_linear_workspace(P, T, K) != BTQ_OK) return 0;
+  return (size_t)(P * T * code_row_bytes(K));
 }
 
 int btq_int8_linear(const void* x, int x_type, int64_t x_shard, int64_t x_pitch, const int8_t* w,
@@ -379,6 +383,7 @@ int btq_int8_linear(const void* x, int x_type, int64_t x_shard, int64_t x_pitch,
                     void* stream) {
   int st = check_matmul(0, w, w_scale, bias, P, T, N, K, y, y_type);
   if (st == BTQ_OK) st = check_strides(P, T, x_shard, x_pitch);
+  if (st == BTQ_OK) st = check_linear_workspace(P, T, K);
   if (st != BTQ_OK) return st;
   if (!value_type(x_type) || (T > 0 && (!x || !workspace))) return BTQ_ERR_ARG;
   if (!aligned(x, value_align(x_type)) || !aligned(workspace, 16)) return BTQ_ERR_ALIGN;

@@ -433,7 +433,9 @@ int btq_int8_linear(const void *x, int x_type, int64_t x_shard, int64_t x_pitch,
                     int64_t P, int64_t T, int64_t N, int64_t K,
                     void *y, int y_type, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes for btq_int8_linear (0 for invalid sizes or T == 0). */
+/* Workspace bytes for btq_int8_linear: P*T*((K rounded up to 16) + 4). 0 for
+ * T == 0 and for sizes that the call refuses, P*T rows of that many bytes past
+ * 2^62 among them. */
 size_t btq_int8_linear_workspace_bytes(int64_t P, int64_t T, int64_t K);
 
 typedef enum { BTQ_NORM_NONE = 0, BTQ_NORM_RMS = 1, BTQ_NORM_LAYER = 2 } btq_norm;
