@@ -83,18 +83,19 @@ _lib = None
 def load() -> ctypes.CDLL:
     """The loaded libbtq (once per process)."""
     global _lib
-    with _lock:
-        if _lib is None:
-            if not os.path.exists(LIB_PATH):
-                raise RuntimeError(
-                    f"{LIB_PATH} is missing: build the HIP library first "
-                    "(python -m bit_tensor_activation_amd.build)")
-            lib = ctypes.CDLL(LIB_PATH)
-            for name, (res, args) in SIGNATURES.items():
-                fn = getattr(lib, name)
-                fn.restype = res
-                fn.argtypes = args
-            _lib = lib
+    if _lib is None:   # set last below: what is there is complete
+        with _lock:
+            if _lib is None:
+                if not os.path.exists(LIB_PATH):
+                    raise RuntimeError(
+                        f"{LIB_PATH} is missing: build the HIP library first "
+                        "(python -m bit_tensor_activation_amd.build)")
+                lib = ctypes.CDLL(LIB_PATH)
+                for name, (res, args) in SIGNATURES.items():
+                    fn = getattr(lib, name)
+                    fn.restype = res
+                    fn.argtypes = args
+                _lib = lib
     return _lib
 
 

@@ -372,7 +372,8 @@ _NORMS = {"none": _lib.BTQ_NORM_NONE, "rms": _lib.BTQ_NORM_RMS, "layer": _lib.BT
 
 # The calls below can be shorter on the GPU than the host's part of them, so
 # they check tensors by the quick way first (the device by its index, messages
-# only when something is wrong) and enter a stream's context only to allocate.
+# only when something is wrong), enter a stream's context only to allocate and a
+# device's only where another one is current.
 
 def _index(x: torch.Tensor) -> int:
     idx = x.get_device()
@@ -401,6 +402,18 @@ def _empty(shape, dtype, idx: int, ctx) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=idx)
     with ctx:
         return torch.empty(shape, dtype=dtype, device=idx)
+
+
+def _run(fn, idx: int, *args) -> None:
+    """Calls the library with device `idx` current. (A default stream's handle
+    is 0 on every device: the launch would go to whichever is current.)"""
+    if idx == torch._C._cuda_getDevice():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(idx):
+            st = fn(*args)
+    if st:
+        _lib.check(st, fn.__name__)
 
 
 def _rows(x: torch.Tensor, name: str, dtypes):
@@ -433,10 +446,9 @@ def btq_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
         q = _empty(shape, torch.int8, idx, ctx)
     if scale is None:
         scale = _empty(shape[:-1], torch.float32, idx, ctx)
-    st = _lib.load().btq_quantize_rows(
-        x.data_ptr(), _T[x.dtype], shard, pitch, 1 if P is None else P, T, K,
-        _at(q, "q", _I8, shape, idx), _at(scale, "scale", _F32, shape[:-1], idx), sh)
-    _lib.check(st, "btq_quantize_rows")
+    _run(_lib.load().btq_quantize_rows, idx, x.data_ptr(), _T[x.dtype], shard, pitch,
+         1 if P is None else P, T, K, _at(q, "q", _I8, shape, idx),
+         _at(scale, "scale", _F32, shape[:-1], idx), sh)
     return q, scale
 
 
@@ -473,9 +485,8 @@ def btq_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
     P, N, wp, sp, bp, y, yp = _product_args(x_p, T, K, w, w_scale, bias, y,
                                             torch.int16 if bf16 else torch.float32, idx, ctx)
     asp = _at(a_scale, "a_scale", _F32, (T,) if x_p is None else (P, T), idx)
-    st = _lib.load().btq_int8_matmul(a.data_ptr(), shard, pitch, asp, 0 if x_p is None else T, wp,
-                                     sp, bp, P, T, N, K, yp, _T[y.dtype], sh)
-    _lib.check(st, "btq_int8_matmul")
+    _run(_lib.load().btq_int8_matmul, idx, a.data_ptr(), shard, pitch, asp,
+         0 if x_p is None else T, wp, sp, bp, P, T, N, K, yp, _T[y.dtype], sh)
     return y
 
 
@@ -503,10 +514,8 @@ def btq_int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
         workspace = _empty(btq_int8_linear_workspace_bytes(P, T, K), torch.uint8, idx, ctx)
     elif workspace.get_device() != idx or not workspace.is_contiguous():
         raise ValueError(f"workspace: must be contiguous and on {x.device}")
-    st = _lib.load().btq_int8_linear(
-        x.data_ptr(), _T[x.dtype], shard, pitch, wp, sp, bp, P, T, N, K, yp, _T[y.dtype],
-        workspace.data_ptr(), workspace.nbytes, sh)
-    _lib.check(st, "btq_int8_linear")
+    _run(_lib.load().btq_int8_linear, idx, x.data_ptr(), _T[x.dtype], shard, pitch, wp, sp, bp,
+         P, T, N, K, yp, _T[y.dtype], workspace.data_ptr(), workspace.nbytes, sh)
     return y
 
 
@@ -564,12 +573,9 @@ def btq_block_norm(y: Optional[torch.Tensor], residual: torch.Tensor, post: str 
         n_scale = _empty((T,), torch.float32, idx, ctx)
     if n_scale is not None:
         sp = _at(n_scale, "n_scale", _F32, (T,), idx)
-    st = _lib.load().btq_block_norm(
-        yp, yt or 0, rp, _T[r_dtype], T, H, _NORMS[post], pw, pb,
-        eps if post_eps is None else post_eps, gp, gt or 0, gr, alpha, _NORMS[pre], nw, nb, eps,
-        op, np_, _T[n.dtype], sp, sh)
-    if st:
-        _lib.check(st, "btq_block_norm")
+    _run(_lib.load().btq_block_norm, idx, yp, yt or 0, rp, _T[r_dtype], T, H, _NORMS[post], pw, pb,
+         eps if post_eps is None else post_eps, gp, gt or 0, gr, alpha, _NORMS[pre], nw, nb, eps,
+         op, np_, _T[n.dtype], sp, sh)
     return (residual_out, n, n_scale) if int8 else (residual_out, n)
 
 
