@@ -40,9 +40,9 @@ __device__ __forceinline__ float scaled(int sum, float sa, float sw, float b) {
 
 // ---- general kernel: any size, stride and alignment ----
 //
-// For k below 16, and rows or strides too large for 32-bit offsets: 64 tokens x
-// 64 channels a block, 4 waves of 32x32, 64 bytes of k a step through LDS (rows
-// padded to 80 bytes).
+// For k below 16, rows or strides too large for 32-bit offsets, and more tiles
+// than a grid holds: 64 tokens x 64 channels a block, 4 waves of 32x32, 64 bytes
+// of k a step through LDS (rows padded to 80 bytes).
 constexpr int kGenTile = 64, kGenK = 64, kGenRow = 80;
 
 __global__ __launch_bounds__(256) void matmul_general_kernel(MatmulArgs g, int64_t tiles_t,
@@ -736,11 +736,22 @@ __global__ __launch_bounds__(256, 2) void linear_small_kernel(MatmulArgs g, cons
 }
 
 constexpr int64_t kMaxBlocks = int64_t(1) << 20;
+// Blocks of 256 threads that a grid may have, one for each tile.
+constexpr int64_t kMaxTiles = int64_t(1) << 23;
+
+hipError_t launch_general(const MatmulArgs& a, hipStream_t s) {
+  const int64_t tt = (a.T + kGenTile - 1) / kGenTile, tn = (a.N + kGenTile - 1) / kGenTile;
+  const int64_t tiles = a.P * tt * tn;
+  matmul_general_kernel<<<dim3((unsigned)(tiles < kMaxBlocks ? tiles : kMaxBlocks)), 256, 0, s>>>(
+      a, tt, tn, tiles);
+  return hipGetLastError();
+}
 
 // A kernel over RN x RT tiles; kernel(vec, bf16, grid, tiles of t, of n, of all).
 template <int RN, int RT, typename F>
-hipError_t launch_tiled(const MatmulArgs& a, F kernel) {
+hipError_t launch_tiled(const MatmulArgs& a, hipStream_t s, F kernel) {
   const int64_t tt = (a.T + RT - 1) / RT, tn = (a.N + RN - 1) / RN, n = a.P * tt * tn;
+  if (n >= kMaxTiles) return launch_general(a, s);
   const bool bf = a.y_type == kBf16, vec = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
   const auto run = [&](auto v, auto b) { kernel(v, b, dim3((unsigned)n), (int)tt, (int)tn, (int)n); };
   constexpr std::true_type yes;
@@ -755,7 +766,7 @@ hipError_t launch_tiled(const MatmulArgs& a, F kernel) {
 template <int WN, int WT, int MN, int MT, int S, Load kLoad = kDirect>
 hipError_t launch_tiles(const MatmulArgs& a, hipStream_t s) {
   return launch_tiled<32 * MN * WN, 32 * MT * WT>(
-      a, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
+      a, s, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
         matmul_tile_kernel<WN, WT, MN, MT, S, kLoad, decltype(v)::value, decltype(b)::value>
             <<<grid, 256, 0, s>>>(a, tt, tn, n);
       });
@@ -763,17 +774,17 @@ hipError_t launch_tiles(const MatmulArgs& a, hipStream_t s) {
 
 template <int MN, int MT, int S, Load kLoad = kDirect>
 hipError_t launch_split(const MatmulArgs& a, hipStream_t s) {
-  return launch_tiled<32 * MN, 32 * MT>(a, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
-    matmul_split_kernel<MN, MT, S, kLoad, decltype(v)::value, decltype(b)::value>
-        <<<grid, 256, 0, s>>>(a, tt, tn, n);
-  });
+  return launch_tiled<32 * MN, 32 * MT>(
+      a, s, [&](auto v, auto b, dim3 grid, int tt, int tn, int n) {
+        matmul_split_kernel<MN, MT, S, kLoad, decltype(v)::value, decltype(b)::value>
+            <<<grid, 256, 0, s>>>(a, tt, tn, n);
+      });
 }
 
 // A block's rows of a, w and y must each span less than 2^31 bytes (there are
-// 256 of them at most), and its blocks must fit a grid.
+// 256 of them at most).
 bool spans_ok(const MatmulArgs& a) {
-  const int64_t blocks = a.P * ((a.N + 31) / 32) * ((a.T + 31) / 32);
-  return a.a_pitch < (int64_t(1) << 22) && a.N < (int64_t(1) << 20) && blocks < kMaxBlocks * 8;
+  return a.a_pitch < (int64_t(1) << 22) && a.N < (int64_t(1) << 20);
 }
 
 // Direct 16-byte loads need every row on a 16-byte boundary.
@@ -907,11 +918,7 @@ hipError_t launch_int8_matmul(const MatmulArgs& a, hipStream_t s) {
       default: return launch_split<1, 1, 4, kAnyByte>(a, s);
     }
   }
-  const int64_t tt = (a.T + kGenTile - 1) / kGenTile, tn = (a.N + kGenTile - 1) / kGenTile;
-  const int64_t tiles = a.P * tt * tn;
-  matmul_general_kernel<<<dim3((unsigned)(tiles < kMaxBlocks ? tiles : kMaxBlocks)), 256, 0, s>>>(
-      a, tt, tn, tiles);
-  return hipGetLastError();
+  return launch_general(a, s);
 }
 
 bool small_linear_ok(const void* x, int x_type, int64_t x_shard, int64_t x_pitch,
