@@ -151,3 +151,53 @@ def test_long_rows_keep_their_sums(H):
     # the same through the first norm, whose weights are absent
     _, n2 = B.btq_block_norm(v, torch.zeros_like(v), post="layer", pre="none", n_dtype=F32)
     assert torch.equal(n2, n)
+
+
+@pytest.mark.parametrize("H", [72, 1001, 5000, 8192, 33000])
+def test_second_norm_weight_or_bias_alone(H):
+    T = 3
+    y, r = rand(H, T, H) + 2.0, rand(H + 1, T, H) * 0.5
+    w, b = 1 + 0.3 * rand(H + 2, H), rand(H + 3, H)
+    eps = float(np.float32(1e-6))
+    for nw, nb in ((None, None), (w, None), (None, b), (w, b)):
+        say(f"case: block norm layer/layer H={H} pre weight={nw is not None} "
+            f"bias={nb is not None}")
+        r64, er, n64, en = plain(host(y), host(r), "layer", None, None, None, 1.0, "layer",
+                                 host(nw), host(nb), eps, eps)
+        assert np.max(en) < 1e-2
+        for n_dt in (F32, I8):
+            out = B.btq_block_norm(y, r, post="layer", pre="layer", pre_weight=nw, pre_bias=nb,
+                                   n_dtype=n_dt)
+            within(out[0], r64, er, F32, "residual")
+            if n_dt == I8:
+                check_int8(out[1], out[2], n64, en, "pre weight or bias alone")
+            else:
+                within(out[1], n64, en, F32, "n")
+
+
+@pytest.mark.parametrize("r_dt", [F32, BF16])
+@pytest.mark.parametrize("H", [200, 1000, 1001, 1024, 2047, 4096, 5000, 5001, 8192, 20000, 33000])
+def test_rows_do_not_depend_on_the_batch(H, r_dt):
+    # a row alone, in a few, in many: bit for bit, within a kernel variant
+    # (4096 < H <= 8192 changes its lanes at T = 256)
+    T = 300
+    y, r = rand(H, T, H) + 1.0, rand(H + 1, T, H).to(r_dt)
+    w = 1 + 0.3 * rand(H + 2, H)
+
+    def run(rows, n_dt):
+        return B.btq_block_norm(y[rows].contiguous(), r[rows].contiguous(), post="layer",
+                                post_weight=w, pre="rms", n_dtype=n_dt)
+    for n_dt in (F32, BF16, I8):
+        say(f"case: block norm rows in other batches H={H} {r_dt} {n_dt}")
+        if 4096 < H <= 8192:
+            few, many = (slice(0, 256), (slice(0, 1), slice(0, 7), slice(100, 137))), (
+                slice(0, 300), (slice(0, 257), slice(20, 290)))
+            groups = (few, many)
+        else:
+            groups = ((slice(0, 300), (slice(0, 1), slice(0, 7), slice(100, 137), slice(1, 300))),)
+        for whole, parts in groups:
+            ref = run(whole, n_dt)
+            for p in parts:
+                at = slice(p.start - whole.start, p.stop - whole.start)
+                for a, c in zip(run(p, n_dt), ref):
+                    assert torch.equal(a, c[at]), (p, n_dt)
