@@ -632,11 +632,15 @@ __global__ __launch_bounds__(256, 2) void matmul_split_kernel(MatmulArgs g, int 
 // above. A wave reads 16/NVEC rows of x, all at once (NVEC vectors of 8 a lane),
 // takes their largest values and leaves codes and scales in LDS, while the first
 // steps of the weights land. Every block of channels quantizes its tokens
-// again, from L2; with at most two blocks a CU that costs less than the launch
-// (P=8 T=1 N=1024 K=1024: 4.1 us against 5.7 for the two kernels in a graph;
-// P=3 T=77 N=999 K=1000: 7.6 against 9.1, and 10.0 against 12.9 called from
-// Python; only 32 rows of short k lose, T=32 N=4096 K=512: 6.1 against 5.5 in a
-// graph).
+// again, from L2. Both sides of the rule (at most two blocks a CU), one launch
+// against two, us: one call after another the host's part counts and one launch
+// always takes less (P=8 T=1 N=1024 K=1024: 7.4 against 10.0; T=32 N=4096 K=512:
+// 7.3 against 10.0; P=8 T=32 N=2048 K=512: 8.1 against 10.1). In a graph it takes
+// less up to about 24 rows a block (P=8 T=1 N=1024 K=1024: 4.1 against 5.7; P=3
+// T=77 N=999 K=1000: 7.7 against 8.9; T=24 N=4096 K=512: 5.5 with either) and
+// more where a block quantizes 32 rows of short k (T=32 N=4096 K=512: 6.3 against
+// 5.5; with two blocks a CU, P=8 T=32 N=2048 K=512, 8.3 against 6.3; P=2 T=16
+// N=8192 K=2048, 16 rows, 9.7 against 8.6).
 template <Load kLoad, int NVEC, bool kBf>
 __global__ __launch_bounds__(256, 2) void linear_small_kernel(MatmulArgs g, const uint16_t* x,
                                                               int64_t x_shard, int64_t x_pitch,
