@@ -201,3 +201,22 @@ def test_rows_do_not_depend_on_the_batch(H, r_dt):
                 at = slice(p.start - whole.start, p.stop - whole.start)
                 for a, c in zip(run(p, n_dt), ref):
                     assert torch.equal(a, c[at]), (p, n_dt)
+
+
+@pytest.mark.parametrize("T,H", [((1 << 22) + 5, 8), ((1 << 20) + 7, 1032)])
+def test_more_rows_than_blocks(T, H):
+    # a block then takes several rows, one after another, and the sums of one
+    # must not meet the next one's
+    say(f"case: block norm and codes of T={T} H={H}")
+    y = torch.empty((T, H), dtype=BF16, device=DEV).normal_(1.0, 1.0)
+    r = torch.empty((T, H), dtype=BF16, device=DEV).normal_()
+    kw = dict(post="layer", pre="layer", n_dtype=I8)
+    whole = B.btq_block_norm(y, r, **kw)
+    codes = B.btq_quantize_rows(y)
+    for sl in (slice(0, 9), slice((1 << 20) - 3, (1 << 20) + 7), slice(T - 1040, T)):
+        for a, b in zip(B.btq_block_norm(y[sl].contiguous(), r[sl].contiguous(), **kw), whole):
+            assert torch.equal(a, b[sl])
+        for a, b in zip(B.btq_quantize_rows(y[sl]), codes):
+            assert torch.equal(a, b[sl])
+    # every row, by its codes' scale: the largest |code| of a row is 127
+    assert (whole[1].abs().amax(-1) == 127).all() and torch.isfinite(whole[2]).all()
