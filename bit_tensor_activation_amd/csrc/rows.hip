@@ -141,8 +141,8 @@ __global__ __launch_bounds__(kGenThreads) void rows_general_kernel(
 // moves and (G > 64) one LDS exchange. A layer norm takes its variance from
 // the deviations in a second sum, so a large mean costs no precision.
 // Bound by HBM: the norm at T=16384 H=8192 (fp32 y, bf16 residual and n, 1.34 GB)
-// takes 234 us, 5.7 TB/s; at T=2048 H=4096 16 us; codes of 32768 x 8192 bf16
-// 140 us, 5.8 TB/s. One row alone takes 4.3 us, most of it the launch and the
+// takes 228 us, 5.9 TB/s; at T=2048 H=4096 16 us; codes of 32768 x 8192 bf16
+// 141 us, 5.7 TB/s. One row alone takes 4.5 us, most of it the launch and the
 // two sums' latency. Row lengths choose G: a row's lanes hold at most 32
 // elements each (16 would halve the loads in flight, 64 spill), and more than 64
 // lanes pay an LDS exchange.

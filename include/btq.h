@@ -364,7 +364,8 @@ int64_t btq_packed_pitch(int64_t H, int64_t k);
  * Extra conventions of these calls
  *  - Value types are BTQ_T_F32, BTQ_T_BF16 (raw 16-bit patterns) and, for
  *    norm outputs, BTQ_T_INT8. Any other value returns BTQ_ERR_ARG.
- *  - Sums, statistics and norms are fp32 (integer sums int32, exact). Each
+ *  - Sums, statistics and norms are fp32 (integer sums int32, exact; sums of
+ *    norm rows past 32768 fp64, rounded once). Each
  *    output is rounded once, to nearest even (codes: see the calls).
  *  - NaN and Inf are carried, not excluded: see each call.
  *  - T == 0 does nothing. Sizes: P <= 65535, H, N, K in [1, 2^30], and every
@@ -413,7 +414,8 @@ int btq_quantize_rows(const void *x, int x_type, int64_t x_shard, int64_t x_pitc
  *   y        fp32 or bf16 [P,T,N]  out, contiguous
  * The fastest kernels run when a, w and their strides are multiples of 16 (so K
  * is, and weights are best stored so); rows on any other byte are as exact and
- * take up to 1.6 times as long.
+ * take 1.1 to 2.2 times as long. K < 16, N >= 2^20 and a_pitch >= 2^22 run on
+ * a general kernel that is several times slower.
  */
 int btq_int8_matmul(const int8_t *a, int64_t a_shard, int64_t a_pitch,
                     const float *a_scale, int64_t as_shard,
@@ -466,7 +468,12 @@ typedef enum { BTQ_NORM_NONE = 0, BTQ_NORM_RMS = 1, BTQ_NORM_LAYER = 2 } btq_nor
  *                 btq_quantize_rows defines them (of the fp32 n), or NULL
  *   n_scale       fp32 [T] out, with int8 n only (else NULL)
  * eps >= 0 and finite, alpha finite. NaN and Inf spread to their row's
- * norms as the formulas give them.
+ * norms as the formulas give them. A row whose sum of squares passes the
+ * largest fp32 (values near 2^64/sqrt(H)) is normed as if it were Inf: to 0
+ * where its values are finite.
+ * The same call gives the same bits every time. A row's do not depend on the
+ * rows around it, except that for 4096 < H <= 8192 its sums are added in one
+ * order for T <= 256 and in another for more.
  */
 int btq_block_norm(const void *y, int y_type, const void *residual, int r_type,
                    int64_t T, int64_t H,
