@@ -16,9 +16,15 @@ from .api import (  # noqa: F401
     btq_decompress_reduce_bf16,
     btq_decompress_reduce_ex,
     btq_decompress_reduce_per_shard,
+    btq_head_norm_rope,
     btq_int8_linear,
     btq_int8_linear_workspace_bytes,
     btq_int8_matmul,
+    btq_kv_append,
+    btq_kv_attention,
+    btq_kv_attention_workspace_bytes,
+    btq_kv_block_bytes,
+    btq_kv_gather,
     btq_packed_pitch,
     btq_packed_row_bytes,
     btq_quantize_rows,

@@ -46,6 +46,16 @@ SIGNATURES = {
     "btq_int8_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "btq_block_norm": (_I, [_P, _I, _P, _I, _I64, _I64, _I, _P, _P, _F, _P, _I, _I64, _F, _I, _P,
                             _P, _F, _P, _P, _I, _P, _P]),
+    "btq_kv_block_bytes": (_I64, [_I64]),
+    "btq_head_norm_rope": (_I, [_P, _I] + [_I64] * 8 + [_I, _P, _I64, _I64, _P, _I64, _I64, _F, _P,
+                                _P, _P, _I64, _I64, _I, _P, _I, _I64, _I64, _I64, _P]),
+    "btq_kv_append": (_I, [_P, _P, _I] + [_I64] * 10 + [_P, _P, _I64, _P, _I64, _P, _P, _I64, _I64,
+                           _I, _P, _I64, _I64, _P]),
+    "btq_kv_gather": (_I, [_P, _P, _I64, _P, _I64, _P, _I64, _I64] + [_I64] * 4 + [_P, _P, _I]
+                      + [_I64] * 6 + [_P]),
+    "btq_kv_attention": (_I, [_P] + [_I64] * 8 + [_P, _P, _I64, _P, _I64, _P, _I64, _I64, _F, _I,
+                              _I64, _I64, _P, _I, _P, _P, _SZ, _P]),
+    "btq_kv_attention_workspace_bytes": (_SZ, [_I64] * 9),
     "btq_status_str": (_c.c_char_p, [_I]),
     "btq_version": (_c.c_char_p, []),
 }
@@ -75,6 +85,9 @@ BTQ_T_INT8 = 2
 BTQ_NORM_NONE = 0
 BTQ_NORM_RMS = 1
 BTQ_NORM_LAYER = 2
+
+BTQ_ROPE_HALF = 0
+BTQ_ROPE_PAIRS = 1
 
 _lock = threading.Lock()
 _lib = None

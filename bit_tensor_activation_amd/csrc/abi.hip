@@ -1,6 +1,6 @@
 // extern "C" entry points of libbtq: host-side argument checks, then the
-// launchers in calib.hip, select.hip, compress.hip, decompress.hip, rows.hip and
-// matmul8.hip.
+// launchers in calib.hip, select.hip, compress.hip, decompress.hip, rows.hip,
+// matmul8.hip, heads.hip, kvcache.hip and attention.hip.
 // The contract of each call is documented in include/btq.h.
 #include <math.h>
 
@@ -343,6 +343,85 @@ int check_linear_workspace(int64_t P, int64_t T, int64_t K) {
   return K < 1 || K > kMaxSumK ? BTQ_ERR_SHAPE : check_dims(P, T, code_row_bytes(K), 0);
 }
 
+// ---- heads, the paged cache and attention ----
+
+// Heads of one tensor: strides >= 0 whose largest element stays inside 2^62.
+int check_head_rows(int64_t P, int64_t T, int64_t H, int64_t D, int64_t shard, int64_t pitch,
+                    int64_t head) {
+  if (shard < 0 || pitch < 0 || head < 0) return BTQ_ERR_SHAPE;
+  const int64_t most = kMaxElems / 4;
+  if (P > 1 && shard > most / P) return BTQ_ERR_SHAPE;
+  if (T > 1 && pitch > most / T) return BTQ_ERR_SHAPE;
+  if (H > 1 && head > most / H) return BTQ_ERR_SHAPE;
+  return D > most ? BTQ_ERR_SHAPE : BTQ_OK;
+}
+
+int check_rope(const float* cos, const float* sin, int64_t rows, int64_t dim, int64_t D, int rope) {
+  if (rope != BTQ_ROPE_HALF && rope != BTQ_ROPE_PAIRS) return BTQ_ERR_ARG;
+  if (!cos != !sin) return BTQ_ERR_ARG;
+  if (!cos) return BTQ_OK;
+  if (rows < 1 || rows > (int64_t(1) << 31) || dim < 2 || dim % 2 != 0 || dim > D)
+    return BTQ_ERR_SHAPE;
+  return aligned(cos, 4) && aligned(sin, 4) ? BTQ_OK : BTQ_ERR_ALIGN;
+}
+
+bool head_features(int64_t D) { return D >= 32 && D <= 256 && D % 32 == 0; }
+constexpr int64_t kMaxPlaces = int64_t(1) << 30;
+constexpr int64_t kMaxKvBlocks = int64_t(1) << 23;   // thread blocks of a launch over places
+
+// Sizes of the batch, its cache and table.
+int check_kv_sizes(int64_t P, int64_t T, int64_t Hk, int64_t D, int64_t B, int64_t max_pages,
+                   int64_t page_size) {
+  if (P < 1 || P > kMaxP || T < 0 || T > kMaxPlaces || Hk < 1 || Hk > kMaxP || B < 0 ||
+      B > kMaxPlaces || !head_features(D))
+    return BTQ_ERR_SHAPE;
+  if (page_size < 32 || page_size > 65536 || (page_size & (page_size - 1)) != 0 || max_pages < 0 ||
+      max_pages > kMaxPlaces / page_size)
+    return BTQ_ERR_SHAPE;
+  // a grid over all places that the rows can touch
+  return (T / 32 + 2 * B) > kMaxKvBlocks / (P * Hk) ? BTQ_ERR_SHAPE : BTQ_OK;
+}
+
+int check_kv(int64_t P, int64_t T, int64_t Hk, int64_t D, const int32_t* starts,
+             const int32_t* lengths, int64_t B, const int32_t* table, int64_t max_pages,
+             const uint8_t* cache, int64_t pages, int64_t page_size) {
+  const int st = check_kv_sizes(P, T, Hk, D, B, max_pages, page_size);
+  if (st != BTQ_OK) return st;
+  if (pages < 1 || pages > kMaxElems / (P * Hk * (page_size / 32) * btq_kv_block_bytes(D)) ||
+      pages >= (int64_t(1) << 31))
+    return BTQ_ERR_SHAPE;
+  if (B > 0 && T > 0 && (!starts || !lengths || (max_pages > 0 && !table) || !cache))
+    return BTQ_ERR_ARG;
+  if (!aligned(starts, 4) || !aligned(lengths, 4) || !aligned(table, 4) || !aligned(cache, 16))
+    return BTQ_ERR_ALIGN;
+  return BTQ_OK;
+}
+
+btq::KvArgs kv_args(int64_t P, int64_t T, int64_t Hk, int64_t D, const int32_t* starts,
+                    const int32_t* lengths, int64_t B, const int32_t* table, int64_t max_pages,
+                    const uint8_t* cache, int64_t pages, int64_t page_size) {
+  int shift = 0;
+  while ((int64_t(32) << shift) < page_size) ++shift;
+  return {P, T, (int)B, (int)Hk, (int)D, starts, lengths, table, max_pages,
+          (int)(max_pages * page_size), const_cast<uint8_t*>(cache), pages, shift};
+}
+
+int check_attention_sizes(int64_t P, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
+                          int64_t max_pages, int64_t page_size, int64_t max_length) {
+  const int st = check_kv_sizes(P, T, Hk, D, B, max_pages, page_size);
+  if (st != BTQ_OK) return st;
+  if (Hq < 1 || Hq > kMaxP || Hq % Hk != 0 || max_length < 0 || max_length > kMaxPlaces)
+    return BTQ_ERR_SHAPE;
+  const int64_t G = Hq / Hk;
+  return T > kMaxPlaces / 2 / G ? BTQ_ERR_SHAPE : BTQ_OK;
+}
+btq::AttnPlan plan_attention(int64_t P, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
+                             int64_t max_pages, int64_t page_size, int64_t max_length) {
+  const int64_t places = max_pages * page_size;
+  return btq::attn_plan(P, T, (int)Hq, (int)Hk, (int)D, (int)B,
+                        max_length == 0 || max_length > places ? places : max_length);
+}
+
 }  // namespace
 
 int btq_quantize_rows(const void* x, int x_type, int64_t x_shard, int64_t x_pitch, int64_t P,
@@ -439,6 +518,127 @@ int btq_block_norm(const void* y, int y_type, const void* residual, int r_type, 
   return hip_status(btq::launch_block_norm(a, (hipStream_t)stream));
 }
 
+int64_t btq_kv_block_bytes(int64_t D) { return head_features(D) ? 32 * D + 256 : 0; }
+
+int btq_head_norm_rope(const void* x, int x_type, int64_t x_shard, int64_t x_pitch, int64_t x_head,
+                       int64_t P, int64_t T, int64_t q_heads, int64_t k_heads, int64_t D, int norm,
+                       const float* q_weight, int64_t qw_shard, int64_t qw_head,
+                       const float* k_weight, int64_t kw_shard, int64_t kw_head, float eps,
+                       const int32_t* positions, const float* cos_table, const float* sin_table,
+                       int64_t rope_rows, int64_t rope_dim, int rope, void* y, int y_type,
+                       int64_t y_shard, int64_t y_pitch, int64_t y_head, void* stream) {
+  if (q_heads < 0 || k_heads < 0 || q_heads > kMaxP || k_heads > kMaxP || q_heads + k_heads < 1 ||
+      D < 1 || D > 65536)
+    return BTQ_ERR_SHAPE;
+  const int64_t H = q_heads + k_heads;
+  int st = check_dims(P, T, H * D, 0);
+  if (st == BTQ_OK) st = check_head_rows(P, T, H, D, x_shard, x_pitch, x_head);
+  if (st == BTQ_OK) st = check_head_rows(P, T, H, D, y_shard, y_pitch, y_head);
+  if (st == BTQ_OK) st = check_head_rows(P, 1, H, D, qw_shard, 0, qw_head);
+  if (st == BTQ_OK) st = check_head_rows(P, 1, H, D, kw_shard, 0, kw_head);
+  if (st == BTQ_OK) st = check_rope(cos_table, sin_table, rope_rows, rope_dim, D, rope);
+  if (st != BTQ_OK) return st;
+  if (!value_type(x_type) || !value_type(y_type) || norm < BTQ_NORM_NONE || norm > BTQ_NORM_LAYER ||
+      !(eps >= 0.0f && eps < INFINITY))
+    return BTQ_ERR_ARG;
+  if (T > 0 && (!x || !y || (cos_table && !positions))) return BTQ_ERR_ARG;
+  if (!aligned(x, value_align(x_type)) || !aligned(y, value_align(y_type)) ||
+      !aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(positions, 4))
+    return BTQ_ERR_ALIGN;
+  if (T == 0) return BTQ_OK;
+  const btq::HeadArgs a = {
+      {const_cast<void*>(x), x_type, x_shard, x_pitch, x_head},
+      {y, y_type, y_shard, y_pitch, y_head},
+      P, T, (int)q_heads, (int)k_heads, (int)D, norm, q_weight, k_weight,
+      qw_shard, qw_head, kw_shard, kw_head, eps, positions,
+      {cos_table, sin_table, rope_rows, (int)rope_dim, rope}};
+  return hip_status(btq::launch_head_norm_rope(a, (hipStream_t)stream));
+}
+
+int btq_kv_append(const void* k, const void* v, int x_type, int64_t k_shard, int64_t k_pitch,
+                  int64_t k_head, int64_t v_shard, int64_t v_pitch, int64_t v_head, int64_t P,
+                  int64_t T, int64_t Hk, int64_t D, const int32_t* seq_starts,
+                  const int32_t* lengths, int64_t B, const int32_t* page_table, int64_t max_pages,
+                  const float* cos_table, const float* sin_table, int64_t rope_rows,
+                  int64_t rope_dim, int rope, uint8_t* cache, int64_t pages, int64_t page_size,
+                  void* stream) {
+  int st = check_kv(P, T, Hk, D, seq_starts, lengths, B, page_table, max_pages, cache, pages,
+                    page_size);
+  if (st == BTQ_OK) st = check_head_rows(P, T, Hk, D, k_shard, k_pitch, k_head);
+  if (st == BTQ_OK) st = check_head_rows(P, T, Hk, D, v_shard, v_pitch, v_head);
+  if (st == BTQ_OK) st = check_rope(cos_table, sin_table, rope_rows, rope_dim, D, rope);
+  if (st != BTQ_OK) return st;
+  if (!value_type(x_type) || (T > 0 && B > 0 && (!k || !v))) return BTQ_ERR_ARG;
+  if (!aligned(k, value_align(x_type)) || !aligned(v, value_align(x_type))) return BTQ_ERR_ALIGN;
+  if (T == 0 || B == 0) return BTQ_OK;
+  return hip_status(btq::launch_kv_append(
+      {const_cast<void*>(k), x_type, k_shard, k_pitch, k_head},
+      {const_cast<void*>(v), x_type, v_shard, v_pitch, v_head},
+      {cos_table, sin_table, rope_rows, (int)rope_dim, rope},
+      kv_args(P, T, Hk, D, seq_starts, lengths, B, page_table, max_pages, cache, pages, page_size),
+      (hipStream_t)stream));
+}
+
+int btq_kv_gather(const int32_t* seq_starts, const int32_t* lengths, int64_t B,
+                  const int32_t* page_table, int64_t max_pages, const uint8_t* cache,
+                  int64_t pages, int64_t page_size, int64_t P, int64_t T, int64_t Hk, int64_t D,
+                  void* k, void* v, int y_type, int64_t k_shard, int64_t k_pitch, int64_t k_head,
+                  int64_t v_shard, int64_t v_pitch, int64_t v_head, void* stream) {
+  int st = check_kv(P, T, Hk, D, seq_starts, lengths, B, page_table, max_pages, cache, pages,
+                    page_size);
+  if (st == BTQ_OK) st = check_head_rows(P, T, Hk, D, k_shard, k_pitch, k_head);
+  if (st == BTQ_OK) st = check_head_rows(P, T, Hk, D, v_shard, v_pitch, v_head);
+  if (st != BTQ_OK) return st;
+  if (!value_type(y_type) || (T > 0 && B > 0 && !k && !v)) return BTQ_ERR_ARG;
+  if (!aligned(k, value_align(y_type)) || !aligned(v, value_align(y_type))) return BTQ_ERR_ALIGN;
+  if (T == 0 || B == 0) return BTQ_OK;
+  return hip_status(btq::launch_kv_gather(
+      {k, y_type, k_shard, k_pitch, k_head}, {v, y_type, v_shard, v_pitch, v_head},
+      kv_args(P, T, Hk, D, seq_starts, lengths, B, page_table, max_pages, cache, pages, page_size),
+      (hipStream_t)stream));
+}
+
+size_t btq_kv_attention_workspace_bytes(int64_t P, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                                        int64_t B, int64_t max_pages, int64_t page_size,
+                                        int64_t max_length) {
+  if (check_attention_sizes(P, T, Hq, Hk, D, B, max_pages, page_size, max_length) != BTQ_OK ||
+      T == 0 || B == 0)
+    return 0;
+  return plan_attention(P, T, Hq, Hk, D, B, max_pages, page_size, max_length).workspace;
+}
+
+int btq_kv_attention(const void* q, int64_t q_shard, int64_t q_pitch, int64_t q_head, int64_t P,
+                     int64_t T, int64_t Hq, int64_t Hk, int64_t D, const int32_t* seq_starts,
+                     const int32_t* lengths, int64_t B, const int32_t* page_table,
+                     int64_t max_pages, const uint8_t* cache, int64_t pages, int64_t page_size,
+                     float scale, int causal, int64_t window, int64_t max_length, void* out,
+                     int out_type, float* lse, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  int st = check_attention_sizes(P, T, Hq, Hk, D, B, max_pages, page_size, max_length);
+  if (st == BTQ_OK)
+    st = check_kv(P, T, Hk, D, seq_starts, lengths, B, page_table, max_pages, cache, pages,
+                  page_size);
+  if (st == BTQ_OK) st = check_head_rows(P, T, Hq, D, q_shard, q_pitch, q_head);
+  if (st != BTQ_OK) return st;
+  if (window < 0) return BTQ_ERR_SHAPE;
+  if (!value_type(out_type) || !(scale > 0.0f && scale < INFINITY)) return BTQ_ERR_ARG;
+  if (T > 0 && B > 0 && (!q || !out)) return BTQ_ERR_ARG;
+  if (!aligned(q, 2) || !aligned(out, out_type == BTQ_T_F32 ? 8 : 4) || !aligned(lse, 4) ||
+      !aligned(workspace, 16))
+    return BTQ_ERR_ALIGN;
+  if (T == 0 || B == 0) return BTQ_OK;
+  const btq::AttnPlan plan = plan_attention(P, T, Hq, Hk, D, B, max_pages, page_size, max_length);
+  if (plan.workspace > 0 && !workspace) return BTQ_ERR_ARG;
+  if (workspace_bytes < plan.workspace) return BTQ_ERR_WORKSPACE;
+  const btq::HeadRows rows = {const_cast<void*>(q), BTQ_T_BF16, q_shard, q_pitch, q_head};
+  const btq::AttnArgs a = {
+      rows, btq::on16(rows),
+      kv_args(P, T, Hk, D, seq_starts, lengths, B, page_table, max_pages, cache, pages, page_size),
+      (int)Hq, (int)(Hq / Hk), scale * 1.4426950408889634f, causal != 0,
+      (int)(window > kMaxPlaces ? 0 : window), out, out_type, lse, (float*)workspace, plan.splits};
+  return hip_status(btq::launch_kv_attention(a, plan, (hipStream_t)stream));
+}
+
 const char* btq_status_str(int status) {
   switch (status) {
     case BTQ_OK: return "ok";
@@ -453,6 +653,6 @@ const char* btq_status_str(int status) {
   }
 }
 
-const char* btq_version(void) { return "0.4.0"; }
+const char* btq_version(void) { return "0.5.0"; }
 
 }  // extern "C"

@@ -287,4 +287,74 @@ struct NormArgs {
 };
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
 
+// Rows of heads: head h of token t of shard p starts at element
+// p*shard + t*pitch + h*head, its D features are contiguous.
+struct HeadRows {
+  void* p;
+  int type;
+  int64_t shard, pitch, head;
+};
+struct RopeArgs {
+  const float *cos, *sin;   // [rows, dim/2]; null: no rotation
+  int64_t rows;
+  int dim, style;           // btq_rope
+};
+
+struct HeadArgs {
+  HeadRows x, y;
+  int64_t P, T;
+  int Hq, Hk, D;
+  int norm;                 // btq_norm
+  const float *q_weight, *k_weight;
+  int64_t qw_shard, qw_head, kw_shard, kw_head;
+  float eps;
+  const int32_t* positions;
+  RopeArgs rope;
+};
+// Every head starts on 16 bytes.
+inline bool on16(const HeadRows& r) {
+  const int64_t n = r.type == kF32 ? 4 : 8;
+  return ((uintptr_t)r.p & 15) == 0 && r.shard % n == 0 && r.pitch % n == 0 && r.head % n == 0;
+}
+hipError_t launch_head_norm_rope(const HeadArgs& a, hipStream_t s);
+
+// A batch of sequences and the paged cache that holds them.
+struct KvArgs {
+  int64_t P, T;
+  int B, Hk, D;
+  const int32_t *starts, *lengths, *table;   // [B+1], [B], [B,max_pages]
+  int64_t max_pages;
+  int capacity;             // max_pages * page size
+  uint8_t* cache;
+  int64_t pages;
+  int page_shift;           // a page holds 2^page_shift blocks
+};
+hipError_t launch_kv_append(const HeadRows& k, const HeadRows& v, const RopeArgs& rope,
+                            const KvArgs& a, hipStream_t s);
+hipError_t launch_kv_gather(const HeadRows& k, const HeadRows& v, const KvArgs& a, hipStream_t s);
+
+struct AttnArgs {
+  HeadRows q;               // bf16
+  bool q_on16;              // every head starts on 16 bytes
+  KvArgs kv;
+  int Hq, G;                // query heads, those of one key head
+  float scale2;             // scale * log2(e)
+  int causal, window;       // window 0: none
+  void* out;                // [P,T,Hq*D]
+  int out_type;
+  float* lse;               // [P,T,Hq] or null
+  float* ws;
+  int splits;
+};
+// Splits of the keys that a launch of these sizes takes, and the workspace for them.
+struct AttnPlan {
+  int tiles_of;             // 16-column tiles of a wave
+  bool by_keys;             // a block's waves share out the keys, else the columns
+  int splits;
+  int64_t items;            // blocks of one head and split
+  size_t workspace;
+};
+AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t max_length);
+hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s);
+
 }  // namespace btq

@@ -1,0 +1,314 @@
+// btq_kv_append and btq_kv_gather: rows of new keys and values into the paged
+// 4-bit cache, and what the cache holds back into rows.
+#include "kv.hpp"
+
+namespace btq {
+namespace {
+
+constexpr int kHalf = 0;   // btq_rope
+constexpr int kThreads = 256;
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+// The block (32 tokens of a head) that a thread block works on.
+struct Place {
+  int64_t at;      // its byte offset in the cache, -1: no page
+  int64_t row;     // batch row of its token 0 (which may lie before the sequence's)
+  int from, to;    // its tokens among the batch's rows
+  int first;       // place of token 0 in its sequence
+};
+__device__ __forceinline__ bool find_place(const KvArgs& a, int64_t item, int64_t shard, int head,
+                                           Place* o) {
+  int64_t sub;
+  const int b = find_sequence(a, 1, 5, 2, item, &sub);
+  if (b < 0) return false;
+  const SeqRange s = seq_range(a, b);
+  const int block = (s.first() >> 5) + (int)sub;
+  o->first = block * kBlockTokens;
+  o->from = max(s.first() - o->first, 0);
+  o->to = min(s.length - o->first, kBlockTokens);
+  if (o->from >= o->to) return false;
+  o->row = (int64_t)s.begin + o->first - s.first();
+  o->at = kv_block(a, b, shard, head, block);
+  return true;
+}
+
+template <bool kVector>
+__device__ __forceinline__ void load_tile(const HeadRows& r, int64_t base, int D, const Place& at,
+                                          float* tile, int pitch) {
+  const int runs = D / 8;
+  for (int i = threadIdx.x; i < kBlockTokens * runs; i += kThreads) {
+    const int t = i / runs, f = (i - t * runs) * 8;
+    if (t < at.from || t >= at.to) continue;
+    const int64_t e = base + (at.row + t) * r.pitch + f;
+    float v[8];
+    if (r.type == kBf16) {
+      uint32_t w[4];
+      if constexpr (kVector) {
+        const v4u x = *(const v4u*)((const uint16_t*)r.p + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = x[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = ((const uint16_t*)r.p)[e + 2 * j] |
+                 (uint32_t)((const uint16_t*)r.p)[e + 2 * j + 1] << 16;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = ((const float*)r.p)[e + j];
+    }
+    float* o = tile + t * pitch + f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = v[j];
+  }
+}
+
+// f combined over groups of 8 lanes.
+template <typename F>
+__device__ __forceinline__ uint32_t combine8(uint32_t x, F f) {
+  x = f(x, dpp<0xb1>(x));
+  x = f(x, dpp<0x4e>(x));
+  return f(x, dpp<0x141>(x));
+}
+
+// Codes of E features a lane, 8 lanes a row; returns the row's word.
+// The quotient x/scale is the correctly rounded one: q = x*r with r the rounded
+// 1/scale, then one step of its residual (Markstein's theorem). A product with r
+// alone would miss the ties that bf16 rows have (x and scale hold 8 bits each).
+template <int E>
+__device__ __forceinline__ uint32_t quantize(const float (&x)[E], uint32_t (&code)[E]) {
+  float lo = 0.0f, hi = 0.0f;
+  uint32_t big = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    lo = fminf(lo, x[e]);
+    hi = fmaxf(hi, x[e]);
+    big = max(big, __float_as_uint(x[e]) & 0x7fffffffu);
+  }
+  lo = __uint_as_float(combine8(__float_as_uint(lo), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+  hi = __uint_as_float(combine8(__float_as_uint(hi), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+  big = combine8(big, [](uint32_t a, uint32_t b) { return max(a, b); });
+  const float range = hi - lo;
+  // rounded up to bf16, so 15 steps span the range and no code is cut off
+  uint32_t sb = (__float_as_uint(range / 15.0f) + 0xffffu) & 0xffff0000u;
+  const bool bad = big >= 0x7f800000u || !(range < INFINITY);
+  if (sb < 0x00800000u) sb = 0x3f800000u;   // below the normal numbers: scale 1, codes 0
+  const float scale = __uint_as_float(sb), r = 1.0f / scale;
+  auto steps = [&](float v) {
+    const float q = v * r;
+    return rintf(__builtin_fmaf(__builtin_fmaf(-q, scale, v), r, q));
+  };
+  const float z = fminf(steps(-lo), 15.0f);
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    code[e] = bad ? 0u : (uint32_t)fminf(fmaxf(steps(x[e]) + z, 0.0f), 15.0f);
+  return bad ? kNanWord : sb | (__float_as_uint(128.0f + z) >> 16);
+}
+
+template <int D, bool kVector>
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(HeadRows k, HeadRows v, RopeArgs rope,
+                                                             KvArgs a, int64_t items) {
+  constexpr int E = D / 8, kPitch = D + 4;
+  __shared__ float tile[2][kBlockTokens * kPitch];
+  __shared__ uint32_t codes[kBlockTokens * (E * 2 + 1)];   // a row of D bytes and 4 more
+  const int64_t hk = blockIdx.x % (a.P * a.Hk), item = blockIdx.x / (a.P * a.Hk);
+  const int64_t shard = hk / a.Hk;
+  const int head = (int)(hk % a.Hk);
+  Place at;
+  if (!find_place(a, item, shard, head, &at) || at.at < 0) return;
+  load_tile<kVector>(k, shard * k.shard + head * k.head, D, at, tile[0], kPitch);
+  load_tile<kVector>(v, shard * v.shard + head * v.head, D, at, tile[1], kPitch);
+  __syncthreads();
+
+  uint8_t* block = a.cache + at.at;
+  const int t = threadIdx.x / 8, sub = threadIdx.x % 8, f0 = sub * E;
+  const bool mine = t >= at.from && t < at.to;
+  uint32_t code[E];
+  float x[E];
+  {
+    const float* row = tile[0] + t * kPitch;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = row[f0 + e];
+    if (rope.cos) {
+      const int half = rope.dim / 2;
+      const int64_t pos = at.first + t;
+      const bool known = pos < rope.rows;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = f0 + e;
+        if (i < rope.dim && mine) {
+          const bool second = rope.style == kHalf ? i >= half : e & 1;
+          const int j = rope.style == kHalf ? (second ? i - half : i) : i / 2;
+          const float other = row[rope.style == kHalf ? (second ? i - half : i + half) : i ^ 1];
+          float c = __uint_as_float(0x7fc00000u), s = c;
+          if (known) c = rope.cos[pos * half + j], s = rope.sin[pos * half + j];
+          x[e] = second ? x[e] * c + other * s : x[e] * c - other * s;
+        }
+      }
+    }
+    const uint32_t word = quantize<E>(x, code);
+    if (mine) {
+      uint8_t* out = block + t * (D / 2) + sub * (E / 2);
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        *(uint16_t*)(out + e / 2) = (uint16_t)(code[e] | code[e + 1] << 4 | code[e + 2] << 8 |
+                                               code[e + 3] << 12);
+      if (sub == 0) *(uint32_t*)(block + 32 * D + t * 4) = word;
+    }
+  }
+  {
+    const float* row = tile[1] + t * kPitch;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = row[f0 + e];
+    const uint32_t word = quantize<E>(x, code);
+    if (mine && sub == 0) *(uint32_t*)(block + 32 * D + 128 + t * 4) = word;
+    uint32_t* out = codes + t * (E * 2 + 1) + sub * (E / 4);
+#pragma unroll
+    for (int e = 0; e < E; e += 4)
+      out[e / 4] = code[e] | code[e + 1] << 8 | code[e + 2] << 16 | code[e + 3] << 24;
+  }
+  __syncthreads();
+  // 16 tokens of a feature a thread: 8 bytes, in which only this batch's tokens change
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    const int d = i >> 1, first = (i & 1) * 16;
+    uint64_t bits = 0, mask = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int token = first + j;
+      const uint64_t c = ((const uint8_t*)(codes + token * (E * 2 + 1)))[d];
+      if (token >= at.from && token < at.to) {
+        bits |= c << (4 * j);
+        mask |= (uint64_t)15 << (4 * j);
+      }
+    }
+    if (!mask) continue;
+    uint64_t* out = (uint64_t*)(block + 16 * D + d * 16 + first / 2);
+    if (~mask) bits |= *out & ~mask;
+    *out = bits;
+  }
+}
+
+template <bool kVector>
+__device__ __forceinline__ void store_rows(const HeadRows& r, int64_t e, const float* v, int n) {
+  if (r.type == kF32) {
+    float* o = (float*)r.p + e;
+    for (int j = 0; j < n; ++j) o[j] = v[j];
+  } else {
+    uint16_t* o = (uint16_t*)r.p + e;
+    for (int j = 0; j < n; j += 2) {
+      const uint32_t w = f32_to_bf16x2(v[j], v[j + 1]);
+      if constexpr (kVector) {
+        *(uint32_t*)(o + j) = w;
+      } else {
+        o[j] = (uint16_t)w;
+        o[j + 1] = (uint16_t)(w >> 16);
+      }
+    }
+  }
+}
+
+template <int D, bool kVector>
+__global__ __launch_bounds__(kThreads) void kv_gather_kernel(HeadRows k, HeadRows v, KvArgs a,
+                                                             int64_t items) {
+  constexpr int E = D / 8;
+  __shared__ uint32_t codes[kBlockTokens * (E * 2 + 1)];
+  const int64_t hk = blockIdx.x % (a.P * a.Hk), item = blockIdx.x / (a.P * a.Hk);
+  const int64_t shard = hk / a.Hk;
+  const int head = (int)(hk % a.Hk);
+  Place at;
+  if (!find_place(a, item, shard, head, &at)) return;
+  const uint8_t* block = a.cache + at.at;
+  if (at.at >= 0) {
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+      const int d = i >> 1, first = (i & 1) * 16;
+      const uint64_t bits = *(const uint64_t*)(block + 16 * D + d * 16 + first / 2);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        ((uint8_t*)(codes + (first + j) * (E * 2 + 1)))[d] = (uint8_t)(bits >> (4 * j) & 15);
+    }
+  }
+  __syncthreads();
+  const int t = threadIdx.x / 8, sub = threadIdx.x % 8;
+  if (t < at.from || t >= at.to) return;
+  float kx[E], vx[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) kx[e] = vx[e] = 0.0f;
+  if (at.at >= 0) {   // a place without a page holds zeros
+    const uint32_t kw = *(const uint32_t*)(block + 32 * D + t * 4);
+    const uint32_t vw = *(const uint32_t*)(block + 32 * D + 128 + t * 4);
+    const float ks = __uint_as_float(kw & 0xffff0000u), kz = __uint_as_float(kw << 16) - 128.0f;
+    const float vs = __uint_as_float(vw & 0xffff0000u), vz = __uint_as_float(vw << 16) - 128.0f;
+    const uint8_t* kr = block + t * (D / 2) + sub * (E / 2);
+    const uint32_t* vr = codes + t * (E * 2 + 1) + sub * (E / 4);
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      const uint32_t c = *(const uint16_t*)(kr + e / 2), d = vr[e / 4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        kx[e + j] = ((float)(c >> (4 * j) & 15) - kz) * ks;
+        vx[e + j] = ((float)(d >> (8 * j) & 15) - vz) * vs;
+      }
+    }
+  }
+  const int64_t row = at.row + t;
+  if (k.p) store_rows<kVector>(k, shard * k.shard + row * k.pitch + head * k.head + sub * E, kx, E);
+  if (v.p) store_rows<kVector>(v, shard * v.shard + row * v.pitch + head * v.head + sub * E, vx, E);
+}
+
+// Blocks of 32 places that T rows of B sequences can touch (find_sequence).
+int64_t place_items(const KvArgs& a) { return a.T / kBlockTokens + 2 * (int64_t)a.B; }
+
+}  // namespace
+
+#define BTQ_FOR_HEAD(D, CALL)            \
+  switch (D) {                           \
+    case 32: CALL(32); break;            \
+    case 64: CALL(64); break;            \
+    case 96: CALL(96); break;            \
+    case 128: CALL(128); break;          \
+    case 160: CALL(160); break;          \
+    case 192: CALL(192); break;          \
+    case 224: CALL(224); break;          \
+    default: CALL(256); break;           \
+  }
+
+hipError_t launch_kv_append(const HeadRows& k, const HeadRows& v, const RopeArgs& rope,
+                            const KvArgs& a, hipStream_t s) {
+  const int64_t items = place_items(a);
+  const dim3 grid((unsigned)(items * a.P * a.Hk));
+  const bool vec = on16(k) && on16(v);
+#define BTQ_CALL(N)                                                                      \
+  if (vec)                                                                               \
+    kv_append_kernel<N, true><<<grid, kThreads, 0, s>>>(k, v, rope, a, items);           \
+  else                                                                                   \
+    kv_append_kernel<N, false><<<grid, kThreads, 0, s>>>(k, v, rope, a, items)
+  BTQ_FOR_HEAD(a.D, BTQ_CALL)
+#undef BTQ_CALL
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_gather(const HeadRows& k, const HeadRows& v, const KvArgs& a, hipStream_t s) {
+  const int64_t items = place_items(a);
+  const dim3 grid((unsigned)(items * a.P * a.Hk));
+  const bool vec = on16(k) && on16(v);
+#define BTQ_CALL(N)                                                                      \
+  if (vec)                                                                               \
+    kv_gather_kernel<N, true><<<grid, kThreads, 0, s>>>(k, v, a, items);                 \
+  else                                                                                   \
+    kv_gather_kernel<N, false><<<grid, kThreads, 0, s>>>(k, v, a, items)
+  BTQ_FOR_HEAD(a.D, BTQ_CALL)
+#undef BTQ_CALL
+  return hipGetLastError();
+}
+
+}  // namespace btq

@@ -482,6 +482,157 @@ int btq_block_norm(const void *y, int y_type, const void *residual, int r_type,
                    int pre, const float *pre_weight, const float *pre_bias, float pre_eps,
                    void *residual_out, void *n, int n_type, float *n_scale, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention between two linear layers: the norm and the rotation of heads, a
+ * paged cache of keys and values in 4-bit codes, and attention over it, for all
+ * P shards.
+ *
+ * Extra conventions of these calls
+ *  - Heads: x[p,t,h,:] starts at element p*x_shard + t*x_pitch + h*x_head and its
+ *    D features are contiguous, so the heads of a fused projection's rows are
+ *    taken where they lie. Strides are >= 0.
+ *  - A batch is B sequences one after another: the rows of sequence b are
+ *    seq_starts[b] <= t < seq_starts[b+1] (i32 [B+1], ascending), lengths[b] (i32
+ *    [B]) is the number of its tokens in the cache WITH those rows, so row t has
+ *    the place lengths[b] - seq_starts[b+1] + t. Rows before seq_starts[0] and
+ *    from seq_starts[B] on belong to no sequence and are left as they are.
+ *    A sequence may have no rows, or no tokens.
+ *  - page_table i32 [B,max_pages]: the page that holds places i*page_size .. of a
+ *    sequence. An entry outside [0,pages) is no page: it is not read, and its
+ *    places are not in the cache. The table's places, max_pages*page_size, may be
+ *    2^30 at most.
+ *  - These arrays are read on the device. Whatever they hold, no call touches
+ *    memory outside its tensors (starts are cut to [0,T], lengths to the table's
+ *    places); where starts do not ascend, the results are unspecified.
+ *  - cache u8 [P,pages,Hk,page_size/32,btq_kv_block_bytes(D)], 16-byte aligned;
+ *    page_size a power of 2 from 32 to 65536, D a multiple of 32 up to 256.
+ *    A block holds 32 tokens of a key head:
+ *      keys    [32][D/2]  feature 2i in the low nibble of byte i, 2i+1 in the high
+ *      values  [D][16]    token 2i in the low nibble of byte i, 2i+1 in the high
+ *      words   u32 [32] of the keys, then u32 [32] of the values: the bf16 bits
+ *              of the scale in the high half, those of 128 + z in the low half
+ *    A code c stands for scale*(c - z).
+ *  - rope: cos_table and sin_table fp32 [rope_rows,rope_dim/2], row = position.
+ *    The first rope_dim features (even, <= D) turn in pairs (a, b) ->
+ *    (a*cos - b*sin, b*cos + a*sin), each product and sum one fp32 operation:
+ *    BTQ_ROPE_HALF pairs feature i with i + rope_dim/2, BTQ_ROPE_PAIRS 2i with
+ *    2i+1, both by column i. Both tables NULL: no rotation. A position outside
+ *    the table turns its features to NaN.
+ *  - NaN and Inf are carried: see each call.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { BTQ_ROPE_HALF = 0, BTQ_ROPE_PAIRS = 1 } btq_rope;
+
+/* Bytes of a block of 32 tokens of a key head, 32*D + 256; 0 for a D that the
+ * cache does not take. */
+int64_t btq_kv_block_bytes(int64_t D);
+
+/*
+ * The norm of each query and key head over its D features, with the rotation by
+ * its token's position, in one pass:
+ *   y = rope(norm(x) * weight)
+ * in fp32, rounded once. norm is a btq_norm over the head (no bias).
+ *   x         fp32 or bf16 [P,T,q_heads+k_heads,D] in: query heads first
+ *   q_weight, k_weight  fp32 or NULL (1): the weights of head h of shard p start
+ *             at p*qw_shard + h*qw_head (k: kw_*, h from 0); strides 0 for one
+ *             set of D weights
+ *   positions i32 [T] in, or NULL without tables
+ *   y         fp32 or bf16 [P,T,q_heads+k_heads,D] out, strides of its own. It
+ *             may be x itself (same address, type and strides); no other overlap.
+ * 1 <= D <= 65536, q_heads and k_heads >= 0, one of them at least. NaN and Inf
+ * spread to their head as the formulas give them. The vector kernel takes
+ * D <= 1024, D and rope_dim multiples of 16, heads, weights and tables on 16
+ * bytes, and fewer than 2^23 heads a shard; others take a general one.
+ */
+int btq_head_norm_rope(const void *x, int x_type, int64_t x_shard, int64_t x_pitch, int64_t x_head,
+                       int64_t P, int64_t T, int64_t q_heads, int64_t k_heads, int64_t D,
+                       int norm, const float *q_weight, int64_t qw_shard, int64_t qw_head,
+                       const float *k_weight, int64_t kw_shard, int64_t kw_head, float eps,
+                       const int32_t *positions, const float *cos_table, const float *sin_table,
+                       int64_t rope_rows, int64_t rope_dim, int rope,
+                       void *y, int y_type, int64_t y_shard, int64_t y_pitch, int64_t y_head,
+                       void *stream);
+
+/*
+ * Appends the batch's keys, rotated by their places, and values to the cache.
+ * For each row of D fp32 values (a key after its rotation), with 0 in the range,
+ * lo = min(0, x), hi = max(0, x):
+ *   scale = (hi - lo)/15 rounded up to bf16; below 2^-126: 1
+ *   z     = rint(-lo/scale),  code = clamp(rint(x/scale) + z, 0, 15)
+ * rint is to nearest even; the quotients are rounded once, so for bf16 rows
+ * without rotation the codes are those of exact arithmetic, ties included. No
+ * value moves by more than scale/2. A row that holds NaN or Inf, or whose range
+ * passes the largest fp32, gets scale NaN and codes 0: queries that see it get NaN.
+ *   k, v      fp32 or bf16 (both x_type) [P,T,Hk,D] in
+ * A row whose place is negative (more rows than lengths[b]) or has no page is
+ * dropped. Other places of the pages keep what they hold. Two rows of a call must not have the
+ * same place in the cache (sequences that share a page may, where it is not
+ * written). Calls that write one page must not run at once, and one that reads it
+ * must wait for them.
+ */
+int btq_kv_append(const void *k, const void *v, int x_type, int64_t k_shard, int64_t k_pitch,
+                  int64_t k_head, int64_t v_shard, int64_t v_pitch, int64_t v_head,
+                  int64_t P, int64_t T, int64_t Hk, int64_t D,
+                  const int32_t *seq_starts, const int32_t *lengths, int64_t B,
+                  const int32_t *page_table, int64_t max_pages,
+                  const float *cos_table, const float *sin_table, int64_t rope_rows,
+                  int64_t rope_dim, int rope,
+                  uint8_t *cache, int64_t pages, int64_t page_size, void *stream);
+
+/*
+ * What the cache holds for the batch's rows: k[p,t,h,:] = scale*(code - z) of the
+ * key at row t's place, v the same of the value, in fp32, rounded once. Rows
+ * without a place in the cache get zeros.
+ *   k, v      fp32 or bf16 (both y_type) [P,T,Hk,D] out; one may be NULL
+ * With lengths as btq_kv_append had them it reads back what that call wrote; with
+ * others any stretch of the cached sequences.
+ */
+int btq_kv_gather(const int32_t *seq_starts, const int32_t *lengths, int64_t B,
+                  const int32_t *page_table, int64_t max_pages,
+                  const uint8_t *cache, int64_t pages, int64_t page_size,
+                  int64_t P, int64_t T, int64_t Hk, int64_t D,
+                  void *k, void *v, int y_type, int64_t k_shard, int64_t k_pitch, int64_t k_head,
+                  int64_t v_shard, int64_t v_pitch, int64_t v_head, void *stream);
+
+/*
+ * Attention of the batch's queries over the cache. Query head h reads key head
+ * h/(Hq/Hk). For a row at place i, over the keys j in the cache that it sees,
+ *   t[j] = scale * sum_d q[d]*k[j,d],  out = sum_j exp(t[j])*v[j] / sum_j exp(t[j])
+ *   lse  = log(sum_j exp(t[j]))
+ * It sees j < lengths[b], and j <= i if causal, and j > i - window if window > 0.
+ * A row that sees no key gets out 0 and lse -Inf.
+ * Scores and sums are fp32; the weight exp(t - max)*(scale of v[j]) is rounded to
+ * bf16 for the second product. NaN or Inf in a query gives NaN; a NaN key or value
+ * gives NaN to the queries that see it and to no others.
+ *   q         bf16 [P,T,Hq,D] in; fastest with heads on 16 bytes
+ *   scale     > 0 and finite
+ *   max_length  an upper bound of lengths (0: the table's places) by which the
+ *             keys are split over the chip. Longer sequences are as correct,
+ *             and may be slower.
+ *   out       fp32 or bf16 [P,T,Hq*D] out, contiguous: an x of btq_int8_linear
+ *   lse       fp32 [P,T,Hq] out, or NULL
+ *   workspace at least btq_kv_attention_workspace_bytes bytes of the same sizes,
+ *             16-byte aligned, with no initial value (NULL if that is 0). Calls at
+ *             the same time need one each.
+ * One launch, or two where keys are split. The result does not depend on the
+ * other sequences of the batch beyond their number, and the same call gives the
+ * same bits.
+ */
+int btq_kv_attention(const void *q, int64_t q_shard, int64_t q_pitch, int64_t q_head,
+                     int64_t P, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                     const int32_t *seq_starts, const int32_t *lengths, int64_t B,
+                     const int32_t *page_table, int64_t max_pages,
+                     const uint8_t *cache, int64_t pages, int64_t page_size,
+                     float scale, int causal, int64_t window, int64_t max_length,
+                     void *out, int out_type, float *lse,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes for btq_kv_attention (0 for sizes that it refuses). max_length
+ * 0 stands for the table's places, max_pages*page_size. */
+size_t btq_kv_attention_workspace_bytes(int64_t P, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                                        int64_t B, int64_t max_pages, int64_t page_size,
+                                        int64_t max_length);
+
 /* Static text for a btq_status value (never NULL). */
 const char *btq_status_str(int status);
 

@@ -1,0 +1,377 @@
+"""btq_kv_attention against plain numpy in 64 bits (kv_helpers.attention, which
+derives the tolerance; the output's own rounding and a factor 1.05 for terms of
+second order are added here)."""
+import numpy as np
+import pytest
+import torch
+
+import bit_tensor_activation_amd as B
+from bit_tensor_activation_amd import _lib
+from helpers import say
+from kv_helpers import (BF16, DEV, F32, NAN_WORD, U, Batch, attention, block_bytes, host,
+                        random_cache)
+
+
+def compare(got, lse, want, dt):
+    out, tol, l, ltol = want
+    P, T, Hq, D = out.shape
+    got, own = host(got).reshape(P, T, Hq, D), ~np.isnan(out)
+    tol = 1.05 * tol + (U if dt == F32 else 2.0 ** -8) * np.abs(out) + 2.0 ** -133
+    off = np.abs(got - out)
+    assert (off[own] <= tol[own]).all(), (
+        f"{(off > tol)[own].sum()} of {own.sum()} off, worst {np.max((off - tol)[own])} at "
+        f"{np.argwhere((off > tol) & own)[:3]}, NaN {np.isnan(got[own]).sum()}")
+    if lse is not None:
+        lse, own = host(lse), ~np.isnan(l)
+        none = own & np.isneginf(l)
+        assert (lse[none] == -np.inf).all()
+        own &= ~none
+        assert (np.abs(lse - l)[own] <= (1.05 * ltol)[own]).all(), np.max((np.abs(lse - l) - ltol)[own])
+
+
+def check(batch, P, Hq, Hk, D, causal=True, window=0, dt=BF16, lse=True, max_length=0, seed=0,
+          sigma=1.0, q_sigma=1.5, edit=None, gap=0, shift=0, scale=None):
+    g = np.random.default_rng(seed + batch.T + 7 * D)
+    size = P * batch.T * (Hq * D + gap) + shift
+    flat = torch.from_numpy((g.standard_normal(size) * q_sigma).astype(np.float32)).to(DEV).to(BF16)
+    q = flat[shift:].view(P, batch.T, Hq * D + gap)[..., :Hq * D].unflatten(-1, (Hq, D))
+    cache = random_cache(batch, P, Hk, D, seed, sigma)
+    if edit is not None:
+        edit(batch, cache)
+    starts, lengths, tb = batch.dev()
+    out = torch.full((P, batch.T, Hq * D), 5.0, dtype=dt, device=DEV)
+    sums = torch.full((P, batch.T, Hq), 5.0, device=DEV) if lse else None
+    dev = torch.from_numpy(cache).to(DEV)
+    got = B.btq_kv_attention(q, starts, lengths, tb, dev, causal=causal, window=window,
+                             max_length=max_length, out=out, lse=sums, scale=scale)
+    assert got is out
+    want = attention(batch, cache, host(q), Hk, D, D ** -0.5 if scale is None else float(np.float32(scale)),
+                     causal, window)
+    compare(out, sums, want, dt)
+    own = np.zeros(batch.T, bool)
+    for row, _, _ in batch.rows():
+        own[row] = True
+    assert (out[:, ~own] == 5).all()
+    assert sums is None or (sums[:, ~own] == 5).all()
+    return out, sums, (q, starts, lengths, tb, dev)
+
+
+BATCHES = [
+    Batch([1], [1]), Batch([1], [2]), Batch([1], [31]), Batch([1], [128]), Batch([1], [129]),
+    Batch([1], [700], page=64), Batch([1] * 6, [1, 40, 127, 128, 300, 513], page=128),
+    Batch([3, 1, 0, 7], [3, 260, 50, 130], before=2, behind=3, slack=1),
+    Batch([40, 9], [40, 200], page=64), Batch([0, 2, 0], [0, 2, 9]), Batch([130], [130]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", range(len(BATCHES)))
+@pytest.mark.parametrize("D", [64, 128])
+def test_batches(n, D):
+    say(f"case: kv attention batch {n} D={D}")
+    check(BATCHES[n], 1, 4, 1, D)
+    check(BATCHES[n], 2, 2, 2, D, dt=F32)
+    check(BATCHES[n], 1, 6, 2, D, causal=False, lse=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [32, 96, 160, 192, 224, 256])
+def test_head_sizes(D):
+    say(f"case: kv attention D={D}")
+    for n in (5, 7, 8):
+        check(BATCHES[n], 2, 4, 1, D)
+    check(BATCHES[10], 1, 8, 1, D)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (3, 3), (8, 1), (5, 1), (16, 1), (17, 1), (40, 2), (64, 1),
+                                   (12, 4)])
+def test_head_groups(Hq, Hk):
+    say(f"case: kv attention Hq={Hq} Hk={Hk}")
+    check(Batch([1, 1], [90, 300]), 1, Hq, Hk, 64)
+    check(Batch([5, 2], [90, 150]), 1, Hq, Hk, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 128, 200, 1 << 29, (1 << 31) + 5])
+def test_windows(window):
+    for causal in (True, False):
+        check(BATCHES[7], 1, 4, 1, 64, window=window, causal=causal)
+        check(BATCHES[6], 1, 4, 1, 64, window=window, causal=causal)
+        check(Batch([70], [300]), 1, 4, 1, 64, window=window, causal=causal)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("length", [512, 513, 2048, 5000])
+def test_split_keys(length):
+    # one sequence on a whole chip: the keys are split, and by other bounds of length
+    # otherwise; rows that stay in one split among them
+    say(f"case: kv attention length={length}")
+    for ml in (0, length, 128, 1 << 20):
+        check(Batch([1], [length], page=64), 1, 8, 1, 128, max_length=ml, dt=F32)
+    check(Batch([2, 1, 1], [length, 3, 900], page=64), 1, 4, 2, 64, dt=F32)
+    check(Batch([40], [length], page=64), 1, 8, 1, 64, dt=F32)
+    check(Batch([40], [length], page=64), 1, 8, 1, 64, dt=F32, window=1000)
+
+
+@pytest.mark.gpu
+def test_rows_that_see_nothing():
+    # more rows than places, no pages, an empty sequence, a table without places
+    b = Batch([12, 4, 5], [4, 64, 0])
+    b.table[1, :] = -1
+    out, lse, _ = check(b, 2, 4, 1, 64)
+    assert (out[:, :8] == 0).all() and torch.isneginf(lse[:, :8]).all()
+    assert (out[:, 12:] == 0).all()
+    b = Batch([3], [3])
+    b.table, b.max_pages = np.zeros((1, 0), np.int32), 0
+    out, _, _ = check(b, 1, 2, 1, 64)
+    assert (out == 0).all()
+
+
+@pytest.mark.gpu
+def test_missing_pages_inside_a_sequence():
+    b = Batch([2, 1], [400, 300], page=32)
+    b.table[0, [0, 3, 4, 5, 6, 11]] = -1
+    b.table[1, 5] = b.pages
+    b.table[1, 2] = -2 ** 31
+    check(b, 1, 4, 1, 128)
+    check(b, 1, 4, 1, 128, window=60)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["key", "value"])
+def test_nan_rows_reach_only_the_queries_that_see_them(what):
+    D = 64
+
+    def edit(batch, cache):
+        for b, place in ((0, 150), (1, 10)):
+            page, block, t = batch.where(b, place)
+            at = 32 * D + (128 if what == "value" else 0) + 4 * t
+            cache[:, page, :, block, at:at + 4] = np.frombuffer(np.uint32(NAN_WORD).tobytes(), np.uint8)
+    b = Batch([60, 1, 1], [180, 400, 30])     # row 30 of the first is place 150
+    g = np.random.default_rng(3)
+    q = torch.from_numpy(g.standard_normal((1, b.T, 4, D)).astype(np.float32)).to(DEV).to(BF16)
+    clean = random_cache(b, 1, 2, D)
+    dirty = clean.copy()
+    edit(b, dirty)
+    starts, lengths, tb = b.dev()
+    for kw in (dict(), dict(window=20)):
+        a = B.btq_kv_attention(q, starts, lengths, tb, torch.from_numpy(clean).to(DEV), **kw)
+        d = B.btq_kv_attention(q, starts, lengths, tb, torch.from_numpy(dirty).to(DEV), **kw)
+        sees = torch.zeros(b.T, dtype=torch.bool)
+        sees[30:50 if kw else 60] = True
+        sees[60] = not kw
+        assert torch.isfinite(a).all()
+        assert torch.isnan(d[0, sees]).all()
+        assert torch.equal(d[0, ~sees], a[0, ~sees])
+
+
+@pytest.mark.gpu
+def test_stale_places_past_the_end_do_not_matter():
+    # NaN words, and any bytes, behind the last token and in pages of no sequence
+    def edit(batch, cache):
+        keep = np.zeros(cache.shape[1:2] + cache.shape[3:4] + (32,), bool)
+        for b in range(batch.B):
+            for j in range(batch.lengths[b]):
+                keep[batch.where(b, j)] = True
+        for page, block, t in np.argwhere(~keep):
+            for at in (32 * 64 + 4 * t, 32 * 64 + 128 + 4 * t):
+                cache[:, page, :, block, at:at + 4] = 0xff
+    check(Batch([1, 1, 4], [37, 129, 70], page=64), 2, 4, 1, 64, edit=edit)
+    check(Batch([50], [50], page=64), 2, 4, 1, 64, edit=edit)
+
+
+@pytest.mark.gpu
+def test_nan_and_inf_queries_stay_in_their_row():
+    b = Batch([1, 1, 40], [300, 300, 60])
+    cache = torch.from_numpy(random_cache(b, 1, 1, 128)).to(DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    q = torch.randn((1, b.T, 2, 128), device=DEV, generator=g).to(BF16)
+    starts, lengths, tb = b.dev()
+    a = B.btq_kv_attention(q, starts, lengths, tb, cache)
+    bad = q.clone()
+    bad[0, 0, 0] = float("nan")
+    bad[0, 1, 1, 5] = float("inf")
+    bad[0, 20, 0, 7] = float("nan")
+    lse = torch.empty((1, b.T, 2), device=DEV)
+    d = B.btq_kv_attention(bad, starts, lengths, tb, cache, lse=lse).view(1, b.T, 2, 128)
+    a = a.view(1, b.T, 2, 128)
+    hit = torch.zeros((b.T, 2), dtype=torch.bool)
+    hit[0, 0] = hit[1, 1] = hit[20, 0] = True
+    assert torch.isnan(d[0, hit]).all() and torch.isnan(lse[0, hit]).all()
+    assert torch.equal(d[0, ~hit], a[0, ~hit])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sigma,q_sigma,scale", [(1.0, 20.0, None), (30.0, 4.0, None), (1e-3, 1.0, None),
+                                                 (1.0, 1.0, 1e-6), (1.0, 1.0, 3.0)])
+def test_flat_and_sharp_softmax(sigma, q_sigma, scale):
+    for n in (6, 7, 8):
+        check(BATCHES[n], 1, 4, 1, 128, sigma=sigma, q_sigma=q_sigma, dt=F32, scale=scale)
+
+
+@pytest.mark.gpu
+def test_maximum_that_rises_late():
+    # scores grow along the keys, so the sums are rescaled again and again
+    D = 64
+
+    def edit(batch, cache):
+        for j in range(batch.lengths[0]):
+            page, block, t = batch.where(0, j)
+            s = np.float32(0.02 * (1 + j) / 4).view(np.uint32) & 0xffff0000
+            cache[:, page, :, block, 32 * D + 4 * t:32 * D + 4 * t + 4] = np.frombuffer(
+                np.uint32(s | 0x4300).tobytes(), np.uint8)
+    check(Batch([1], [900], page=64), 1, 4, 1, D, edit=edit, dt=F32, q_sigma=3.0)
+    check(Batch([64], [900], page=64), 1, 2, 1, D, edit=edit, dt=F32, q_sigma=3.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift,gap", [(0, 0), (1, 0), (3, 5), (8, 64), (0, 3)])
+def test_query_strides_and_alignment(shift, gap):
+    check(BATCHES[7], 2, 4, 2, 64, shift=shift, gap=gap)
+
+
+@pytest.mark.gpu
+def test_same_bits_again_and_in_other_batches():
+    out, lse, (q, starts, lengths, tb, cache) = check(BATCHES[7], 2, 4, 1, 128)
+    again = B.btq_kv_attention(q, starts, lengths, tb, cache)
+    assert torch.equal(again[:, 2:13], out[:, 2:13])
+    # the other sequences' contents do not matter
+    other = q.clone()
+    other[:, 2:5] = 1.0
+    part = B.btq_kv_attention(other, starts, lengths, tb, cache)
+    assert torch.equal(part[:, 5:13], out[:, 5:13])
+
+
+@pytest.mark.gpu
+def test_long_cache_offsets_pass_32_bits():
+    D, page = 128, 64
+    per = page // 32 * block_bytes(D)
+    pages = (6 << 30) // per
+    b = Batch([1], [190], page=page)
+    small = torch.from_numpy(random_cache(b, 1, 1, D)).to(DEV)
+    q = torch.randn((1, 1, 8, D), device=DEV).to(BF16)
+    starts, lengths, tb = b.dev()
+    want = B.btq_kv_attention(q, starts, lengths, tb, small)
+    cache = torch.zeros((1, pages, 1, page // 32, block_bytes(D)), dtype=torch.uint8, device=DEV)
+    far = [pages - 1, (4 << 30) // per, (4 << 30) // per - 1]
+    for i, p in enumerate(far):
+        cache[0, p] = small[0, int(b.table[0, i])]
+    got = B.btq_kv_attention(q, starts, lengths, torch.tensor([far], dtype=torch.int32, device=DEV), cache)
+    assert torch.equal(got, want) and want.any()
+
+
+@pytest.mark.gpu
+def test_capture_and_replay():
+    # one graph replayed over a growing sequence, whose lengths and pages it reads
+    D, page = 128, 64
+    b = Batch([1, 1], [2000, 2000], page=page)
+    cache = torch.from_numpy(random_cache(b, 2, 1, D)).to(DEV)
+    starts, lengths, tb = b.dev()
+    q = torch.randn((2, 2, 8, D), device=DEV).to(BF16)
+    out = torch.zeros((2, 2, 8 * D), dtype=BF16, device=DEV)
+    need = B.btq_kv_attention_workspace_bytes(2, 2, 8, 1, D, 2, tb.shape[1], page)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    assert need > 0
+    run = lambda o: B.btq_kv_attention(q, starts, lengths, tb, cache, out=o, workspace=ws)  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(out)
+    for n in (1, 700, 1999, 2000, 0, 513):
+        lengths.copy_(torch.tensor([n, max(n - 300, 0)], dtype=torch.int32))
+        q.normal_()
+        eager = torch.empty_like(out)
+        B.btq_kv_attention(q, starts, lengths, tb, cache, out=eager)
+        ws.fill_(0xff)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), n
+
+
+@pytest.mark.gpu
+def test_other_stream_and_no_shards():
+    b = Batch([1, 3], [800, 50], page=64)
+    cache = torch.from_numpy(random_cache(b, 1, 2, 64)).to(DEV)
+    q = torch.randn((1, 4, 4, 64), device=DEV).to(BF16)
+    starts, lengths, tb = b.dev()
+    want = B.btq_kv_attention(q, starts, lengths, tb, cache)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = B.btq_kv_attention(q[0], starts, lengths, tb, cache[0], stream=s)
+    s.synchronize()
+    assert torch.equal(got, want[0])
+    bits = B.btq_kv_attention(q.view(torch.int16), starts, lengths, tb, cache)
+    assert bits.dtype == torch.int16 and torch.equal(bits, want.view(torch.int16))
+    empty = B.btq_kv_attention(q[:, :0], starts * 0, lengths, tb, cache)
+    assert empty.shape == (1, 0, 256)
+
+
+@pytest.mark.gpu
+def test_python_refusals():
+    b = Batch([1], [600])
+    cache = torch.from_numpy(random_cache(b, 1, 2, 64)).to(DEV)
+    q = torch.zeros((1, 1, 4, 64), dtype=BF16, device=DEV)
+    starts, lengths, tb = b.dev()
+    args = dict(q=q, seq_starts=starts, lengths=lengths, page_table=tb, cache=cache)
+    for kw in (dict(q=q[:, :, :3]), dict(q=q[..., :32]), dict(cache=cache[0]), dict(q=q[0]),
+               dict(out=torch.zeros((1, 1, 4, 64), dtype=BF16, device=DEV)),
+               dict(lse=torch.zeros((1, 1, 2), device=DEV)), dict(seq_starts=starts[1:])):
+        with pytest.raises(ValueError):
+            B.btq_kv_attention(**{**args, **kw})
+    for kw in (dict(q=q.float()), dict(q=q.half()), dict(page_table=tb.long())):
+        with pytest.raises(TypeError):
+            B.btq_kv_attention(**{**args, **kw})
+    for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(window=-1),
+               dict(max_length=-1), dict(workspace=torch.empty(16, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(RuntimeError):
+            B.btq_kv_attention(**{**args, **kw})
+
+
+# ---- CPU: all return before any HIP call ---------------------------------------
+
+A = 0x10000
+OK, ARG, SHAPE, ALIGN = _lib.BTQ_OK, _lib.BTQ_ERR_ARG, _lib.BTQ_ERR_SHAPE, _lib.BTQ_ERR_ALIGN
+
+
+def call(q=A, qs=0, qp=1024, qh=128, P=1, T=4, Hq=8, Hk=2, D=128, starts=A, lengths=A, nb=1, tb=A,
+         mp=2, cache=A, pages=4, size=64, scale=0.1, causal=1, window=0, ml=0, out=A, ot=1, lse=A,
+         ws=A, wsb=1 << 40):
+    return _lib.load().btq_kv_attention(q, qs, qp, qh, P, T, Hq, Hk, D, starts, lengths, nb, tb, mp,
+                                        cache, pages, size, scale, causal, window, ml, out, ot, lse,
+                                        ws, wsb, None)
+
+
+def test_refusals():
+    assert call(T=0) == OK and call(nb=0) == OK
+    for kw in (dict(P=0), dict(P=65536), dict(T=-1), dict(Hk=0), dict(Hq=0), dict(Hq=7), dict(Hq=65536),
+               dict(D=48), dict(D=320), dict(nb=-1), dict(mp=-1), dict(mp=1 << 25), dict(size=33),
+               dict(size=1 << 17), dict(pages=0), dict(pages=1 << 31), dict(qp=-1), dict(qh=-1),
+               dict(P=2, qs=-1), dict(qp=1 << 61), dict(window=-1), dict(ml=-1), dict(ml=1 << 31),
+               dict(T=1 << 28, Hq=16)):
+        assert call(**kw) == SHAPE, kw
+    for kw in (dict(q=None), dict(out=None), dict(starts=None), dict(lengths=None), dict(tb=None),
+               dict(cache=None), dict(ot=2), dict(scale=0.0), dict(scale=-1.0),
+               dict(scale=float("inf")), dict(scale=float("nan"))):
+        assert call(**kw) == ARG, kw
+    for kw in (dict(q=A + 1), dict(out=A + 2), dict(ot=0, out=A + 4), dict(lse=A + 2), dict(ws=A + 8),
+               dict(cache=A + 8), dict(starts=A + 1)):
+        assert call(**kw) == ALIGN, kw
+    assert call(mp=1 << 12, ws=None) == ARG
+    assert call(mp=1 << 12, wsb=0) == _lib.BTQ_ERR_WORKSPACE
+
+
+def test_workspace_bytes():
+    f = _lib.load().btq_kv_attention_workspace_bytes
+    assert f(1, 1, 8, 1, 128, 1, 2, 64, 0) == 0                 # short: one split
+    n = f(1, 1, 8, 1, 128, 1, 1 << 12, 64, 0)
+    assert n > 0 and f(1, 1, 8, 1, 128, 1, 1 << 12, 64, 1 << 29) == n
+    assert f(1, 1, 8, 1, 128, 1, 1 << 12, 64, 100) == 0         # the bound says short
+    for bad in ((0, 1, 8, 1, 128, 1, 2, 64, 0), (1, 1, 8, 3, 128, 1, 2, 64, 0),
+                (1, 1, 8, 1, 100, 1, 2, 64, 0), (1, 1, 8, 1, 128, 1, 2, 40, 0),
+                (1, 1, 8, 1, 128, 1, 2, 64, -1), (1, 0, 8, 1, 128, 1, 2, 64, 0)):
+        assert f(*bad) == 0
