@@ -402,6 +402,7 @@ btq::KvArgs kv_args(int64_t P, int64_t T, int64_t Hk, int64_t D, const int32_t* 
                     const uint8_t* cache, int64_t pages, int64_t page_size) {
   int shift = 0;
   while ((int64_t(32) << shift) < page_size) ++shift;
+  if (max_pages == 0) table = starts;   // (an address that may be read; no entry counts)
   return {P, T, (int)B, (int)Hk, (int)D, starts, lengths, table, max_pages,
           (int)(max_pages * page_size), const_cast<uint8_t*>(cache), pages, shift};
 }

@@ -14,8 +14,13 @@
 // S is computed transposed (keys down, columns across), so that the 4 values of a
 // column that a lane holds of two 16-key tiles are the 8 consecutive keys of the
 // second product's operand: keys are dealt to tile rows to make it so, and
-// nothing moves between lanes but the running maximum. One wave takes 128 keys
-// (4 blocks) a step: 16-byte loads of K and V from HBM to registers, no LDS.
+// nothing moves between lanes but the running maximum.
+//
+// Two kernels. attention_keys_kernel, for few columns a sequence, is bound by the
+// cache's bytes: each wave streams blocks of 32 tokens from HBM to registers (no
+// LDS) and a block's waves share out the keys. attention_columns_kernel, for many,
+// is bound by instructions: a block's waves take columns of their own and share
+// the conversion of the codes through LDS.
 #include "kv.hpp"
 
 namespace btq {
@@ -25,21 +30,21 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
-constexpr int kTile = 128;                     // keys of a wave's step
-constexpr int kTileBlocks = kTile / kBlockTokens;
 constexpr float kNegInf = -INFINITY;
 
 __device__ __forceinline__ v4f mfma(v8b a, v8b b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// 8 codes of a dword as bf16 128 + code, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ v8b codes_to_bf16(uint32_t w) {
+// 8 codes of a dword as bf16 128 + code, in the order 0 4 1 5 2 6 3 7. `magic` is
+// 0x43004300 in a register: and-or takes one constant only.
+__device__ __forceinline__ v4u codes_to_bf16(uint32_t w, uint32_t magic) {
   v4u r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
-  return __builtin_bit_cast(v8b, r);
+  for (int j = 0; j < 4; ++j) r[j] = ((w >> (4 * j)) & 0x000f000fu) | magic;
+  return r;
 }
+__device__ __forceinline__ v8b as_bf16(v4u w) { return __builtin_bit_cast(v8b, w); }
 // 8 bf16 in that order.
 __device__ __forceinline__ v8b deal(v4u w) {
   v4u r;
@@ -73,23 +78,676 @@ __device__ __forceinline__ float column_sum(float v) {
   return column_combine(v, [](float a, float b) { return a + b; });
 }
 
-// A launch item: columns [col0, col0 + ncols) of a sequence and a key head.
-struct Item {
+// Keeps a uniform branch a branch: without it the compiler turns short ones into
+// selects that every pass pays for.
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+template <int kBegin, int kEnd, int kStep, typename F>
+__device__ __forceinline__ void static_for(F f) {
+  if constexpr (kBegin < kEnd) {
+    f(Int<kBegin>{});
+    static_for<kBegin + kStep, kEnd, kStep>(f);
+  }
+}
+
+// ---- what a wave keeps of its columns: 16*NT of them, column n*16 + lane%16 in
+// the 4 lanes of that number ----
+template <int D, int NT>
+struct Columns {
+  static constexpr int NS = D / 32, ND = D / 16;
+  v8b q[NT][NS];             // operand B of the first product
+  float qsum[NT];
+  int lo[NT], hi[NT];        // keys that the column sees
+  v4f o[NT][ND], oz[NT];     // sums of p*s'*(128 + code) of 4 features, and of p*s'*(128 + z')
+  float m2[NT], l[NT];       // running maximum times scale*log2(e); sum of p of this lane's keys
+  int all_lo, all_hi;        // keys that every column sees
+  int any_lo, any_hi;        // keys that some column sees
+
+  // Columns [col0, col0 + 16*NT) of a sequence, of which those below cols exist.
+  __device__ __forceinline__ void load(const AttnArgs& a, const SeqRange& s, int64_t shard, int head,
+                                       int col0, int cols) {
+    const int lane = threadIdx.x & 63, cl = lane & 15, g = lane >> 4;
+    const int last = (min(col0 + 16 * NT, cols) - 1) / a.G, first = col0 / a.G;
+    all_hi = a.causal ? min(s.first() + first + 1, s.length) : s.length;
+    all_lo = a.window ? s.first() + last + 1 - a.window : 0;
+    any_hi = a.causal ? clamp_int(s.first() + last + 1, 0, s.length) : s.length;
+    any_lo = a.window ? max(s.first() + first + 1 - a.window, 0) : 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = col0 + n * 16 + cl;
+      const bool live = col < cols;
+      const int qi = live ? col / a.G : 0, pos = s.first() + qi;
+      hi[n] = a.causal ? min(pos + 1, s.length) : s.length;
+      lo[n] = a.window ? max(pos + 1 - a.window, 0) : 0;
+      const uint16_t* row = (const uint16_t*)a.q.p + shard * a.q.shard +
+                            (s.begin + (int64_t)qi) * a.q.pitch +
+                            (head * (int64_t)a.G + (live ? col - qi * a.G : 0)) * a.q.head +
+                            g * (D / 4);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        v4u w;
+        if (a.q_on16) {
+          w = *(const v4u*)(row + 8 * i);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = row[8 * i + 2 * j] | (uint32_t)row[8 * i + 2 * j + 1] << 16;
+        }
+        if (!live) w = v4u{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
+        q[n][i] = deal(w);
+      }
+      qsum[n] = column_sum(sum);
+      oz[n] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[n][d] = v4f{0, 0, 0, 0};
+      m2[n] = kNegInf;
+      l[n] = 0.0f;
+    }
+  }
+
+  // Scores t (value k is a key of the lane's) to weights p; l and the sums follow
+  // the running maximum. It is raised only when a new one is 8 powers of 2 above
+  // it: p stays below 2^8, and the sums are rarely rescaled.
+  template <int kValues>
+  __device__ __forceinline__ void weights(const AttnArgs& a, float (&t)[NT][kValues]) {
+    float top[NT];
+    bool raise = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float m = t[n][0];
+#pragma unroll
+      for (int k = 1; k < kValues; ++k) m = fmaxf(m, t[n][k]);
+      top[n] = column_max(m) * a.scale2;
+      raise |= top[n] > m2[n] + 8.0f || (m2[n] == kNegInf && top[n] > kNegInf);
+    }
+    if (__ballot(raise)) {
+      keep_branch();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float m = fmaxf(m2[n], top[n]);
+        const float f = m == kNegInf ? 1.0f : exp2f(m2[n] - m);
+        m2[n] = m;
+        l[n] *= f;
+        oz[n] *= f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[n][d] *= f;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float off = m2[n] == kNegInf ? 0.0f : m2[n];
+#pragma unroll
+      for (int k = 0; k < kValues; ++k) {
+        t[n][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(t[n][k], a.scale2, -off));   // hidden: 0
+        l[n] += t[n][k];
+      }
+    }
+  }
+};
+
+// The 8 weights p*s' of a lane's keys 0 .. 7 (values 4*h + i) as operand B.
+__device__ __forceinline__ v8b weights_to_bf16(const float* p) {
+  v4u w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16x2(p[i], p[4 + i]);
+  return as_bf16(w);
+}
+
+// ---- results ----
+__device__ __forceinline__ void store_out2(const AttnArgs& a, int64_t at, float x, float y) {
+  if (a.out_type == kBf16)
+    *(uint32_t*)((uint16_t*)a.out + at) = f32_to_bf16x2(x, y);
+  else
+    *(float2*)((float*)a.out + at) = make_float2(x, y);
+}
+// Row of out and lse of a column.
+__device__ __forceinline__ int64_t out_row(const AttnArgs& a, const SeqRange& s, int64_t shard,
+                                           int head, int col) {
+  return (shard * a.kv.T + s.begin + col / a.G) * a.Hq + head * a.G + col % a.G;
+}
+// Factor of sums relative to the maximum m2 when they join others under m. Where
+// no score was above -Inf the sum of p is 0, or NaN if the scores were.
+__device__ __forceinline__ float share(float m2, float sum, float m) {
+  return m2 == kNegInf ? sum : exp2f(m2 - m);
+}
+__device__ __forceinline__ float lse_of(float m2, float l) {
+  return l > 0.0f || l != l ? 0.6931471805599453f * (m2 + log2f(l)) : kNegInf;
+}
+// Partial results of `cols` columns: rows of D sums, then (maximum, sum of p) pairs.
+struct Partial {
+  float* sums;
+  float* stats;
+};
+__device__ __forceinline__ Partial partial(const AttnArgs& a, int64_t slot, int64_t slots, int cols,
+                                           int D) {
+  return {a.ws + slot * cols * D, a.ws + slots * cols * D + slot * cols * 2};
+}
+
+// ---- few columns: waves share out the keys ----
+//
+// A wave takes 128 keys (4 blocks) a step: 16-byte loads of keys and values,
+// 17 KB in flight a wave while the step before is computed, its page numbers a
+// step earlier.
+constexpr int kTile = 128;
+constexpr int kTileBlocks = kTile / kBlockTokens;
+
+template <int D, int NT, int kTeam, bool kStream>
+struct KeysShape {
+  static constexpr int C = 16 * NT;
+  static constexpr int kShift = NT == 1 ? 4 : 5;
+  static constexpr int kChunkMax = 128 * 4 / (kTeam * NT);   // features of a round of the join
+  static constexpr int kChunk = D < kChunkMax ? D : kChunkMax;
+};
+
+template <int D, int NT>
+struct KeysWave {
+  static constexpr int NS = D / 32, ND = D / 16;
+  Columns<D, NT> c;
+  const AttnArgs& a;
   int b, head;
   int64_t shard;
-  SeqRange seq;
-  int col0;
+  uint32_t magic;
+  uint32_t k[4][2][NS], kw[2], vw[2];
+  v4u v[ND];
+
+  __device__ __forceinline__ explicit KeysWave(const AttnArgs& args) : a(args) {
+    magic = 0x43004300u;
+    opaque(magic);
+  }
+  // Page number of block `i` of a tile, and its place in the cache. A block that is
+  // not there reads the cache's first one, and the mask hides it.
+  __device__ __forceinline__ int page(int tile, int i) const {
+    const int slot = (tile * kTileBlocks + i) >> a.kv.page_shift;
+    return a.kv.table[(int64_t)b * a.kv.max_pages + min(slot, (int)a.kv.max_pages - 1)];
+  }
+  __device__ __forceinline__ bool place(int tile, int end, int i, int page, int64_t* at) const {
+    const int block = tile * kTileBlocks + i, shift = a.kv.page_shift;
+    const bool there = tile < end && (block >> shift) < a.kv.max_pages && page >= 0 && page < a.kv.pages;
+    const int64_t in_page = block & ((1 << shift) - 1);
+    *at = there ? ((((shard * a.kv.pages + page) * a.kv.Hk + head) << shift) + in_page) *
+                      kv_block_bytes(D)
+                : 0;
+    return there;
+  }
+
+  // Tiles begin, begin + step, .. of [begin, end).
+  __device__ __forceinline__ void run(int begin, int end, int step) {
+    if (begin >= end) return;
+    const int lane = threadIdx.x & 63, cl = lane & 15, g = lane >> 4;
+    int pk = page(begin, cl / 4), pv = page(begin, g);
+    int64_t kat, vat;
+    place(begin, end, cl / 4, pk, &kat);
+    bool there = place(begin, end, g, pv, &vat);
+    pk = page(begin + step, cl / 4), pv = page(begin + step, g);
+    load_keys(kat);
+    load_words(vat, kw, vw);
+    load_values(vat);
+    for (int tile = begin; tile < end; tile += step) {
+      const int key0 = tile * kTile;
+      const bool full = key0 >= c.all_lo && key0 + kTile <= c.all_hi && __ballot(!there) == 0;
+      place(tile + step, end, cl / 4, pk, &kat);
+      const bool there_next = place(tile + step, end, g, pv, &vat);
+      pk = page(tile + 2 * step, cl / 4), pv = page(tile + 2 * step, g);
+      uint32_t kw_next[2], vw_next[2];
+      load_words(vat, kw_next, vw_next);
+      compute(kat, vat, key0, there, __builtin_amdgcn_readfirstlane(!full));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) kw[j] = kw_next[j], vw[j] = vw_next[j];
+      there = there_next;
+    }
+  }
+  __device__ __forceinline__ void load_keys(int64_t at) {
+    const int lane = threadIdx.x & 63, cl = lane & 15, g = lane >> 4;
+    const uint8_t* p = a.kv.cache + at + g * (D / 8) + (cl & 3) * (D / 2);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) __builtin_memcpy(k[s][h], p + (8 * s + 4 * h) * (D / 2), 4 * NS);
+  }
+  // words of keys and values 2*cl and 2*cl + 1 of the lane's block
+  __device__ __forceinline__ void load_words(int64_t at, uint32_t (&x)[2], uint32_t (&y)[2]) {
+    const uint8_t* p = a.kv.cache + at + 32 * D + (threadIdx.x & 15) * 8;
+    __builtin_memcpy(x, p, 8);
+    __builtin_memcpy(y, p + 128, 8);
+  }
+  __device__ __forceinline__ void load_values(int64_t at) {
+    const uint8_t* p = a.kv.cache + at + 16 * D + (threadIdx.x & 15) * 16;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) v[d] = *(const v4u*)(p + d * 256);
+  }
+
+  // One tile; the next one's keys load when the first product is done with these,
+  // its values after the second.
+  __device__ __forceinline__ void compute(int64_t kat, int64_t vat, int key0, bool there, int mask) {
+    constexpr int KS = NT == 1 ? 2 : 1;   // steps of 32 keys whose scores are held at once
+    const int base = key0 + ((threadIdx.x & 63) >> 4) * kBlockTokens;
+    static_for<0, 4, KS>([&](auto first) {
+      constexpr int S0 = decltype(first)::value;
+      float t[NT][8 * KS];
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          v4f acc[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) acc[n] = v4f{0, 0, 0, 0};
+#pragma unroll
+          for (int w = 0; w < NS; ++w) {
+            const v8b kc = as_bf16(codes_to_bf16(k[S0 + s][h][w], magic));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[n] = mfma(kc, c.q[n][w], acc[n]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[n][8 * s + 4 * h + i] = acc[n][i];
+          issue_fence();   // (else the scheduler converts all codes at once, and spills)
+        }
+      if constexpr (S0 + KS == 4) {
+        load_keys(kat);
+        issue_fence();
+      }
+      static_for<0, 4 * KS, 1>([&](auto pair) {
+        constexpr int kPair = decltype(pair)::value;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t w = row_lane<4 * S0 + kPair>(kw[j]);
+          const float ks = __uint_as_float(w & 0xffff0000u), kz = __uint_as_float(w << 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float& x = t[n][2 * kPair + j];
+            x = __builtin_fmaf(-kz, c.qsum[n], x) * ks;
+          }
+        }
+      });
+      auto hide = [&](float (&x)[NT][8 * KS], float with) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int from = there ? c.lo[n] - base - 8 * S0 : 32, to = c.hi[n] - base - 8 * S0;
+#pragma unroll
+          for (int key = 0; key < 8 * KS; ++key)
+            x[n][key] = key >= from && key < to ? x[n][key] : with;
+        }
+      };
+      if (mask) {
+        keep_branch();
+        hide(t, kNegInf);
+      }
+      c.weights(a, t);
+      uint32_t z[4 * KS];
+      static_for<0, 4 * KS, 1>([&](auto pair) {
+        constexpr int kPair = decltype(pair)::value;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int key = 2 * kPair + j;
+          const uint32_t w = row_lane<4 * S0 + kPair>(vw[j]);
+          const float vs = __uint_as_float(w & 0xffff0000u);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) t[n][key] *= vs;
+          // 128 + z of keys i (low half) and 4 + i; whatever stands in a place that
+          // holds no value, it is a number
+          uint32_t& zz = z[(key >> 3) * 4 + (key & 3)];
+          if ((key & 4) == 0)
+            zz = (w & 0xfu) | magic;
+          else
+            zz |= (w & 0xfu) << 16;
+        }
+      });
+      if (mask) {   // the scale of a hidden value may be NaN
+        keep_branch();
+        hide(t, 0.0f);
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        v8b p[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          p[n] = weights_to_bf16(&t[n][8 * s]);
+          c.oz[n] = mfma(as_bf16(v4u{z[4 * s], z[4 * s + 1], z[4 * s + 2], z[4 * s + 3]}), p[n], c.oz[n]);
+        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const v8b vc = as_bf16(codes_to_bf16(v[d][S0 + s], magic));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) c.o[n][d] = mfma(vc, p[n], c.o[n][d]);
+          if (d % 2 == 1) issue_fence();
+        }
+      }
+    });
+    load_values(vat);
+    issue_fence();
+  }
+};
+
+// Tiles of a sequence's columns, from its rows' first key to their last; one at
+// least where there are columns, so that rows that see nothing are written too.
+// (All column tiles count the same; a mask hides what a causal one does not see.)
+struct SeqTiles {
+  int first, tiles, groups;   // first tile, tiles, column groups of 2^shift
+};
+__device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, const SeqRange& s, int shift) {
+  SeqTiles r;
+  const int64_t cols = (int64_t)s.n * a.G;
+  r.groups = (int)((cols + (1 << shift) - 1) >> shift);
+  const int hi = s.length;
+  const int lo = a.window ? min(max(s.first() + 1 - a.window, 0), max(hi - 1, 0)) : 0;
+  r.first = lo / kTile;
+  r.tiles = max((hi + kTile - 1) / kTile - r.first, 1);
+  return r;
+}
+
+// The work of a launch laid out flat: head after head, sequence after sequence,
+// column group after group, tile after tile.
+struct Flat {
+  int64_t per_head;   // tiles of a head
+  int b;              // the sequence that holds position `at` of a head, and
+  int64_t begin;      // where its tiles begin
+};
+template <int kThreads>
+__device__ __forceinline__ int64_t flat_total(const AttnArgs& a, int shift, int64_t* lds, int64_t* mine,
+                                              int* b0, int* b1) {
+  const int each = (a.kv.B + kThreads - 1) / kThreads;
+  *b0 = min((int)threadIdx.x * each, a.kv.B);
+  *b1 = min(*b0 + each, a.kv.B);
+  int64_t sum = 0;
+  for (int b = *b0; b < *b1; ++b) {
+    const SeqTiles t = seq_tiles(a, seq_range(a.kv, b), shift);
+    sum += (int64_t)t.groups * t.tiles;
+  }
+  int64_t inc = sum;   // inclusive sum over the wave
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t v = __shfl_up(inc, d);
+    if ((int)(threadIdx.x & 63) >= d) inc += v;
+  }
+  if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = inc;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kThreads / 64; ++w) {
+    if (w < (int)threadIdx.x >> 6) before += lds[w];
+    total += lds[w];
+  }
+  *mine = before + inc - sum;
+  return total;
+}
+template <int kThreads>
+__device__ __forceinline__ void flat_find(const AttnArgs& a, int shift, int64_t at, int64_t mine, int b0,
+                                          int b1, Flat* out) {
+  for (int b = b0; b < b1; ++b) {
+    const SeqTiles t = seq_tiles(a, seq_range(a.kv, b), shift);
+    const int64_t n = (int64_t)t.groups * t.tiles;
+    if (at >= mine && at < mine + n) {
+      out->b = b;
+      out->begin = mine;
+    }
+    mine += n;
+  }
+}
+// Tiles of a block: an equal share of all, and a step for each wave at least.
+__device__ __forceinline__ int64_t flat_share(int64_t all, int64_t blocks, int team) {
+  const int64_t n = (all + blocks - 1) / blocks;
+  return n < team ? team : n;
+}
+
+// The team's sums, each relative to the common maximum, added in the waves' order;
+// to `out` where they are whole, else to a partial result.
+template <int D, int NT, int kTeam, bool kStream>
+__device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, NT>& c, const SeqRange& seq,
+                                          int64_t shard, int head, int col0, int cols, bool whole,
+                                          const Partial& part) {
+  using S = KeysShape<D, NT, kTeam, kStream>;
+  __shared__ float stat[kTeam][S::C][2];
+  __shared__ float sums[kTeam][S::C][S::kChunk + 4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const float sum = column_sum(c.l[n]);
+    if (g == 0) {
+      stat[wave][n * 16 + cl][0] = c.m2[n];
+      stat[wave][n * 16 + cl][1] = sum;
+    }
+  }
+  lds_barrier();
+  auto top = [&](int col) {
+    float m = stat[0][col][0];
+#pragma unroll
+    for (int w = 1; w < kTeam; ++w) m = fmaxf(m, stat[w][col][0]);
+    return m;
+  };
+  float f[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) f[n] = share(c.m2[n], stat[wave][n * 16 + cl][1], top(n * 16 + cl));
+#pragma unroll
+  for (int d0 = 0; d0 < D; d0 += S::kChunk) {
+    if (d0) lds_barrier();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+        if (d * 16 >= d0 && d * 16 < d0 + S::kChunk)
+          *(v4f*)&sums[wave][n * 16 + cl][d * 16 - d0 + g * 4] = (c.o[n][d] - c.oz[n]) * f[n];
+    lds_barrier();
+    const int width = min(S::kChunk, D - d0), live = min(S::C, cols - col0);
+    for (int i = threadIdx.x; i < live * (width / 2); i += 64 * kTeam) {
+      const int col = i / (width / 2), d = (i - col * (width / 2)) * 2;
+      const float m = top(col);
+      float sum = 0.0f, x = 0.0f, y = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kTeam; ++w) {
+        const float l = stat[w][col][1];
+        sum += l * share(stat[w][col][0], l, m);
+        const float2 v = *(const float2*)&sums[w][col][d];
+        x += v.x;
+        y += v.y;
+      }
+      if (whole) {
+        const int64_t at = out_row(a, seq, shard, head, col0 + col);
+        const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+        store_out2(a, at * D + d0 + d, x * r, y * r);
+        if (a.lse && d0 + d == 0) a.lse[at] = lse_of(m, sum);
+      } else {
+        *(float2*)(part.sums + (int64_t)col * D + d0 + d) = make_float2(x, y);
+        if (d0 + d == 0) {
+          part.stats[2 * col] = m;
+          part.stats[2 * col + 1] = sum;
+        }
+      }
+    }
+  }
+  if (kStream) lds_barrier();   // the next segment writes stat and sums again
+}
+
+// kStream: the flat order is cut into equal shares, one a block, so a batch of any
+// lengths fills the chip evenly; a group of columns that a cut divides leaves
+// partial results (slot 2*block + 1 where it begins in the block, else 2*block),
+// which attention_join_kernel adds. Else a block takes one group of columns.
+template <int D, int NT, int kTeam, bool kStream>
+__global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_kernel(AttnArgs a, int64_t first_block,
+                                                                       int64_t items) {
+  using S = KeysShape<D, NT, kTeam, kStream>;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t heads = a.kv.P * a.kv.Hk;
+  KeysWave<D, NT> w(a);
+  if constexpr (!kStream) {
+    const int64_t id = first_block + blockIdx.x, hk = id % heads;
+    int64_t sub;
+    w.b = find_sequence(a.kv, a.G, S::kShift, 1, id / heads, &sub);
+    if (w.b < 0) return;
+    const SeqRange seq = uniform(seq_range(a.kv, w.b));
+    const int cols = seq.n * a.G;
+    if ((sub << S::kShift) >= cols) return;
+    const int col0 = (int)sub << S::kShift;
+    w.shard = hk / a.kv.Hk;
+    w.head = (int)(hk % a.kv.Hk);
+    w.c.load(a, seq, w.shard, w.head, col0, cols);
+    w.run(w.c.any_lo / kTile + wave, (w.c.any_hi + kTile - 1) / kTile, kTeam);
+    join_team<D, NT, kTeam, kStream>(a, w.c, seq, w.shard, w.head, col0, cols, true, Partial{});
+  } else {
+    __shared__ int64_t scan[kTeam];
+    __shared__ Flat found;
+    int64_t mine;
+    int b0, b1;
+    const int64_t per_head =
+        uniform(flat_total<64 * kTeam>(a, S::kShift, scan, &mine, &b0, &b1));
+    const int64_t all = per_head * heads, each = flat_share(all, gridDim.x, kTeam);
+    const int64_t x0 = blockIdx.x * each, x1 = min(x0 + each, all);
+    if (x0 >= x1) return;
+    int64_t hk = x0 / per_head;
+    flat_find<64 * kTeam>(a, S::kShift, x0 - hk * per_head, mine, b0, b1, &found);
+    __syncthreads();
+    w.b = __builtin_amdgcn_readfirstlane(found.b);
+    int64_t begin = hk * per_head + uniform(found.begin);   // of sequence w.b of head hk
+    for (int64_t x = x0; x < x1;) {
+      const SeqRange seq = uniform(seq_range(a.kv, w.b));
+      const SeqTiles st = seq_tiles(a, seq, S::kShift);
+      const int64_t n = (int64_t)st.groups * st.tiles;
+      if (x >= begin + n) {   // on to the next sequence, or the next head's first
+        begin += n;
+        if (++w.b == a.kv.B) w.b = 0, ++hk;
+        continue;
+      }
+      const int group = (int)((x - begin) / st.tiles);
+      const int64_t unit = begin + (int64_t)group * st.tiles;
+      const int t0 = (int)(x - unit), t1 = (int)(min(x1, unit + st.tiles) - unit);
+      const int cols = seq.n * a.G, col0 = group << S::kShift;
+      w.shard = hk / a.kv.Hk;
+      w.head = (int)(hk % a.kv.Hk);
+      w.c.load(a, seq, w.shard, w.head, col0, cols);
+      w.run(st.first + t0 + wave, st.first + t1, kTeam);
+      join_team<D, NT, kTeam, kStream>(
+          a, w.c, seq, w.shard, w.head, col0, cols, t1 - t0 == st.tiles,
+          partial(a, 2 * (int64_t)blockIdx.x + (t0 == 0), 2 * (int64_t)gridDim.x, S::C, D));
+      x += t1 - t0;
+    }
+  }
+}
+
+// Adds the partial results of the group of columns that begins in the share of
+// block blockIdx.x and goes on past its end, if one does.
+constexpr int kJoinThreads = 1024;
+template <int D, int NT, int kTeam>
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a) {
+  using S = KeysShape<D, NT, kTeam, true>;
+  constexpr int kVec = D / 4;   // vectors of a row
+  __shared__ int64_t scan[kJoinThreads / 64];
+  __shared__ Flat found;
+  __shared__ int top[S::C];
+  __shared__ v4f sums[kJoinThreads];
+  __shared__ float ls[kJoinThreads];
+  const int64_t heads = a.kv.P * a.kv.Hk;
+  int64_t mine;
+  int b0, b1;
+  const int64_t per_head = flat_total<kJoinThreads>(a, S::kShift, scan, &mine, &b0, &b1);
+  const int64_t all = per_head * heads, each = flat_share(all, gridDim.x, kTeam);
+  const int64_t x0 = blockIdx.x * each, x1 = x0 + each;
+  if (x1 >= all) return;
+  const int64_t hk = (x1 - 1) / per_head;
+  flat_find<kJoinThreads>(a, S::kShift, x1 - 1 - hk * per_head, mine, b0, b1, &found);
+  if (threadIdx.x < S::C) top[threadIdx.x] = INT32_MIN;
+  __syncthreads();
+  const int b = found.b;
+  const SeqRange seq = uniform(seq_range(a.kv, b));
+  const SeqTiles st = seq_tiles(a, seq, S::kShift);
+  const int64_t begin = hk * per_head + found.begin;
+  const int group = (int)((x1 - 1 - begin) / st.tiles);
+  const int64_t unit = begin + (int64_t)group * st.tiles;
+  if (unit < x0 || unit + st.tiles <= x1) return;
+  const int parts = (int)((unit + st.tiles - 1) / each - blockIdx.x) + 1;
+  const int cols = seq.n * a.G, col0 = group << S::kShift, live = min(S::C, cols - col0);
+  const int64_t slots = 2 * (int64_t)gridDim.x;
+  auto part = [&](int p) {
+    return partial(a, 2 * ((int64_t)blockIdx.x + p) + (p == 0), slots, S::C, D);
+  };
+  // the largest maximum: floats as ordered integers (it does not depend on the order)
+  for (int i = threadIdx.x; i < parts * live; i += kJoinThreads) {
+    const int p = i / live, c = i - p * live;
+    const int v = __float_as_int(part(p).stats[2 * c]);
+    atomicMax(&top[c], v < 0 ? v ^ 0x7fffffff : v);
+  }
+  __syncthreads();
+  // threads by (part of the partial results, column, 4 features)
+  const int vecs = live * kVec, teams = max(kJoinThreads / vecs, 1);
+  const int span = (parts + teams - 1) / teams;
+  for (int i0 = 0; i0 < vecs; i0 += kJoinThreads) {
+    const int team = vecs >= kJoinThreads ? 0 : (int)threadIdx.x / vecs;
+    const int i = i0 + (vecs >= kJoinThreads ? (int)threadIdx.x : (int)threadIdx.x - team * vecs);
+    const int c = i / kVec, d = (i - c * kVec) * 4;
+    const bool mine_is = team < teams && i < vecs;
+    v4f x = {0, 0, 0, 0};
+    float sum = 0.0f;
+    if (mine_is) {
+      const int v = top[c];
+      const float m = __int_as_float(v < 0 ? v ^ 0x7fffffff : v);
+      const int end = min((team + 1) * span, parts);
+#pragma unroll 8
+      for (int p = team * span; p < end; ++p) {
+        const Partial q = part(p);
+        const float l = q.stats[2 * c + 1], f = share(q.stats[2 * c], l, m);
+        const v4f y = *(const v4f*)(q.sums + (int64_t)c * D + d);
+        sum += l * f;
+        x += y * f;
+      }
+    }
+    if (teams > 1) {
+      sums[threadIdx.x] = x;
+      ls[threadIdx.x] = sum;
+      __syncthreads();
+      if (mine_is && team == 0)
+        for (int t = 1; t < teams; ++t) {
+          x += sums[t * vecs + i];
+          sum += ls[t * vecs + i];
+        }
+    }
+    if (mine_is && team == 0) {
+      const int64_t at = out_row(a, seq, hk / a.kv.Hk, (int)(hk % a.kv.Hk), col0 + c);
+      const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+      store_out2(a, at * D + d, x[0] * r, x[1] * r);
+      store_out2(a, at * D + d + 2, x[2] * r, x[3] * r);
+      if (a.lse && d == 0) {
+        const int v = top[c];
+        a.lse[at] = lse_of(__int_as_float(v < 0 ? v ^ 0x7fffffff : v), sum);
+      }
+    }
+  }
+}
+
+// ---- many columns: a block's 4 waves take 16*NT columns each ----
+//
+// A tile of 64 keys goes from HBM through registers, as bf16 128 + code, to LDS, in
+// the order in which the matrix instructions' operands are read: 64 lanes of 16
+// consecutive bytes. Two tiles of LDS: while one is used the next is converted,
+// and the one after is on its way from memory.
+constexpr int kColsTile = 64;
+
+template <int D, int NT>
+struct ColsShape {
+  static constexpr int NS = D / 32, ND = D / 16, C = 16 * NT, kCols = 4 * C;
+  static constexpr int kShift = NT == 1 ? 6 : 7;
+  static constexpr int kKeyFrags = 4 * NS, kValueFrags = 2 * ND;   // of 1 KB
+  static constexpr int VN = (2 * D + 255) / 256;                   // value rows a thread
+  struct Buffer {
+    v4u k[kKeyFrags][64], v[kValueFrags][64];
+    float ks[64], kz[64], vs[64];
+    uint16_t vz[64];
+  };
 };
 
 // The keys of split `split`, in tiles: an equal share of the tiles that the item's
 // columns see, no split shorter than kMinTiles.
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 8;
 struct KeyTiles {
   int begin, end;   // this split's
   int splits;       // those that have any
 };
 __device__ __forceinline__ KeyTiles key_tiles(int lo, int hi, int split, int splits) {
-  const int t0 = lo / kTile, t1 = (hi + kTile - 1) / kTile;
+  const int t0 = lo / kColsTile, t1 = (hi + kColsTile - 1) / kColsTile;
   const int n = max(t1 - t0, 0);
   const int each = max((n + splits - 1) / splits, kMinTiles);
   KeyTiles k;
@@ -106,151 +764,105 @@ __device__ __forceinline__ void keys_seen(const AttnArgs& a, const SeqRange& s, 
   *lo = a.window ? min(max(first + 1 - a.window, 0), *hi) : 0;
 }
 
-template <int D, int NT, bool kKeys>
-struct AttnShape {
-  static constexpr int C = 16 * NT;                    // columns of a wave
-  static constexpr int kCols = kKeys ? C : 4 * C;      // of a block
-  static constexpr int kShift = (kKeys ? 4 : 6) + (NT == 1 ? 0 : NT == 2 ? 1 : 2);
-};
-
-// Partial results of a split: [item][split][column] rows of D sums, then as many
-// (maximum, sum of p) pairs.
-struct Partial {
-  float* sums;
-  float* stats;
-};
-__device__ __forceinline__ Partial partial(const AttnArgs& a, int64_t unit, int64_t units, int split,
-                                           int cols, int D) {
-  const int64_t row = (unit * a.splits + split) * cols;
-  return {a.ws + row * D, a.ws + units * a.splits * cols * D + row * 2};
-}
-
-__device__ __forceinline__ void store_out2(const AttnArgs& a, int64_t at, float x, float y) {
-  if (a.out_type == kBf16)
-    *(uint32_t*)((uint16_t*)a.out + at) = f32_to_bf16x2(x, y);
-  else
-    *(float2*)((float*)a.out + at) = make_float2(x, y);
-}
-__device__ __forceinline__ int64_t out_row(const AttnArgs& a, const Item& it, int col) {
-  return ((it.shard * a.kv.T + it.seq.begin + col / a.G) * a.Hq + it.head * a.G + col % a.G);
-}
-// Factor of sums relative to the maximum m2 when they join others under m. Where
-// no score was above -Inf the sum of p is 0, or NaN if the scores were.
-__device__ __forceinline__ float share(float m2, float sum, float m) {
-  return m2 == kNegInf ? sum : exp2f(m2 - m);
-}
-__device__ __forceinline__ float lse_of(float m2, float l) {
-  return l > 0.0f || l != l ? 0.6931471805599453f * (m2 + log2f(l)) : kNegInf;
-}
-
-template <int D, int NT, bool kKeys>
-__global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a, int64_t first_block,
-                                                           int64_t items) {
-  using S = AttnShape<D, NT, kKeys>;
-  constexpr int NS = D / 32, ND = D / 16, C = S::C;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int cl = lane & 15, g = lane >> 4;   // column (or tile row) and quarter of the wave
+template <int D, int NT>
+__global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, int64_t first_block,
+                                                                   int64_t items) {
+  using S = ColsShape<D, NT>;
+  constexpr int NS = S::NS, ND = S::ND, C = S::C;
+  __shared__ typename S::Buffer buf[2];
+  const int tid = threadIdx.x, lane = tid & 63, cl = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   const int64_t heads = a.kv.P * a.kv.Hk, id = first_block + blockIdx.x;
   const int64_t hk = id % heads, rest = id / heads;
   const int split = (int)(rest / items);
   // the last items of a causal batch see the most keys: they go first
-  const int64_t item_id = items - 1 - rest % items;
-  Item it;
-  it.shard = hk / a.kv.Hk;
-  it.head = (int)(hk % a.kv.Hk);
+  const int64_t item = items - 1 - rest % items;
+  const int64_t shard = hk / a.kv.Hk;
+  const int head = (int)(hk % a.kv.Hk);
   int64_t sub;
-  it.b = find_sequence(a.kv, a.G, S::kShift, 1, item_id, &sub);
-  if (it.b < 0) return;
-  it.seq = seq_range(a.kv, it.b);
-  const int cols = it.seq.n * a.G;
-  if (sub >= ((int64_t)cols + S::kCols - 1) / S::kCols) return;
-  it.col0 = (int)sub * S::kCols + (kKeys ? 0 : wave * C);
-  if (it.col0 >= cols) return;   // (a whole wave; no barrier follows where waves take columns)
-
-  const int col1 = min(it.col0 + C, cols);
+  const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub);
+  if (b < 0) return;
+  const SeqRange seq = uniform(seq_range(a.kv, b));
+  const int cols = seq.n * a.G;
+  if ((sub << S::kShift) >= cols) return;
+  const int block_col = (int)sub << S::kShift;
   int klo, khi;
-  keys_seen(a, it.seq, it.col0, col1, &klo, &khi);
+  keys_seen(a, seq, block_col, min(block_col + S::kCols, cols), &klo, &khi);
   const KeyTiles kt = key_tiles(klo, khi, split, a.splits);
   if (split >= kt.splits) return;
 
-  // the queries: operand B of the first product, and their sums
-  v8b q[NT][NS];
-  float qsum[NT];
-  int lo[NT], hi[NT];
+  const int col0 = block_col + wave * C;
+  const bool live = col0 < cols;    // a wave without columns loads and waits with the others
+  Columns<D, NT> c;
+  c.load(a, seq, shard, head, live ? col0 : block_col, cols);
+  uint32_t magic = 0x43004300u;
+  opaque(magic);
+
+  // loads: a thread takes a quarter (wave) of a key's row, and rows of values
+  const int kq = lane >> 4, krow = 8 * ((lane & 15) >> 2) + 4 * (kq & 1) + (lane & 3);
+  uint32_t kreg[NS], word = 0;
+  v4u vreg[S::VN];
+  auto load = [&](int tile) {
+    const int t = min(tile, kt.end - 1);
+    int64_t at[2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int col = it.col0 + n * 16 + cl;
-    const int qi = col / a.G, pos = it.seq.first() + qi;
-    hi[n] = a.causal ? min(pos + 1, it.seq.length) : it.seq.length;
-    lo[n] = a.window ? max(pos + 1 - a.window, 0) : 0;
-    const bool live = col < cols;
-    const uint16_t* row = (const uint16_t*)a.q.p + it.shard * a.q.shard +
-                          (it.seq.begin + (int64_t)(live ? qi : 0)) * a.q.pitch +
-                          (it.head * (int64_t)a.G + (live ? col % a.G : 0)) * a.q.head + g * (D / 4);
-    float sum = 0.0f;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      v4u w;
-      if (a.q_on16) {
-        w = *(const v4u*)(row + 8 * s);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = row[8 * s + 2 * j] | (uint32_t)row[8 * s + 2 * j + 1] << 16;
-      }
-      if (!live) w = v4u{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
-      q[n][s] = deal(w);
+    for (int j = 0; j < 2; ++j) {
+      const int64_t x = kv_block(a.kv, b, shard, head, 2 * t + j);
+      at[j] = x;
     }
-    qsum[n] = column_sum(sum);
-  }
-  // keys that every column sees, for the tiles that need no mask
-  const int all_hi = a.causal ? it.seq.first() + it.col0 / a.G + 1 : it.seq.length;
-  const int all_lo = a.window ? it.seq.first() + (col1 - 1) / a.G + 1 - a.window : 0;
-
-  v4f o[NT][ND], oz[NT];
-  float m2[NT], l[NT];   // running maximum times scale*log2(e), sum of p of this lane's keys
+    const int64_t ka = at[kq >> 1] < 0 ? 0 : at[kq >> 1];
+    __builtin_memcpy(kreg, a.kv.cache + ka + krow * (D / 2) + wave * (D / 8), 4 * NS);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    oz[n] = v4f{0, 0, 0, 0};
+    for (int i = 0; i < S::VN; ++i) {
+      const int r = min(i * 256 + tid, 2 * D - 1);
+      const int64_t va = r < D ? at[0] : at[1];
+      vreg[i] = *(const v4u*)(a.kv.cache + (va < 0 ? 0 : va) + 16 * D + (r < D ? r : r - D) * 16);
+    }
+    // words: waves 0 and 1 those of keys and of values
+    const int64_t wa = lane < 32 ? at[0] : at[1];
+    if (wave < 2) {
+      word = *(const uint32_t*)(a.kv.cache + (wa < 0 ? 0 : wa) + 32 * D + 128 * wave + (lane & 31) * 4);
+      // a place that holds nothing: 0, so that it stays a number
+      if (wa < 0 || t * kColsTile + lane >= seq.length) word = kZeroWord;
+    }
+  };
+  auto write = [&](typename S::Buffer& o) {
 #pragma unroll
-    for (int d = 0; d < ND; ++d) o[n][d] = v4f{0, 0, 0, 0};
-    m2[n] = kNegInf;
-    l[n] = 0.0f;
-  }
-
-  constexpr int kStep = kKeys ? 4 : 1;
-  for (int tile = kt.begin + (kKeys ? wave : 0); tile < kt.end; tile += kStep) {
-    const int64_t vb = kv_block(a.kv, it.b, it.shard, it.head, tile * kTileBlocks + g);
-    const int64_t kb = kv_block(a.kv, it.b, it.shard, it.head, tile * kTileBlocks + cl / 4);
-    // a block without a page reads the cache's first one; the mask hides it
-    const uint8_t* vp = a.kv.cache + (vb < 0 ? 0 : vb);
-    const uint8_t* kp = a.kv.cache + (kb < 0 ? 0 : kb) + g * (D / 8) + (cl & 3) * (D / 2);
-    uint32_t k[4][2][NS];
+    for (int w = 0; w < NS; ++w) o.k[kq * NS + w][wave * 16 + (lane & 15)] = codes_to_bf16(kreg[w], magic);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int i = 0; i < S::VN; ++i) {
+      const int r = i * 256 + tid;
+      if (2 * D % 256 != 0 && r >= 2 * D) break;
+      const int j = r < D ? 0 : 1, d = r < D ? r : r - D;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        __builtin_memcpy(k[s][h], kp + (8 * s + 4 * h) * (D / 2), 4 * NS);
-    // words of keys and values 2*cl and 2*cl + 1 of the lane's block
-    uint32_t kw[2], vw[2];
-    __builtin_memcpy(kw, vp + 32 * D + cl * 8, 8);
-    __builtin_memcpy(vw, vp + 32 * D + 128 + cl * 8, 8);
-    v4u v[ND];
+      for (int q = 0; q < 4; ++q)
+        o.v[j * ND + (d >> 4)][q * 16 + (d & 15)] = codes_to_bf16(vreg[i][q], magic);
+    }
+    if (wave == 0) {
+      o.ks[lane] = __uint_as_float(word & 0xffff0000u);
+      o.kz[lane] = __uint_as_float(word << 16);
+    } else if (wave == 1) {
+      o.vs[lane] = __uint_as_float(word & 0xffff0000u);
+      o.vz[(lane & 32) + (lane & 24) + (lane & 3) * 2 + ((lane >> 2) & 1)] = (uint16_t)word;
+    }
+  };
+  auto compute = [&](const typename S::Buffer& in, int key0, int mask) {
+    float t[NT][16];
+    auto hide = [&](float with) {
+      const int64_t b0 = kv_block(a.kv, b, shard, head, key0 / 32);
+      const int64_t b1 = kv_block(a.kv, b, shard, head, key0 / 32 + 1);
 #pragma unroll
-    for (int d = 0; d < ND; ++d) v[d] = *(const v4u*)(vp + 16 * D + (d * 16 + cl) * 16);
-
-    const int key0 = tile * kTile;
-    const bool full = key0 >= all_lo && key0 + kTile <= all_hi && __ballot(vb < 0) == 0;
-
-    // scores of 32 keys a lane and column: step s, half h, value i is the key
-    // 8s + 4h + i of the lane's block
-    float t[NT][4][2][4];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+        for (int k = 0; k < 16; ++k) {
+          const int key = key0 + (k >> 3) * 32 + g * 8 + (k & 7);
+          const bool seen = key >= c.lo[n] && key < c.hi[n] && (k < 8 ? b0 : b1) >= 0;
+          t[n][k] = seen ? t[n][k] : with;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         v4f acc[NT];
@@ -258,288 +870,184 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a, int64_t f
         for (int n = 0; n < NT; ++n) acc[n] = v4f{0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < NS; ++w) {
-          const v8b kc = codes_to_bf16(k[s][h][w]);
+          const v8b kc = as_bf16(in.k[(j * 2 + h) * NS + w][lane]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) acc[n] = mfma(kc, q[n][w], acc[n]);
+          for (int n = 0; n < NT; ++n) acc[n] = mfma(kc, c.q[n][w], acc[n]);
         }
+        const v4f ks = *(const v4f*)&in.ks[j * 32 + g * 8 + h * 4];
+        const v4f kz = *(const v4f*)&in.kz[j * 32 + g * 8 + h * 4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) t[n][s][h][i] = acc[n][i];
+          for (int i = 0; i < 4; ++i)
+            t[n][8 * j + 4 * h + i] = __builtin_fmaf(-kz[i], c.qsum[n], acc[n][i]) * ks[i];
+        issue_fence();
       }
-    auto each_key = [&](auto f) {
-      f(std::integral_constant<int, 0>{}); f(std::integral_constant<int, 1>{});
-      f(std::integral_constant<int, 2>{}); f(std::integral_constant<int, 3>{});
-      f(std::integral_constant<int, 4>{}); f(std::integral_constant<int, 5>{});
-      f(std::integral_constant<int, 6>{}); f(std::integral_constant<int, 7>{});
-      f(std::integral_constant<int, 8>{}); f(std::integral_constant<int, 9>{});
-      f(std::integral_constant<int, 10>{}); f(std::integral_constant<int, 11>{});
-      f(std::integral_constant<int, 12>{}); f(std::integral_constant<int, 13>{});
-      f(std::integral_constant<int, 14>{}); f(std::integral_constant<int, 15>{});
-    };
-    each_key([&](auto pair) {
-      constexpr int kPair = decltype(pair)::value;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        constexpr int kKey0 = 2 * kPair;
-        const int key = kKey0 + j;
-        const uint32_t w = row_lane<kPair>(kw[j]);
-        const float ks = __uint_as_float(w & 0xffff0000u), kz = __uint_as_float(w << 16);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float& x = t[n][key >> 3][(key >> 2) & 1][key & 3];
-          x = __builtin_fmaf(-kz, qsum[n], x) * ks;
-        }
-      }
-    });
-    if (!full) {
-      const int base = key0 + g * kBlockTokens;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int from = vb < 0 ? kBlockTokens : lo[n] - base, to = hi[n] - base;
-#pragma unroll
-        for (int key = 0; key < 32; ++key) {
-          float& x = t[n][key >> 3][(key >> 2) & 1][key & 3];
-          x = key >= from && key < to ? x : kNegInf;
-        }
-      }
+    if (mask) {
+      keep_branch();
+      hide(kNegInf);
     }
-    // the running maximum is raised only when a new one is 8 powers of 2 above it:
-    // p then stays below 2^8, and the sums are rarely rescaled
-    float alpha[NT];
-    bool raise = false;
+    c.weights(a, t);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float m = kNegInf;
-#pragma unroll
-      for (int key = 0; key < 32; ++key) m = fmaxf(m, t[n][key >> 3][(key >> 2) & 1][key & 3]);
-      alpha[n] = column_max(m) * a.scale2;
-      raise |= alpha[n] > m2[n] + 8.0f || (m2[n] == kNegInf && alpha[n] > kNegInf);
-    }
-    if (__ballot(raise)) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float m = fmaxf(m2[n], alpha[n]);
-        const float f = m == kNegInf ? 1.0f : exp2f(m2[n] - m);
-        m2[n] = m;
-        l[n] *= f;
-        oz[n] *= f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o[n][d] *= f;
-      }
-    }
-    // p, and the second product 8 keys of each block at a time
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float off = m2[n] == kNegInf ? 0.0f : m2[n];
-#pragma unroll
-      for (int key = 0; key < 32; ++key) {
-        float& x = t[n][key >> 3][(key >> 2) & 1][key & 3];
-        x = __builtin_amdgcn_exp2f(__builtin_fmaf(x, a.scale2, -off));   // hidden: 0
-        l[n] += x;
-      }
-    }
-    uint32_t zrow[16];
-    each_key([&](auto pair) {
-      constexpr int kPair = decltype(pair)::value;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int key = 2 * kPair + j;
-        const uint32_t w = row_lane<kPair>(vw[j]);
-        const float vs = __uint_as_float(w & 0xffff0000u);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float& x = t[n][key >> 3][(key >> 2) & 1][key & 3];
-          // a hidden value's scale may be NaN
-          x = !full && x == 0.0f ? 0.0f : x * vs;
-        }
-        // 128 + z of keys i (low half) and 4 + i; whatever stands in a place that
-        // holds no value, it is a number
-        uint32_t& pair_z = zrow[(key >> 3) * 4 + (key & 3)];
-        if ((key & 4) == 0)
-          pair_z = (w & 0xfu) | 0x43004300u;
-        else
-          pair_z |= (w & 0xfu) << 16;
-      }
-    });
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      v8b p[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        v4u w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16x2(t[n][s][0][i], t[n][s][1][i]);
-        p[n] = __builtin_bit_cast(v8b, w);
-      }
-      const v4u zw = {zrow[4 * s], zrow[4 * s + 1], zrow[4 * s + 2], zrow[4 * s + 3]};
-      const v8b z = __builtin_bit_cast(v8b, zw);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) oz[n] = mfma(z, p[n], oz[n]);
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const v8b vc = codes_to_bf16(v[d][s]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][d] = mfma(vc, p[n], o[n][d]);
-      }
-    }
-  }
-
-  const int64_t unit = item_id * heads + hk, units = items * heads;
-  if constexpr (!kKeys) {
-    const Partial part = partial(a, unit, units, split, S::kCols, D);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = it.col0 + n * 16 + cl;
-      const float sum = column_sum(l[n]);
-      if (col >= cols) continue;
-      const int pc = wave * C + n * 16 + cl;
-      const float f = kt.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int64_t at = kt.splits > 1 ? 0 : out_row(a, it, col);
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const v4f x = (o[n][d] - oz[n]) * f;
-        const int f0 = d * 16 + g * 4;
-        if (kt.splits > 1) {
-          *(v4f*)(part.sums + (int64_t)pc * D + f0) = x;
-        } else {
-          store_out2(a, at * D + f0, x[0], x[1]);
-          store_out2(a, at * D + f0 + 2, x[2], x[3]);
-        }
-      }
-      if (g == 0) {
-        if (kt.splits > 1) {
-          part.stats[2 * pc] = m2[n];
-          part.stats[2 * pc + 1] = sum;
-        } else if (a.lse) {
-          a.lse[at] = lse_of(m2[n], sum);
-        }
-      }
-    }
-  } else {
-    // the waves' sums, each relative to the common maximum, added in their order
-    __shared__ float stat[4][C][2];
-    constexpr int kChunk = NT == 1 ? (D < 128 ? D : 128) : NT == 2 ? (D < 64 ? D : 64) : 32;
-    __shared__ float sums[4][C][kChunk + 4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float sum = column_sum(l[n]);
-      if (g == 0) {
-        stat[wave][n * 16 + cl][0] = m2[n];
-        stat[wave][n * 16 + cl][1] = sum;
-      }
-    }
-    __syncthreads();
-    float f[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int c = n * 16 + cl;
-      const float m = fmaxf(fmaxf(stat[0][c][0], stat[1][c][0]), fmaxf(stat[2][c][0], stat[3][c][0]));
-      f[n] = share(m2[n], stat[wave][c][1], m);
-    }
-    const Partial part = partial(a, unit, units, split, S::kCols, D);
-    for (int d0 = 0; d0 < D; d0 += kChunk) {
-      if (d0) __syncthreads();
+    for (int k = 0; k < 16; k += 4) {
+      const v4f vs = *(const v4f*)&in.vs[(k >> 3) * 32 + g * 8 + (k & 4)];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          if (d * 16 < d0 || d * 16 >= d0 + kChunk) continue;
-          const v4f x = (o[n][d] - oz[n]) * f[n];
-          *(v4f*)&sums[wave][n * 16 + cl][d * 16 - d0 + g * 4] = f[n] == 0.0f ? v4f{0, 0, 0, 0} : x;
-        }
-      __syncthreads();
-      const int width = min(kChunk, D - d0);
-      for (int i = threadIdx.x; i < C * width / 2; i += 256) {
-        const int c = i / (width / 2), d = (i - c * (width / 2)) * 2;
-        const int col = it.col0 + c;
-        if (col >= cols) continue;
-        const float m = fmaxf(fmaxf(stat[0][c][0], stat[1][c][0]), fmaxf(stat[2][c][0], stat[3][c][0]));
-        float sum = 0.0f, x = 0.0f, y = 0.0f;
+        for (int i = 0; i < 4; ++i) t[n][k + i] *= vs[i];
+    }
+    if (mask) {   // the scale of a hidden value may be NaN
+      keep_branch();
+      hide(0.0f);
+    }
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float mw = stat[w][c][0];
-          sum += stat[w][c][1] * share(mw, stat[w][c][1], m);
-          x += sums[w][c][d];
-          y += sums[w][c][d + 1];
-        }
-        if (kt.splits > 1) {
-          *(float2*)(part.sums + (int64_t)c * D + d0 + d) = make_float2(x, y);
-          if (d0 + d == 0) {
-            part.stats[2 * c] = m;
-            part.stats[2 * c + 1] = sum;
-          }
-        } else {
-          const int64_t at = out_row(a, it, col);
-          const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
-          store_out2(a, at * D + d0 + d, x * r, y * r);
-          if (a.lse && d0 + d == 0) a.lse[at] = lse_of(m, sum);
-        }
+    for (int j = 0; j < 2; ++j) {
+      v8b p[NT];
+      const v8b z = as_bf16(*(const v4u*)&in.vz[j * 32 + g * 8]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        p[n] = weights_to_bf16(&t[n][8 * j]);
+        c.oz[n] = mfma(z, p[n], c.oz[n]);
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const v8b vc = as_bf16(in.v[j * ND + d][lane]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) c.o[n][d] = mfma(vc, p[n], c.o[n][d]);
+        if (d % 4 == 3) issue_fence();
+      }
+    }
+  };
+
+  if (kt.begin < kt.end) {
+    load(kt.begin);
+    write(buf[0]);
+    load(kt.begin + 1);
+    lds_barrier();
+  }
+  for (int tile = kt.begin; tile < kt.end; ++tile) {
+    const int even = (tile - kt.begin) & 1;
+    if (tile + 1 < kt.end) {
+      write(buf[even ^ 1]);
+      load(tile + 2);
+    }
+    const int key0 = tile * kColsTile;
+    if (live && key0 < c.any_hi && key0 + kColsTile > c.any_lo) {
+      const bool there = kv_block(a.kv, b, shard, head, 2 * tile) >= 0 &&
+                         kv_block(a.kv, b, shard, head, 2 * tile + 1) >= 0;
+      const bool full = there && key0 >= c.all_lo && key0 + kColsTile <= c.all_hi;
+      compute(buf[even], key0, __builtin_amdgcn_readfirstlane(!full));
+    }
+    lds_barrier();
+  }
+  if (!live) return;
+
+  const int64_t slot = (item * heads + hk) * a.splits + split;
+  const Partial part = partial(a, slot, items * heads * a.splits, S::kCols, D);
+  const bool whole = kt.splits == 1;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int col = col0 + n * 16 + cl;
+    const float sum = column_sum(c.l[n]);
+    if (col >= cols) continue;
+    const int pc = wave * C + n * 16 + cl;
+    const float f = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t at = out_row(a, seq, shard, head, col);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      const v4f x = (c.o[n][d] - c.oz[n]) * f;
+      const int f0 = d * 16 + g * 4;
+      if (whole) {
+        store_out2(a, at * D + f0, x[0], x[1]);
+        store_out2(a, at * D + f0 + 2, x[2], x[3]);
+      } else {
+        *(v4f*)(part.sums + (int64_t)pc * D + f0) = x;
+      }
+    }
+    if (g == 0) {
+      if (!whole) {
+        part.stats[2 * pc] = c.m2[n];
+        part.stats[2 * pc + 1] = sum;
+      } else if (a.lse) {
+        a.lse[at] = lse_of(c.m2[n], sum);
       }
     }
   }
 }
 
-// Joins the splits of an item's columns, in their order.
-template <int D, int NT, bool kKeys>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int64_t first_block,
-                                                             int64_t items) {
-  using S = AttnShape<D, NT, kKeys>;
-  constexpr int C = S::C;
+// Adds the splits of an item's columns, in their order.
+template <int D, int NT>
+__global__ __launch_bounds__(256) void attention_splits_kernel(AttnArgs a, int64_t first_block,
+                                                               int64_t items) {
+  using S = ColsShape<D, NT>;
   const int64_t heads = a.kv.P * a.kv.Hk, id = first_block + blockIdx.x;
-  const int64_t hk = id % heads, item_id = id / heads;
-  Item it;
-  it.shard = hk / a.kv.Hk;
-  it.head = (int)(hk % a.kv.Hk);
+  const int64_t hk = id % heads, item = id / heads;
+  const int64_t shard = hk / a.kv.Hk;
+  const int head = (int)(hk % a.kv.Hk);
   int64_t sub;
-  it.b = find_sequence(a.kv, a.G, S::kShift, 1, item_id, &sub);
-  if (it.b < 0) return;
-  it.seq = seq_range(a.kv, it.b);
-  const int cols = it.seq.n * a.G;
-  if (sub >= ((int64_t)cols + S::kCols - 1) / S::kCols) return;
-  it.col0 = (int)sub * S::kCols;
-  const int64_t unit = id, units = items * heads;
-  for (int i = threadIdx.x; i < S::kCols * D / 2; i += 256) {
-    const int c = i / (D / 2), d = (i - c * (D / 2)) * 2, col = it.col0 + c;
-    if (col >= cols) return;
-    // the same splits as the wave that had this column
-    const int col0 = it.col0 + c / C * C;
-    int klo, khi;
-    keys_seen(a, it.seq, col0, min(col0 + C, cols), &klo, &khi);
-    const KeyTiles kt = key_tiles(klo, khi, 0, a.splits);
-    if (kt.splits <= 1) continue;
+  const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub);
+  if (b < 0) return;
+  const SeqRange seq = uniform(seq_range(a.kv, b));
+  const int cols = seq.n * a.G;
+  if ((sub << S::kShift) >= cols) return;
+  const int block_col = (int)sub << S::kShift;
+  int klo, khi;
+  keys_seen(a, seq, block_col, min(block_col + S::kCols, cols), &klo, &khi);
+  const KeyTiles kt = key_tiles(klo, khi, 0, a.splits);
+  if (kt.splits == 1) return;
+  auto part = [&](int s) {
+    return partial(a, id * a.splits + s, items * heads * a.splits, S::kCols, D);
+  };
+  const int live = min(S::kCols, cols - block_col);
+  for (int i = threadIdx.x; i < live * (D / 4); i += 256) {
+    const int c = i / (D / 4), d = (i - c * (D / 4)) * 4;
     float m = kNegInf;
-    for (int s = 0; s < kt.splits; ++s)
-      m = fmaxf(m, partial(a, unit, units, s, S::kCols, D).stats[2 * c]);
-    float sum = 0.0f, x = 0.0f, y = 0.0f;
+    for (int s = 0; s < kt.splits; ++s) m = fmaxf(m, part(s).stats[2 * c]);
+    float sum = 0.0f;
+    v4f x = {0, 0, 0, 0};
+#pragma unroll 4
     for (int s = 0; s < kt.splits; ++s) {
-      const Partial part = partial(a, unit, units, s, S::kCols, D);
-      const float ms = part.stats[2 * c];
-      const float f = share(ms, part.stats[2 * c + 1], m);
-      const float2 v = *(const float2*)(part.sums + (int64_t)c * D + d);
-      sum += part.stats[2 * c + 1] * f;
-      x += v.x * f;
-      y += v.y * f;
+      const Partial p = part(s);
+      const float l = p.stats[2 * c + 1], f = share(p.stats[2 * c], l, m);
+      sum += l * f;
+      x += *(const v4f*)(p.sums + (int64_t)c * D + d) * f;
     }
-    const int64_t at = out_row(a, it, col);
+    const int64_t at = out_row(a, seq, shard, head, block_col + c);
     const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
-    store_out2(a, at * D + d, x * r, y * r);
+    store_out2(a, at * D + d, x[0] * r, x[1] * r);
+    store_out2(a, at * D + d + 2, x[2] * r, x[3] * r);
     if (a.lse && d == 0) a.lse[at] = lse_of(m, sum);
   }
 }
 
-constexpr int64_t kMaxLaunch = int64_t(1) << 23;   // blocks of a launch
+constexpr int64_t kMaxLaunch = int64_t(1) << 22;   // blocks of a launch
 
-template <int D, int NT, bool kKeys>
-hipError_t launch_shape(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+template <int D, int NT, int kTeam>
+hipError_t launch_keys(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+  const int64_t blocks = plan.items * a.kv.P * a.kv.Hk;
+  for (int64_t b = 0; b < blocks; b += kMaxLaunch)
+    attention_keys_kernel<D, NT, kTeam, false>
+        <<<dim3((unsigned)(blocks - b < kMaxLaunch ? blocks - b : kMaxLaunch)), 64 * kTeam, 0, s>>>(
+            a, b, plan.items);
+  return hipGetLastError();
+}
+template <int D, int NT>
+hipError_t launch_stream(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+  attention_keys_kernel<D, NT, 4, true><<<dim3((unsigned)plan.splits), 256, 0, s>>>(a, 0, 0);
+  attention_join_kernel<D, NT, 4><<<dim3((unsigned)plan.splits), kJoinThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <int D>
+hipError_t launch_columns(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+  constexpr int NT = D <= 128 ? 2 : 1;
   const int64_t units = plan.items * a.kv.P * a.kv.Hk, blocks = units * plan.splits;
   for (int64_t b = 0; b < blocks; b += kMaxLaunch)
-    attention_kernel<D, NT, kKeys>
+    attention_columns_kernel<D, NT>
         <<<dim3((unsigned)(blocks - b < kMaxLaunch ? blocks - b : kMaxLaunch)), 256, 0, s>>>(
             a, b, plan.items);
   if (plan.splits > 1)
     for (int64_t b = 0; b < units; b += kMaxLaunch)
-      attention_join_kernel<D, NT, kKeys>
+      attention_splits_kernel<D, NT>
           <<<dim3((unsigned)(units - b < kMaxLaunch ? units - b : kMaxLaunch)), 256, 0, s>>>(
               a, b, plan.items);
   return hipGetLastError();
@@ -547,29 +1055,48 @@ hipError_t launch_shape(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) 
 
 template <int D>
 hipError_t launch_head(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
-  if (plan.by_keys) return launch_shape<D, 1, true>(a, plan, s);
-  return launch_shape<D, 2, false>(a, plan, s);
+  switch (plan.kind) {
+    case kAttnKeys8:
+      if constexpr (D <= 128) return launch_keys<D, 1, 8>(a, plan, s);
+    case kAttnKeys4: return launch_keys<D, 1, 4>(a, plan, s);
+    case kAttnStream: return launch_stream<D, 1>(a, plan, s);
+    default: return launch_columns<D>(a, plan, s);
+  }
 }
 
 }  // namespace
 
 AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t max_length) {
-  AttnPlan p;
+  AttnPlan p = {};
   const int G = Hq / Hk;
-  // columns of a sequence on average: a block's waves share out the keys of 16
-  // columns, or take 32 columns each
-  p.by_keys = T * G <= (int64_t)32 * B;
-  p.tiles_of = p.by_keys ? 1 : 2;
-  const int64_t cols = p.by_keys ? 16 : 128;
-  p.items = T * G / cols + B;
-  // blocks that fill the chip twice; a split has kMinTiles tiles at least
-  const int64_t work = p.items < T * G ? p.items : T * G;
-  const int64_t units = (work < 1 ? 1 : work) * P * Hk;
-  int64_t most = (max_length + kTile * kMinTiles - 1) / (kTile * kMinTiles);
-  int64_t want = (1024 + units - 1) / units;
+  const int64_t heads = P * Hk, columns = T * G;
+  p.splits = 1;
+  if (columns <= (int64_t)32 * B) {   // 32 columns a sequence on average
+    p.items = columns / 16 + B;
+    // groups of columns that exist, as far as the host knows: each row has one at least
+    const int64_t rows = T < B ? T : B;
+    const int64_t units = (rows > columns / 16 ? rows : columns / 16) * heads;
+    if (max_length <= 1024 || units >= 4096) {
+      p.kind = units <= 256 && D <= 128 ? kAttnKeys8 : kAttnKeys4;
+    } else {
+      p.kind = kAttnStream;
+      p.splits = 512;   // two blocks a CU
+      p.workspace = (size_t)(2 * p.splits * 16) * (D + 2) * 4;
+    }
+    return p;
+  }
+  p.kind = kAttnColumns;
+  const int64_t cols = D <= 128 ? 128 : 64;
+  p.items = columns / cols + B;
+  // blocks that fill the chip
+  const int64_t units = (columns + cols - 1) / cols * heads;
+  const int64_t most = (max_length + kColsTile * kMinTiles - 1) / (kColsTile * kMinTiles);
+  int64_t want = (512 + units - 1) / units;
   if (want > most) want = most;
-  p.splits = (int)(want < 1 ? 1 : want);
-  p.workspace = p.splits > 1 ? (size_t)(p.items * P * Hk * p.splits * cols) * (D + 2) * 4 : 0;
+  if (want > 1) {
+    p.splits = (int)want;
+    p.workspace = (size_t)(p.items * heads * want * cols) * (D + 2) * 4;
+  }
   return p;
 }
 

@@ -346,12 +346,12 @@ struct AttnArgs {
   float* ws;
   int splits;
 };
-// Splits of the keys that a launch of these sizes takes, and the workspace for them.
+// How a call of these sizes runs (attention.hip).
+enum AttnKind { kAttnKeys4, kAttnKeys8, kAttnStream, kAttnColumns };
 struct AttnPlan {
-  int tiles_of;             // 16-column tiles of a wave
-  bool by_keys;             // a block's waves share out the keys, else the columns
-  int splits;
-  int64_t items;            // blocks of one head and split
+  AttnKind kind;
+  int splits;               // kAttnColumns: of the keys; kAttnStream: blocks
+  int64_t items;            // groups of columns of one head that are set aside
   size_t workspace;
 };
 AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t max_length);

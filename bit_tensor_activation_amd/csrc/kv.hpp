@@ -40,6 +40,15 @@ __device__ __forceinline__ SeqRange seq_range(const KvArgs& a, int b) {
   return s;
 }
 
+// Values that are the same in all lanes, in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+__device__ __forceinline__ SeqRange uniform(const SeqRange& s) {
+  return {uniform(s.begin), uniform(s.n), uniform(s.length)};
+}
+
 // Work items lie sequence after sequence. An item covers 2^shift of a sequence's
 // rows*mul, so b's begin at most at floor(starts[b]*mul / 2^shift) + b*extra, and
 // that many are set aside: with extra 1 for parts that begin at the first row, 2

@@ -313,7 +313,7 @@ def test_other_stream_and_no_shards():
 
 @pytest.mark.gpu
 def test_python_refusals():
-    b = Batch([1], [600])
+    b = Batch([1], [2100], page=64)     # (long enough to need a workspace)
     cache = torch.from_numpy(random_cache(b, 1, 2, 64)).to(DEV)
     q = torch.zeros((1, 1, 4, 64), dtype=BF16, device=DEV)
     starts, lengths, tb = b.dev()
