@@ -564,6 +564,17 @@ __device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, NT
   if (kStream) lds_barrier();   // the next segment writes stat and sums again
 }
 
+// A group of columns that goes on past the end of the block it begins in. The cuts
+// of all blocks lie behind their partial results.
+struct Cut {
+  int32_t parts;   // blocks that it lies in; 0: none
+  int32_t b, hk, group;
+};
+template <int D, int C>
+__device__ __forceinline__ Cut* cuts(const AttnArgs& a, int64_t blocks) {
+  return (Cut*)(a.ws + 2 * blocks * C * (D + 2));
+}
+
 // kStream: the flat order is cut into equal shares, one a block, so a batch of any
 // lengths fills the chip evenly; a group of columns that a cut divides leaves
 // partial results (slot 2*block + 1 where it begins in the block, else 2*block),
@@ -578,9 +589,9 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
   if constexpr (!kStream) {
     const int64_t id = first_block + blockIdx.x, hk = id % heads;
     int64_t sub;
-    w.b = find_sequence(a.kv, a.G, S::kShift, 1, id / heads, &sub);
+    SeqRange seq;
+    w.b = find_sequence(a.kv, a.G, S::kShift, 1, id / heads, &sub, &seq);
     if (w.b < 0) return;
-    const SeqRange seq = uniform(seq_range(a.kv, w.b));
     const int cols = seq.n * a.G;
     if ((sub << S::kShift) >= cols) return;
     const int col0 = (int)sub << S::kShift;
@@ -598,7 +609,11 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
         uniform(flat_total<64 * kTeam>(a, S::kShift, scan, &mine, &b0, &b1));
     const int64_t all = per_head * heads, each = flat_share(all, gridDim.x, kTeam);
     const int64_t x0 = blockIdx.x * each, x1 = min(x0 + each, all);
-    if (x0 >= x1) return;
+    Cut* cut = cuts<D, S::C>(a, gridDim.x) + blockIdx.x;
+    if (x0 >= x1) {
+      if (threadIdx.x == 0) cut->parts = 0;
+      return;
+    }
     int64_t hk = x0 / per_head;
     flat_find<64 * kTeam>(a, S::kShift, x0 - hk * per_head, mine, b0, b1, &found);
     __syncthreads();
@@ -625,95 +640,98 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
           a, w.c, seq, w.shard, w.head, col0, cols, t1 - t0 == st.tiles,
           partial(a, 2 * (int64_t)blockIdx.x + (t0 == 0), 2 * (int64_t)gridDim.x, S::C, D));
       x += t1 - t0;
+      if (x >= x1 && threadIdx.x == 0) {
+        const int64_t last = (unit + st.tiles - 1) / each - blockIdx.x;   // blocks after this one
+        *cut = {t0 == 0 && last > 0 ? (int32_t)last + 1 : 0, w.b, (int32_t)hk, group};
+      }
     }
   }
 }
 
-// Adds the partial results of the group of columns that begins in the share of
-// block blockIdx.x and goes on past its end, if one does.
-constexpr int kJoinThreads = 1024;
-template <int D, int NT, int kTeam>
+// Adds the partial results of a cut group: blockIdx.x is the block that it begins
+// in, blockIdx.y a part of its columns. Threads by (team, column, 4 features), the
+// blocks of a cut shared out over teams.
+constexpr int kJoinThreads = 256;
+template <int D, int NT>
 __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a) {
-  using S = KeysShape<D, NT, kTeam, true>;
-  constexpr int kVec = D / 4;   // vectors of a row
-  __shared__ int64_t scan[kJoinThreads / 64];
-  __shared__ Flat found;
-  __shared__ int top[S::C];
-  __shared__ v4f sums[kJoinThreads];
-  __shared__ float ls[kJoinThreads];
-  const int64_t heads = a.kv.P * a.kv.Hk;
-  int64_t mine;
-  int b0, b1;
-  const int64_t per_head = flat_total<kJoinThreads>(a, S::kShift, scan, &mine, &b0, &b1);
-  const int64_t all = per_head * heads, each = flat_share(all, gridDim.x, kTeam);
-  const int64_t x0 = blockIdx.x * each, x1 = x0 + each;
-  if (x1 >= all) return;
-  const int64_t hk = (x1 - 1) / per_head;
-  flat_find<kJoinThreads>(a, S::kShift, x1 - 1 - hk * per_head, mine, b0, b1, &found);
-  if (threadIdx.x < S::C) top[threadIdx.x] = INT32_MIN;
-  __syncthreads();
-  const int b = found.b;
-  const SeqRange seq = uniform(seq_range(a.kv, b));
-  const SeqTiles st = seq_tiles(a, seq, S::kShift);
-  const int64_t begin = hk * per_head + found.begin;
-  const int group = (int)((x1 - 1 - begin) / st.tiles);
-  const int64_t unit = begin + (int64_t)group * st.tiles;
-  if (unit < x0 || unit + st.tiles <= x1) return;
-  const int parts = (int)((unit + st.tiles - 1) / each - blockIdx.x) + 1;
-  const int cols = seq.n * a.G, col0 = group << S::kShift, live = min(S::C, cols - col0);
+  constexpr int C = 16 * NT, kVec = D / 4;
+  constexpr int kSpan = C / 4;                                       // columns of a block
+  constexpr int kItems = kSpan * kVec;
+  constexpr int kTeams = kItems >= kJoinThreads ? 1 : kJoinThreads / kItems;
+  __shared__ v4f sums[kTeams][kItems];
+  __shared__ float stat[kTeams][kItems][2];
+  const Cut cut = cuts<D, C>(a, gridDim.x)[blockIdx.x];
+  if (cut.parts == 0) return;
+  const SeqRange seq = uniform(seq_range(a.kv, cut.b));
+  const int cols = seq.n * a.G, first = blockIdx.y * kSpan, col0 = (cut.group << (NT == 1 ? 4 : 5)) + first;
+  if (col0 >= cols) return;
   const int64_t slots = 2 * (int64_t)gridDim.x;
-  auto part = [&](int p) {
-    return partial(a, 2 * ((int64_t)blockIdx.x + p) + (p == 0), slots, S::C, D);
-  };
-  // the largest maximum: floats as ordered integers (it does not depend on the order)
-  for (int i = threadIdx.x; i < parts * live; i += kJoinThreads) {
-    const int p = i / live, c = i - p * live;
-    const int v = __float_as_int(part(p).stats[2 * c]);
-    atomicMax(&top[c], v < 0 ? v ^ 0x7fffffff : v);
-  }
-  __syncthreads();
-  // threads by (part of the partial results, column, 4 features)
-  const int vecs = live * kVec, teams = max(kJoinThreads / vecs, 1);
-  const int span = (parts + teams - 1) / teams;
-  for (int i0 = 0; i0 < vecs; i0 += kJoinThreads) {
-    const int team = vecs >= kJoinThreads ? 0 : (int)threadIdx.x / vecs;
-    const int i = i0 + (vecs >= kJoinThreads ? (int)threadIdx.x : (int)threadIdx.x - team * vecs);
+  for (int i = threadIdx.x % (kTeams == 1 ? kJoinThreads : kItems); i < kItems;
+       i += kTeams == 1 ? kJoinThreads : kItems) {
+    const int team = kTeams == 1 ? 0 : threadIdx.x / kItems;
     const int c = i / kVec, d = (i - c * kVec) * 4;
-    const bool mine_is = team < teams && i < vecs;
+    const bool live = team < kTeams && col0 + c < cols;
+    // relative to a running maximum, 8 blocks at a time
+    float m = kNegInf, l = 0.0f;
     v4f x = {0, 0, 0, 0};
-    float sum = 0.0f;
-    if (mine_is) {
-      const int v = top[c];
-      const float m = __int_as_float(v < 0 ? v ^ 0x7fffffff : v);
-      const int end = min((team + 1) * span, parts);
-#pragma unroll 8
-      for (int p = team * span; p < end; ++p) {
-        const Partial q = part(p);
-        const float l = q.stats[2 * c + 1], f = share(q.stats[2 * c], l, m);
-        const v4f y = *(const v4f*)(q.sums + (int64_t)c * D + d);
-        sum += l * f;
-        x += y * f;
+    if (live) {
+      const int span = (cut.parts + kTeams - 1) / kTeams, end = min((team + 1) * span, cut.parts);
+      for (int p0 = team * span; p0 < end; p0 += 8) {
+        float ms[8], ls[8];
+        v4f ys[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int p = min(p0 + j, end - 1);
+          const Partial q = partial(a, 2 * ((int64_t)blockIdx.x + p) + (p == 0), slots, C, D);
+          const float2 st = *(const float2*)(q.stats + 2 * (first + c));
+          ms[j] = p0 + j < end ? st.x : kNegInf;
+          ls[j] = p0 + j < end ? st.y : 0.0f;
+          ys[j] = *(const v4f*)(q.sums + (int64_t)(first + c) * D + d);
+        }
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, ms[j]);
+        float f = share(m, l, top);
+        l *= f;
+        x *= f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f = share(ms[j], ls[j], top);
+          l += ls[j] * f;
+          if (p0 + j < end) x += ys[j] * f;
+        }
+        m = top;
       }
     }
-    if (teams > 1) {
-      sums[threadIdx.x] = x;
-      ls[threadIdx.x] = sum;
+    if constexpr (kTeams > 1) {
+      if (team < kTeams) {
+        sums[team][i] = x;
+        stat[team][i][0] = m;
+        stat[team][i][1] = l;
+      }
       __syncthreads();
-      if (mine_is && team == 0)
-        for (int t = 1; t < teams; ++t) {
-          x += sums[t * vecs + i];
-          sum += ls[t * vecs + i];
+      if (team == 0) {
+        float top = m;
+#pragma unroll
+        for (int t = 1; t < kTeams; ++t) top = fmaxf(top, stat[t][i][0]);
+        float f = share(m, l, top);
+        m = top;
+        l *= f;
+        x *= f;
+#pragma unroll
+        for (int t = 1; t < kTeams; ++t) {
+          f = share(stat[t][i][0], stat[t][i][1], top);
+          l += stat[t][i][1] * f;
+          x += sums[t][i] * f;
         }
+      }
     }
-    if (mine_is && team == 0) {
-      const int64_t at = out_row(a, seq, hk / a.kv.Hk, (int)(hk % a.kv.Hk), col0 + c);
-      const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (live && team == 0) {
+      const int64_t at = out_row(a, seq, cut.hk / a.kv.Hk, (int)(cut.hk % a.kv.Hk), col0 + c);
+      const float r = l == 0.0f ? 0.0f : 1.0f / l;
       store_out2(a, at * D + d, x[0] * r, x[1] * r);
       store_out2(a, at * D + d + 2, x[2] * r, x[3] * r);
-      if (a.lse && d == 0) {
-        const int v = top[c];
-        a.lse[at] = lse_of(__int_as_float(v < 0 ? v ^ 0x7fffffff : v), sum);
-      }
+      if (a.lse && d == 0) a.lse[at] = lse_of(m, l);
     }
   }
 }
@@ -781,9 +799,9 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, i
   const int64_t shard = hk / a.kv.Hk;
   const int head = (int)(hk % a.kv.Hk);
   int64_t sub;
-  const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub);
+  SeqRange seq;
+  const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub, &seq);
   if (b < 0) return;
-  const SeqRange seq = uniform(seq_range(a.kv, b));
   const int cols = seq.n * a.G;
   if ((sub << S::kShift) >= cols) return;
   const int block_col = (int)sub << S::kShift;
@@ -803,28 +821,43 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, i
   const int kq = lane >> 4, krow = 8 * ((lane & 15) >> 2) + 4 * (kq & 1) + (lane & 3);
   uint32_t kreg[NS], word = 0;
   v4u vreg[S::VN];
-  auto load = [&](int tile) {
-    const int t = min(tile, kt.end - 1);
-    int64_t at[2];
+  // page numbers of a tile's blocks, a step before its loads
+  int pages[2];
+  auto look_up = [&](int tile) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t x = kv_block(a.kv, b, shard, head, 2 * t + j);
-      at[j] = x;
+      const int slot = min((2 * tile + j) >> a.kv.page_shift, (int)a.kv.max_pages - 1);
+      pages[j] = a.kv.table[(int64_t)b * a.kv.max_pages + slot];
     }
-    const int64_t ka = at[kq >> 1] < 0 ? 0 : at[kq >> 1];
+  };
+  int there = 0;   // bit j: block j of the tile loaded last has a page
+  auto load = [&](int tile) {
+    const int t = min(tile, kt.end - 1), shift = a.kv.page_shift;
+    int64_t at[2];
+    there = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int page = uniform(pages[j]), block = 2 * t + j;
+      const bool ok = (block >> shift) < a.kv.max_pages && page >= 0 && page < a.kv.pages;
+      at[j] = ok ? ((((shard * a.kv.pages + page) * a.kv.Hk + head) << shift) +
+                    (block & ((1 << shift) - 1))) * kv_block_bytes(D)
+                 : 0;   // (the mask hides what a block without a page seems to hold)
+      there |= ok << j;
+    }
+    look_up(tile + 1);
+    const int64_t ka = at[kq >> 1];
     __builtin_memcpy(kreg, a.kv.cache + ka + krow * (D / 2) + wave * (D / 8), 4 * NS);
 #pragma unroll
     for (int i = 0; i < S::VN; ++i) {
       const int r = min(i * 256 + tid, 2 * D - 1);
-      const int64_t va = r < D ? at[0] : at[1];
-      vreg[i] = *(const v4u*)(a.kv.cache + (va < 0 ? 0 : va) + 16 * D + (r < D ? r : r - D) * 16);
+      vreg[i] = *(const v4u*)(a.kv.cache + (r < D ? at[0] : at[1]) + 16 * D + (r < D ? r : r - D) * 16);
     }
     // words: waves 0 and 1 those of keys and of values
-    const int64_t wa = lane < 32 ? at[0] : at[1];
     if (wave < 2) {
-      word = *(const uint32_t*)(a.kv.cache + (wa < 0 ? 0 : wa) + 32 * D + 128 * wave + (lane & 31) * 4);
+      word = *(const uint32_t*)(a.kv.cache + (lane < 32 ? at[0] : at[1]) + 32 * D + 128 * wave +
+                                (lane & 31) * 4);
       // a place that holds nothing: 0, so that it stays a number
-      if (wa < 0 || t * kColsTile + lane >= seq.length) word = kZeroWord;
+      if (!(there >> (lane >> 5) & 1) || t * kColsTile + lane >= seq.length) word = kZeroWord;
     }
   };
   auto write = [&](typename S::Buffer& o) {
@@ -847,17 +880,15 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, i
       o.vz[(lane & 32) + (lane & 24) + (lane & 3) * 2 + ((lane >> 2) & 1)] = (uint16_t)word;
     }
   };
-  auto compute = [&](const typename S::Buffer& in, int key0, int mask) {
+  auto compute = [&](const typename S::Buffer& in, int key0, int blocks, int mask) {
     float t[NT][16];
     auto hide = [&](float with) {
-      const int64_t b0 = kv_block(a.kv, b, shard, head, key0 / 32);
-      const int64_t b1 = kv_block(a.kv, b, shard, head, key0 / 32 + 1);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int key = key0 + (k >> 3) * 32 + g * 8 + (k & 7);
-          const bool seen = key >= c.lo[n] && key < c.hi[n] && (k < 8 ? b0 : b1) >= 0;
+          const bool seen = key >= c.lo[n] && key < c.hi[n] && (blocks >> (k >> 3) & 1);
           t[n][k] = seen ? t[n][k] : with;
         }
     };
@@ -881,7 +912,6 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, i
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             t[n][8 * j + 4 * h + i] = __builtin_fmaf(-kz[i], c.qsum[n], acc[n][i]) * ks[i];
-        issue_fence();
       }
     if (mask) {
       keep_branch();
@@ -914,30 +944,30 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, i
         const v8b vc = as_bf16(in.v[j * ND + d][lane]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) c.o[n][d] = mfma(vc, p[n], c.o[n][d]);
-        if (d % 4 == 3) issue_fence();
       }
     }
   };
 
+  int there_now = 0;
   if (kt.begin < kt.end) {
+    look_up(kt.begin);
     load(kt.begin);
+    there_now = there;
     write(buf[0]);
     load(kt.begin + 1);
     lds_barrier();
   }
   for (int tile = kt.begin; tile < kt.end; ++tile) {
     const int even = (tile - kt.begin) & 1;
+    const int there_next = there;
     if (tile + 1 < kt.end) {
       write(buf[even ^ 1]);
       load(tile + 2);
     }
     const int key0 = tile * kColsTile;
-    if (live && key0 < c.any_hi && key0 + kColsTile > c.any_lo) {
-      const bool there = kv_block(a.kv, b, shard, head, 2 * tile) >= 0 &&
-                         kv_block(a.kv, b, shard, head, 2 * tile + 1) >= 0;
-      const bool full = there && key0 >= c.all_lo && key0 + kColsTile <= c.all_hi;
-      compute(buf[even], key0, __builtin_amdgcn_readfirstlane(!full));
-    }
+    const bool full = there_now == 3 && key0 >= c.all_lo && key0 + kColsTile <= c.all_hi;
+    compute(buf[even], key0, there_now, uniform(!full));
+    there_now = there_next;
     lds_barrier();
   }
   if (!live) return;
@@ -985,9 +1015,9 @@ __global__ __launch_bounds__(256) void attention_splits_kernel(AttnArgs a, int64
   const int64_t shard = hk / a.kv.Hk;
   const int head = (int)(hk % a.kv.Hk);
   int64_t sub;
-  const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub);
+  SeqRange seq;
+  const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub, &seq);
   if (b < 0) return;
-  const SeqRange seq = uniform(seq_range(a.kv, b));
   const int cols = seq.n * a.G;
   if ((sub << S::kShift) >= cols) return;
   const int block_col = (int)sub << S::kShift;
@@ -1034,7 +1064,7 @@ hipError_t launch_keys(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
 template <int D, int NT>
 hipError_t launch_stream(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
   attention_keys_kernel<D, NT, 4, true><<<dim3((unsigned)plan.splits), 256, 0, s>>>(a, 0, 0);
-  attention_join_kernel<D, NT, 4><<<dim3((unsigned)plan.splits), kJoinThreads, 0, s>>>(a);
+  attention_join_kernel<D, NT><<<dim3((unsigned)plan.splits, 4), kJoinThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 template <int D>
@@ -1081,7 +1111,7 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
     } else {
       p.kind = kAttnStream;
       p.splits = 512;   // two blocks a CU
-      p.workspace = (size_t)(2 * p.splits * 16) * (D + 2) * 4;
+      p.workspace = (size_t)(2 * p.splits * 16) * (D + 2) * 4 + p.splits * sizeof(Cut);
     }
     return p;
   }

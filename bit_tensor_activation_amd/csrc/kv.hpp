@@ -32,12 +32,15 @@ struct SeqRange {
   int length;
   __device__ __forceinline__ int first() const { return length - n; }   // place of the first row
 };
-__device__ __forceinline__ SeqRange seq_range(const KvArgs& a, int b) {
+__device__ __forceinline__ SeqRange cut_range(const KvArgs& a, int start, int next, int length) {
   SeqRange s;
-  s.begin = clamp_int(a.starts[b], 0, (int)a.T);
-  s.n = clamp_int(a.starts[b + 1], s.begin, (int)a.T) - s.begin;
-  s.length = clamp_int(a.lengths[b], 0, a.capacity);
+  s.begin = clamp_int(start, 0, (int)a.T);
+  s.n = clamp_int(next, s.begin, (int)a.T) - s.begin;
+  s.length = clamp_int(length, 0, a.capacity);
   return s;
+}
+__device__ __forceinline__ SeqRange seq_range(const KvArgs& a, int b) {
+  return cut_range(a, a.starts[b], a.starts[b + 1], a.lengths[b]);
 }
 
 // Values that are the same in all lanes, in scalar registers.
@@ -54,26 +57,34 @@ __device__ __forceinline__ SeqRange uniform(const SeqRange& s) {
 // that many are set aside: with extra 1 for parts that begin at the first row, 2
 // for parts that begin at a multiple of 2^shift in the sequence. The grid then
 // follows from T and the number of sequences, which the host knows.
-// Returns the sequence of `item` (a whole wave asks for one item) and leaves the
-// item's number in it, or -1. 64 sequences a step.
+// Returns the sequence of `item` (a whole wave asks for one item) with its rows and
+// length, and leaves the item's number in it; or -1. 64 sequences a step; the last
+// step has loaded the rows and lengths of all it looks at, so they cost no load of
+// their own after it.
 __device__ __forceinline__ int find_sequence(const KvArgs& a, int mul, int shift, int extra,
-                                             int64_t item, int64_t* sub) {
+                                             int64_t item, int64_t* sub, SeqRange* range) {
   const int lane = threadIdx.x & 63;
   int lo = 0, hi = a.B;
   for (;;) {
     const int step = (hi - lo + 63) >> 6;
     const int b = lo + lane * step;
-    bool before = false;
-    if (b < hi) before = (((int64_t)a.starts[b] * mul) >> shift) + (int64_t)b * extra <= item;
-    const int n = __popcll(__ballot(before));
+    const int at = min(b, a.B - 1);
+    const int start = a.starts[at], next = a.starts[at + 1], length = a.lengths[at];
+    const int64_t first = (((int64_t)start * mul) >> shift) + (int64_t)b * extra;
+    const int n = __popcll(__ballot(b < hi && first <= item));
     if (n == 0) return -1;
     lo += (n - 1) * step;
     hi = min(hi, lo + step);
-    if (step == 1) break;
+    if (step == 1) {
+      *sub = item - (((int64_t)__builtin_amdgcn_readlane(start, n - 1) * mul) >> shift) -
+             (int64_t)lo * extra;
+      *range = cut_range(a, __builtin_amdgcn_readlane(start, n - 1),
+                         __builtin_amdgcn_readlane(next, n - 1),
+                         __builtin_amdgcn_readlane(length, n - 1));
+      break;
+    }
   }
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  *sub = item - (((int64_t)a.starts[lo] * mul) >> shift) - (int64_t)lo * extra;
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // Byte offset of a sequence's block in the cache, or -1 where it has no page.

@@ -20,9 +20,9 @@ struct Place {
 __device__ __forceinline__ bool find_place(const KvArgs& a, int64_t item, int64_t shard, int head,
                                            Place* o) {
   int64_t sub;
-  const int b = find_sequence(a, 1, 5, 2, item, &sub);
+  SeqRange s;
+  const int b = find_sequence(a, 1, 5, 2, item, &sub, &s);
   if (b < 0) return false;
-  const SeqRange s = seq_range(a, b);
   const int block = (s.first() >> 5) + (int)sub;
   o->first = block * kBlockTokens;
   o->from = max(s.first() - o->first, 0);
@@ -113,6 +113,158 @@ __device__ __forceinline__ uint32_t quantize(const float (&x)[E], uint32_t (&cod
   for (int e = 0; e < E; ++e)
     code[e] = bad ? 0u : (uint32_t)fminf(fmaxf(steps(x[e]) + z, 0.0f), 15.0f);
   return bad ? kNanWord : sb | (__float_as_uint(128.0f + z) >> 16);
+}
+
+// ---- the usual form: 8 lanes a token, its features in registers ----
+//
+// A lane holds two runs of W = D/16 features of a key, those that turn into each
+// other (W*i and D/2 + W*i where halves pair, neighbours else), and 2*W neighbouring
+// features of a value. Codes of values turn in LDS: a thread merges a dword of 4
+// features of each of 8 tokens into 4 rows of 8 tokens, 12 instructions for 32
+// codes. Takes whole heads turned or none, rows on 16 bytes, and D a multiple of 64
+// (a run of whole dwords' codes).
+template <int W, int kType>
+__device__ __forceinline__ void load_run(const void* base, int64_t first, float (&x)[W]) {
+#pragma unroll
+  for (int e = 0; e < W; e += 4) {
+    if constexpr (kType == kF32) {
+      const v4u w = *(const v4u*)((const float*)base + first + e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[e + j] = __uint_as_float(w[j]);
+    } else {
+      const v2u w = *(const v2u*)((const uint16_t*)base + first + e);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[e + 2 * j] = __uint_as_float(w[j] << 16);
+        x[e + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+  }
+}
+
+template <int D, int kType>
+__global__ __launch_bounds__(kThreads) void kv_append_heads_kernel(HeadRows k, HeadRows v,
+                                                                   RopeArgs rope, KvArgs a) {
+  constexpr int W = D / 16, kPitch = D / 4 + 1;
+  __shared__ uint32_t codes[kBlockTokens * kPitch];
+  const int64_t hk = blockIdx.x % (a.P * a.Hk), item = blockIdx.x / (a.P * a.Hk);
+  const int64_t shard = hk / a.Hk;
+  const int head = (int)(hk % a.Hk);
+  Place at;
+  if (!find_place(a, item, shard, head, &at)) return;
+  const int t = threadIdx.x / 8, sub = threadIdx.x % 8;
+  const bool mine = t >= at.from && t < at.to;
+  const int64_t row = at.row + (mine ? t : at.from);   // (idle lanes read a row that is there)
+  const bool halves = rope.cos && rope.style == kHalf;
+  const int f0 = halves ? W * sub : 2 * W * sub, f1 = halves ? D / 2 + f0 : f0 + W;
+  float x[W], y[W], c[W], s[W], u[W], w[W];
+  const int64_t kb = shard * k.shard + row * k.pitch + head * k.head;
+  const int64_t vb = shard * v.shard + row * v.pitch + head * v.head + 2 * W * sub;
+  load_run<W, kType>(k.p, kb + f0, x);
+  load_run<W, kType>(k.p, kb + f1, y);
+  const int64_t pos = at.first + (mine ? t : at.from);
+  const bool known = pos < rope.rows;
+  if (rope.cos) {
+    const int64_t e = (known ? pos : 0) * (D / 2) + W * sub;
+    load_run<W, kF32>(rope.cos, e, c);
+    load_run<W, kF32>(rope.sin, e, s);
+  }
+  load_run<W, kType>(v.p, vb, u);
+  load_run<W, kType>(v.p, vb + W, w);
+  if (at.at < 0) return;
+  uint8_t* block = a.cache + at.at;
+  // this thread's part of the values' block: features 4*fq .. of tokens 8*group ..
+  const int fq = threadIdx.x / 4, group = threadIdx.x % 4;
+  uint32_t mask = 0, old[(D + 255) / 256][4];
+  {
+    const int from = max(at.from - 8 * group, 0), to = min(at.to - 8 * group, 8);
+    if (from < to) mask = (to == 8 ? 0xffffffffu : (1u << (4 * to)) - 1) & (0xffffffffu << (4 * from));
+  }
+  if (mask && ~mask) {
+#pragma unroll
+    for (int i = 0; i < (D + 255) / 256; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (4 * (fq + 64 * i) < D)
+          old[i][r] = *(const uint32_t*)(block + 16 * D + (4 * (fq + 64 * i) + r) * 16 + group * 4);
+  }
+
+  if (rope.cos) {
+    if (!known) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) c[e] = s[e] = __uint_as_float(0x7fc00000u);
+    }
+    if (halves) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const float p = x[e], q = y[e];
+        x[e] = p * c[e] - q * s[e];
+        y[e] = q * c[e] + p * s[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; e += 2) {
+        const float p = x[e], q = x[e + 1], m = y[e], n = y[e + 1];
+        x[e] = p * c[e / 2] - q * s[e / 2];
+        x[e + 1] = q * c[e / 2] + p * s[e / 2];
+        y[e] = m * c[(W + e) / 2] - n * s[(W + e) / 2];
+        y[e + 1] = n * c[(W + e) / 2] + m * s[(W + e) / 2];
+      }
+    }
+  }
+  float z[2 * W];
+  uint32_t code[2 * W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) z[e] = x[e], z[W + e] = y[e];
+  const uint32_t kw = quantize<2 * W>(z, code);
+  if (mine) {
+    uint8_t* out = block + t * (D / 2);
+#pragma unroll
+    for (int e = 0; e < 2 * W; e += 4)
+      *(uint16_t*)(out + (e < W ? f0 + e : f1 + e - W) / 2) =
+          (uint16_t)(code[e] | code[e + 1] << 4 | code[e + 2] << 8 | code[e + 3] << 12);
+    if (sub == 0) *(uint32_t*)(block + 32 * D + t * 4) = kw;
+  }
+#pragma unroll
+  for (int e = 0; e < W; ++e) z[e] = u[e], z[W + e] = w[e];
+  const uint32_t vw = quantize<2 * W>(z, code);
+  if (mine && sub == 0) *(uint32_t*)(block + 32 * D + 128 + t * 4) = vw;
+#pragma unroll
+  for (int e = 0; e < 2 * W; e += 4)
+    codes[t * kPitch + (2 * W * sub + e) / 4] =
+        code[e] | code[e + 1] << 8 | code[e + 2] << 16 | code[e + 3] << 24;
+  lds_barrier();
+  if (!mask) return;
+#pragma unroll
+  for (int i = 0; i < (D + 255) / 256; ++i) {
+    const int q = fq + 64 * i;
+    if (4 * q >= D) break;
+    uint32_t p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      p[j] = codes[(8 * group + 2 * j) * kPitch + q] | codes[(8 * group + 2 * j + 1) * kPitch + q] << 4;
+    const uint32_t a0 = __builtin_amdgcn_perm(p[1], p[0], 0x05010400u);
+    const uint32_t a1 = __builtin_amdgcn_perm(p[1], p[0], 0x07030602u);
+    const uint32_t b0 = __builtin_amdgcn_perm(p[3], p[2], 0x05010400u);
+    const uint32_t b1 = __builtin_amdgcn_perm(p[3], p[2], 0x07030602u);
+    const uint32_t rows[4] = {
+        __builtin_amdgcn_perm(b0, a0, 0x05040100u), __builtin_amdgcn_perm(b0, a0, 0x07060302u),
+        __builtin_amdgcn_perm(b1, a1, 0x05040100u), __builtin_amdgcn_perm(b1, a1, 0x07060302u)};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *(uint32_t*)(block + 16 * D + (4 * q + r) * 16 + group * 4) =
+          ~mask ? (rows[r] & mask) | (old[i][r] & ~mask) : rows[r];
+  }
+}
+
+template <int D>
+hipError_t launch_append_heads(const HeadRows& k, const HeadRows& v, const RopeArgs& rope,
+                               const KvArgs& a, dim3 grid, hipStream_t s) {
+  if (k.type == kF32)
+    kv_append_heads_kernel<D, kF32><<<grid, kThreads, 0, s>>>(k, v, rope, a);
+  else
+    kv_append_heads_kernel<D, kBf16><<<grid, kThreads, 0, s>>>(k, v, rope, a);
+  return hipGetLastError();
 }
 
 template <int D, bool kVector>
@@ -287,6 +439,15 @@ hipError_t launch_kv_append(const HeadRows& k, const HeadRows& v, const RopeArgs
   const int64_t items = place_items(a);
   const dim3 grid((unsigned)(items * a.P * a.Hk));
   const bool vec = on16(k) && on16(v);
+  if (vec && a.D % 64 == 0 &&
+      (!rope.cos || (rope.dim == a.D && ((uintptr_t)rope.cos & 15) == 0 && ((uintptr_t)rope.sin & 15) == 0))) {
+    switch (a.D) {
+      case 64: return launch_append_heads<64>(k, v, rope, a, grid, s);
+      case 128: return launch_append_heads<128>(k, v, rope, a, grid, s);
+      case 192: return launch_append_heads<192>(k, v, rope, a, grid, s);
+      default: return launch_append_heads<256>(k, v, rope, a, grid, s);
+    }
+  }
 #define BTQ_CALL(N)                                                                      \
   if (vec)                                                                               \
     kv_append_kernel<N, true><<<grid, kThreads, 0, s>>>(k, v, rope, a, items);           \
