@@ -411,7 +411,7 @@ int check_attention_sizes(int64_t P, int64_t T, int64_t Hq, int64_t Hk, int64_t 
                           int64_t max_pages, int64_t page_size, int64_t max_length) {
   const int st = check_kv_sizes(P, T, Hk, D, B, max_pages, page_size);
   if (st != BTQ_OK) return st;
-  if (Hq < 1 || Hq > kMaxP || Hq % Hk != 0 || max_length < 0 || max_length > kMaxPlaces)
+  if (Hq < 1 || Hq > kMaxP / 2 || Hq % Hk != 0 || max_length < 0 || max_length > kMaxPlaces)
     return BTQ_ERR_SHAPE;
   const int64_t G = Hq / Hk;
   return T > kMaxPlaces / 2 / G ? BTQ_ERR_SHAPE : BTQ_OK;
@@ -635,7 +635,7 @@ int btq_kv_attention(const void* q, int64_t q_shard, int64_t q_pitch, int64_t q_
   const btq::AttnArgs a = {
       rows, btq::on16(rows),
       kv_args(P, T, Hk, D, seq_starts, lengths, B, page_table, max_pages, cache, pages, page_size),
-      (int)Hq, (int)(Hq / Hk), scale * 1.4426950408889634f, causal != 0,
+      (int)Hq, (int)(Hq / Hk), (uint32_t)(((uint64_t(1) << 32) + Hq / Hk - 1) / (Hq / Hk)), scale * 1.4426950408889634f, causal != 0,
       (int)(window > kMaxPlaces ? 0 : window), out, out_type, lse, (float*)workspace, plan.splits};
   return hip_status(btq::launch_kv_attention(a, plan, (hipStream_t)stream));
 }

@@ -4,12 +4,13 @@
 // heads of n queries give n*G columns c of S = K Q^T, for each
 //   t[key] = scale * sum_d q[d]*(code[key,d] - z[key])*s[key],  p = exp(t - max),
 //   out = sum_key p*s'[key]*(code'[key,:] - z'[key]) / sum_key p.
-// A nibble or-ed into the mantissa of bf16 128 is the exact bf16 128 + code, 7
-// instructions for the 8 codes of a dword. So both products run on the matrix
-// cores on 128 + code, and 128 + z is taken off after: from S as a product with
-// the sum of q, from out as one more row of V^T that holds 128 + z', whose
-// product sees the same rounded p*s' as the codes do. Scores are exact to fp32
-// rounding; p*s' is rounded to bf16, as a weight of the second product.
+// Both products run on the matrix cores on the codes themselves, and z is taken off
+// after: from S as a product with the sum of q, from out as one more row of V^T
+// that holds z', whose product sees the same rounded p*s' as the codes do. A nibble
+// or-ed into the mantissa of bf16 128 is the exact bf16 128 + code, 7 instructions
+// for the 8 codes of a dword; a nibble in a byte of its own is the exact 8-bit float
+// (e4m3) code*2^-9, its subnormal numbers and first binade being evenly spaced: 3
+// instructions. p*s' is rounded to bf16, as a weight of the second product.
 //
 // S is computed transposed (keys down, columns across), so that the 4 values of a
 // column that a lane holds of two 16-key tiles are the 8 consecutive keys of the
@@ -56,10 +57,23 @@ __device__ __forceinline__ v8b deal(v4u w) {
   return __builtin_bit_cast(v8b, r);
 }
 
+// The thread's number, computed where it stands: what follows from it is not kept in
+// registers over the loops around.
+__device__ __forceinline__ int thread_here() {
+  int t = threadIdx.x;
+  settle(t);
+  return t;
+}
+
 // x of lane kLane of each row of 16 lanes.
 template <int kLane>
 __device__ __forceinline__ uint32_t row_lane(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x150 + kLane, 0xf, 0xf, true);
+}
+
+template <int kLane>
+__device__ __forceinline__ float from_lane(float x) {
+  return __uint_as_float(row_lane<kLane>(__float_as_uint(x)));
 }
 
 // x combined over the 4 lanes that hold one column.
@@ -96,11 +110,19 @@ __device__ __forceinline__ void static_for(F f) {
 
 // ---- what a wave keeps of its columns: 16*NT of them, column n*16 + lane%16 in
 // the 4 lanes of that number ----
-template <int D, int NT>
+//
+// Queries are operand B of the first product: bf16 as they come (kBytes false), or
+// the sum of two 8-bit floats, for keys as 8-bit floats. The latter takes them by a
+// power of 2 to below 256 (a column's largest to 128 or more); the first float holds
+// 4 bits of a value and the second the other 4 of bf16, down to 2^-10. So a query is
+// off by 2^-18 of its largest feature at most.
+template <int D, int NT, bool kBytes>
 struct Columns {
   static constexpr int NS = D / 32, ND = D / 16;
-  v8b q[NT][NS];             // operand B of the first product
-  float qsum[NT];
+  v8b q[NT][NS];
+  long q8[NT][NS][2];
+  float qsum[NT];            // in the units of the first product
+  float unit[NT];            // what it takes to powers of 2 of p
   int lo[NT], hi[NT];        // keys that the column sees
   v4f o[NT][ND], oz[NT];     // sums of p*s'*(128 + code) of 4 features, and of p*s'*(128 + z')
   float m2[NT], l[NT];       // running maximum times scale*log2(e); sum of p of this lane's keys
@@ -110,8 +132,14 @@ struct Columns {
   // Columns [col0, col0 + 16*NT) of a sequence, of which those below cols exist.
   __device__ __forceinline__ void load(const AttnArgs& a, const SeqRange& s, int64_t shard, int head,
                                        int col0, int cols) {
-    const int lane = threadIdx.x & 63, cl = lane & 15, g = lane >> 4;
-    const int last = (min(col0 + 16 * NT, cols) - 1) / a.G, first = col0 / a.G;
+    const int lane = thread_here() & 63, cl = lane & 15, g = lane >> 4;
+    // (col0 the same in all lanes; col/G by a product, exact below 2^32/G)
+    const int first = col0 / a.G, rest = col0 - first * a.G;
+    auto query = [&](int col) {
+      const uint32_t x = (uint32_t)(rest + col - col0);
+      return first + (int)(a.G == 1 ? x : __umulhi(x, a.G_inverse));
+    };
+    const int last = query(min(col0 + 16 * NT, cols) - 1);
     all_hi = a.causal ? min(s.first() + first + 1, s.length) : s.length;
     all_lo = a.window ? s.first() + last + 1 - a.window : 0;
     any_hi = a.causal ? clamp_int(s.first() + last + 1, 0, s.length) : s.length;
@@ -120,31 +148,40 @@ struct Columns {
     for (int n = 0; n < NT; ++n) {
       const int col = col0 + n * 16 + cl;
       const bool live = col < cols;
-      const int qi = live ? col / a.G : 0, pos = s.first() + qi;
+      const int qi = query(live ? col : col0), pos = s.first() + qi;
       hi[n] = a.causal ? min(pos + 1, s.length) : s.length;
       lo[n] = a.window ? max(pos + 1 - a.window, 0) : 0;
       const uint16_t* row = (const uint16_t*)a.q.p + shard * a.q.shard +
                             (s.begin + (int64_t)qi) * a.q.pitch +
-                            (head * (int64_t)a.G + (live ? col - qi * a.G : 0)) * a.q.head +
+                            (head * (int64_t)a.G + (live ? col : col0) - (int64_t)qi * a.G) * a.q.head +
                             g * (D / 4);
-      float sum = 0.0f;
+      v4u w[NS];
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        v4u w;
         if (a.q_on16) {
-          w = *(const v4u*)(row + 8 * i);
+          w[i] = *(const v4u*)(row + 8 * i);
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            w[j] = row[8 * i + 2 * j] | (uint32_t)row[8 * i + 2 * j + 1] << 16;
+            w[i][j] = row[8 * i + 2 * j] | (uint32_t)row[8 * i + 2 * j + 1] << 16;
         }
-        if (!live) w = v4u{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
-        q[n][i] = deal(w);
+        if (!live) w[i] = v4u{0, 0, 0, 0};
       }
-      qsum[n] = column_sum(sum);
+      if constexpr (kBytes) {
+        to_bytes(n, w);
+        unit[n] *= a.scale2;
+      } else {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sum += __uint_as_float(w[i][j] << 16) + __uint_as_float(w[i][j] & 0xffff0000u);
+          q[n][i] = deal(w[i]);
+        }
+        qsum[n] = column_sum(sum);
+        unit[n] = a.scale2;
+      }
       oz[n] = v4f{0, 0, 0, 0};
 #pragma unroll
       for (int d = 0; d < ND; ++d) o[n][d] = v4f{0, 0, 0, 0};
@@ -153,11 +190,59 @@ struct Columns {
     }
   }
 
+  __device__ __forceinline__ void to_bytes(int n, const v4u (&w)[NS]) {
+    float top = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x = fabsf(__uint_as_float(h ? w[i][j] & 0xffff0000u : w[i][j] << 16));
+          top = fmaxf(top, x);
+          bad |= !(x < INFINITY);
+        }
+    top = column_max(top);
+    // 2^(7 - exponent of top), within the powers that have a reciprocal
+    const int e = clamp_int((int)(__float_as_uint(top) >> 23), 20, 254);
+    const float up = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
+    unit[n] = 512.0f / up;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      uint32_t r[2][2];   // [first, second float][even, odd features]
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x[4];
+        int first = 0, second = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[j] = __uint_as_float(h ? w[i][j] & 0xffff0000u : w[i][j] << 16) * up;
+        first = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], first, false);
+        first = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], first, true);
+        const auto a0 = __builtin_amdgcn_cvt_pk_f32_fp8(first, false);
+        const auto a1 = __builtin_amdgcn_cvt_pk_f32_fp8(first, true);
+        second = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] - a0[0], x[1] - a0[1], second, false);
+        second = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] - a1[0], x[3] - a1[1], second, true);
+        const auto b0 = __builtin_amdgcn_cvt_pk_f32_fp8(second, false);
+        const auto b1 = __builtin_amdgcn_cvt_pk_f32_fp8(second, true);
+        sum += (a0[0] + b0[0]) + (a0[1] + b0[1]) + (a1[0] + b1[0]) + (a1[1] + b1[1]);
+        r[0][h] = (uint32_t)first;
+        r[1][h] = (uint32_t)second;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) q8[n][i][k] = (long)((uint64_t)r[k][1] << 32 | r[k][0]);
+    }
+    // NaN and Inf in a query make all its scores NaN
+    qsum[n] = column_sum(bad ? __uint_as_float(0x7fc00000u) : sum * 0x1p-9f);
+  }
+
   // Scores t (value k is a key of the lane's) to weights p; l and the sums follow
   // the running maximum. It is raised only when a new one is 8 powers of 2 above
   // it: p stays below 2^8, and the sums are rarely rescaled.
   template <int kValues>
-  __device__ __forceinline__ void weights(const AttnArgs& a, float (&t)[NT][kValues]) {
+  __device__ __forceinline__ void weights(float (&t)[NT][kValues]) {
     float top[NT];
     bool raise = false;
 #pragma unroll
@@ -165,7 +250,7 @@ struct Columns {
       float m = t[n][0];
 #pragma unroll
       for (int k = 1; k < kValues; ++k) m = fmaxf(m, t[n][k]);
-      top[n] = column_max(m) * a.scale2;
+      top[n] = column_max(m) * unit[n];
       raise |= top[n] > m2[n] + 8.0f || (m2[n] == kNegInf && top[n] > kNegInf);
     }
     if (__ballot(raise)) {
@@ -186,7 +271,7 @@ struct Columns {
       const float off = m2[n] == kNegInf ? 0.0f : m2[n];
 #pragma unroll
       for (int k = 0; k < kValues; ++k) {
-        t[n][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(t[n][k], a.scale2, -off));   // hidden: 0
+        t[n][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(t[n][k], unit[n], -off));   // hidden: 0
         l[n] += t[n][k];
       }
     }
@@ -250,7 +335,7 @@ struct KeysShape {
 template <int D, int NT>
 struct KeysWave {
   static constexpr int NS = D / 32, ND = D / 16;
-  Columns<D, NT> c;
+  Columns<D, NT, true> c;
   const AttnArgs& a;
   int b, head;
   int64_t shard;
@@ -312,11 +397,11 @@ struct KeysWave {
 #pragma unroll
       for (int h = 0; h < 2; ++h) __builtin_memcpy(k[s][h], p + (8 * s + 4 * h) * (D / 2), 4 * NS);
   }
-  // words of keys and values 2*cl and 2*cl + 1 of the lane's block
+  // words of keys and values 8*(cl/4) + cl%4 and 4 further of the lane's block
   __device__ __forceinline__ void load_words(int64_t at, uint32_t (&x)[2], uint32_t (&y)[2]) {
-    const uint8_t* p = a.kv.cache + at + 32 * D + (threadIdx.x & 15) * 8;
-    __builtin_memcpy(x, p, 8);
-    __builtin_memcpy(y, p + 128, 8);
+    const int cl = threadIdx.x & 15;
+    const uint32_t* p = (const uint32_t*)(a.kv.cache + at + 32 * D) + 8 * (cl >> 2) + (cl & 3);
+    x[0] = p[0], x[1] = p[4], y[0] = p[32], y[1] = p[36];
   }
   __device__ __forceinline__ void load_values(int64_t at) {
     const uint8_t* p = a.kv.cache + at + 16 * D + (threadIdx.x & 15) * 16;
@@ -329,99 +414,87 @@ struct KeysWave {
   __device__ __forceinline__ void compute(int64_t kat, int64_t vat, int key0, bool there, int mask) {
     constexpr int KS = NT == 1 ? 2 : 1;   // steps of 32 keys whose scores are held at once
     const int base = key0 + ((threadIdx.x & 63) >> 4) * kBlockTokens;
-    static_for<0, 4, KS>([&](auto first) {
-      constexpr int S0 = decltype(first)::value;
-      float t[NT][8 * KS];
+    // of the lane's 2 keys and values; a step's products take them from the lanes
+    // that have them. Whatever stands in a place that holds nothing, z' is a number.
+    float ks[2], kz[2], vs[2];
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+    for (int h = 0; h < 2; ++h) {
+      ks[h] = __uint_as_float(kw[h] & 0xffff0000u);
+      kz[h] = 128.0f - __uint_as_float(kw[h] << 16);
+      vs[h] = __uint_as_float(vw[h] & 0xffff0000u);
+    }
+    const uint32_t vz = (vw[0] & 0xfu) | (vw[1] & 0xfu) << 16 | magic;
+    static_for<0, 4, KS>([&](auto step) {
+      constexpr int S0 = decltype(step)::value;
+      float t[NT][8 * KS];   // value 8*s + 4*h + i is key 8*(S0 + s) + 4*h + i of the lane's block
+      static_for<0, 2 * KS, 1>([&](auto group) {
+        constexpr int SH = decltype(group)::value, s = SH / 2, h = SH % 2;
+        v4f acc[NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          v4f acc[NT];
+        for (int n = 0; n < NT; ++n) acc[n] = v4f{0, 0, 0, 0};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) acc[n] = v4f{0, 0, 0, 0};
-#pragma unroll
-          for (int w = 0; w < NS; ++w) {
-            const v8b kc = as_bf16(codes_to_bf16(k[S0 + s][h][w], magic));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n] = mfma(kc, c.q[n][w], acc[n]);
-          }
+        for (int w = 0; w < NS; ++w) {
+          const uint32_t x = k[S0 + s][h][w];
+          const long kc = (long)((uint64_t)(x >> 4 & 0x0f0f0f0fu) << 32 | (x & 0x0f0f0f0fu));
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) t[n][8 * s + 4 * h + i] = acc[n][i];
-          issue_fence();   // (else the scheduler converts all codes at once, and spills)
+            for (int j = 0; j < 2; ++j)
+              acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(kc, c.q8[n][w][j], acc[n], 0, 0, 0);
         }
+        static_for<0, 4, 1>([&](auto index) {
+          constexpr int i = decltype(index)::value, L = 4 * (S0 + s) + i;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            t[n][8 * s + 4 * h + i] = (acc[n][i] + from_lane<L>(kz[h]) * c.qsum[n]) * from_lane<L>(ks[h]);
+        });
+      });
       if constexpr (S0 + KS == 4) {
+        issue_fence();
         load_keys(kat);
         issue_fence();
       }
-      static_for<0, 4 * KS, 1>([&](auto pair) {
-        constexpr int kPair = decltype(pair)::value;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t w = row_lane<4 * S0 + kPair>(kw[j]);
-          const float ks = __uint_as_float(w & 0xffff0000u), kz = __uint_as_float(w << 16);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float& x = t[n][2 * kPair + j];
-            x = __builtin_fmaf(-kz, c.qsum[n], x) * ks;
-          }
-        }
-      });
-      auto hide = [&](float (&x)[NT][8 * KS], float with) {
+      auto hide = [&](float with) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int from = there ? c.lo[n] - base - 8 * S0 : 32, to = c.hi[n] - base - 8 * S0;
 #pragma unroll
           for (int key = 0; key < 8 * KS; ++key)
-            x[n][key] = key >= from && key < to ? x[n][key] : with;
+            t[n][key] = key >= from && key < to ? t[n][key] : with;
         }
       };
       if (mask) {
         keep_branch();
-        hide(t, kNegInf);
+        hide(kNegInf);
       }
-      c.weights(a, t);
-      uint32_t z[4 * KS];
-      static_for<0, 4 * KS, 1>([&](auto pair) {
-        constexpr int kPair = decltype(pair)::value;
+      c.weights(t);
+      static_for<0, 8 * KS, 1>([&](auto index) {
+        constexpr int key = decltype(index)::value, L = 4 * (S0 + key / 8) + key % 4;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int key = 2 * kPair + j;
-          const uint32_t w = row_lane<4 * S0 + kPair>(vw[j]);
-          const float vs = __uint_as_float(w & 0xffff0000u);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) t[n][key] *= vs;
-          // 128 + z of keys i (low half) and 4 + i; whatever stands in a place that
-          // holds no value, it is a number
-          uint32_t& zz = z[(key >> 3) * 4 + (key & 3)];
-          if ((key & 4) == 0)
-            zz = (w & 0xfu) | magic;
-          else
-            zz |= (w & 0xfu) << 16;
-        }
+        for (int n = 0; n < NT; ++n) t[n][key] *= from_lane<L>(vs[key / 4 % 2]);
       });
       if (mask) {   // the scale of a hidden value may be NaN
         keep_branch();
-        hide(t, 0.0f);
+        hide(0.0f);
       }
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
+      static_for<0, KS, 1>([&](auto index) {
+        constexpr int s = decltype(index)::value, L = 4 * (S0 + s);
+        const v8b z = as_bf16(v4u{row_lane<L>(vz), row_lane<L + 1>(vz), row_lane<L + 2>(vz), row_lane<L + 3>(vz)});
         v8b p[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           p[n] = weights_to_bf16(&t[n][8 * s]);
-          c.oz[n] = mfma(as_bf16(v4u{z[4 * s], z[4 * s + 1], z[4 * s + 2], z[4 * s + 3]}), p[n], c.oz[n]);
+          c.oz[n] = mfma(z, p[n], c.oz[n]);
         }
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
           const v8b vc = as_bf16(codes_to_bf16(v[d][S0 + s], magic));
 #pragma unroll
           for (int n = 0; n < NT; ++n) c.o[n][d] = mfma(vc, p[n], c.o[n][d]);
-          if (d % 2 == 1) issue_fence();
         }
-      }
+      });
     });
+    issue_fence();
     load_values(vat);
     issue_fence();
   }
@@ -490,22 +563,28 @@ __device__ __forceinline__ void flat_find(const AttnArgs& a, int shift, int64_t 
     mine += n;
   }
 }
+constexpr int64_t kStreamBlocks = 512;   // two a CU
+// a/b, in 32 bits where they fit (a 64-bit division takes some 150 instructions).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if ((uint64_t)(a | b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
 // Tiles of a block: an equal share of all, and a step for each wave at least.
-__device__ __forceinline__ int64_t flat_share(int64_t all, int64_t blocks, int team) {
-  const int64_t n = (all + blocks - 1) / blocks;
+__device__ __forceinline__ int64_t flat_share(int64_t all, int team) {
+  const int64_t n = (all + kStreamBlocks - 1) / kStreamBlocks;
   return n < team ? team : n;
 }
 
 // The team's sums, each relative to the common maximum, added in the waves' order;
 // to `out` where they are whole, else to a partial result.
 template <int D, int NT, int kTeam, bool kStream>
-__device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, NT>& c, const SeqRange& seq,
+__device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, NT, true>& c, const SeqRange& seq,
                                           int64_t shard, int head, int col0, int cols, bool whole,
                                           const Partial& part) {
   using S = KeysShape<D, NT, kTeam, kStream>;
   __shared__ float stat[kTeam][S::C][2];
   __shared__ float sums[kTeam][S::C][S::kChunk + 4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cl = lane & 15, g = lane >> 4;
+  const int tid = thread_here(), lane = tid & 63, wave = tid >> 6, cl = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const float sum = column_sum(c.l[n]);
@@ -535,7 +614,7 @@ __device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, NT
           *(v4f*)&sums[wave][n * 16 + cl][d * 16 - d0 + g * 4] = (c.o[n][d] - c.oz[n]) * f[n];
     lds_barrier();
     const int width = min(S::kChunk, D - d0), live = min(S::C, cols - col0);
-    for (int i = threadIdx.x; i < live * (width / 2); i += 64 * kTeam) {
+    for (int i = tid; i < live * (width / 2); i += 64 * kTeam) {
       const int col = i / (width / 2), d = (i - col * (width / 2)) * 2;
       const float m = top(col);
       float sum = 0.0f, x = 0.0f, y = 0.0f;
@@ -571,8 +650,8 @@ struct Cut {
   int32_t b, hk, group;
 };
 template <int D, int C>
-__device__ __forceinline__ Cut* cuts(const AttnArgs& a, int64_t blocks) {
-  return (Cut*)(a.ws + 2 * blocks * C * (D + 2));
+__device__ __forceinline__ Cut* cuts(const AttnArgs& a) {
+  return (Cut*)(a.ws + 2 * kStreamBlocks * C * (D + 2));
 }
 
 // kStream: the flat order is cut into equal shares, one a block, so a batch of any
@@ -580,23 +659,21 @@ __device__ __forceinline__ Cut* cuts(const AttnArgs& a, int64_t blocks) {
 // partial results (slot 2*block + 1 where it begins in the block, else 2*block),
 // which attention_join_kernel adds. Else a block takes one group of columns.
 template <int D, int NT, int kTeam, bool kStream>
-__global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_kernel(AttnArgs a, int64_t first_block,
-                                                                       int64_t items) {
+__global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_kernel(AttnArgs a,
+                                                                                     uint32_t first_item) {
   using S = KeysShape<D, NT, kTeam, kStream>;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t heads = a.kv.P * a.kv.Hk;
+  const int wave = uniform((int)threadIdx.x >> 6);
   KeysWave<D, NT> w(a);
   if constexpr (!kStream) {
-    const int64_t id = first_block + blockIdx.x, hk = id % heads;
+    w.head = blockIdx.x;
+    w.shard = blockIdx.y;
     int64_t sub;
     SeqRange seq;
-    w.b = find_sequence(a.kv, a.G, S::kShift, 1, id / heads, &sub, &seq);
+    w.b = find_sequence(a.kv, a.G, S::kShift, 1, first_item + blockIdx.z, &sub, &seq);
     if (w.b < 0) return;
     const int cols = seq.n * a.G;
     if ((sub << S::kShift) >= cols) return;
     const int col0 = (int)sub << S::kShift;
-    w.shard = hk / a.kv.Hk;
-    w.head = (int)(hk % a.kv.Hk);
     w.c.load(a, seq, w.shard, w.head, col0, cols);
     w.run(w.c.any_lo / kTile + wave, (w.c.any_hi + kTile - 1) / kTile, kTeam);
     join_team<D, NT, kTeam, kStream>(a, w.c, seq, w.shard, w.head, col0, cols, true, Partial{});
@@ -607,14 +684,14 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
     int b0, b1;
     const int64_t per_head =
         uniform(flat_total<64 * kTeam>(a, S::kShift, scan, &mine, &b0, &b1));
-    const int64_t all = per_head * heads, each = flat_share(all, gridDim.x, kTeam);
+    const int64_t all = per_head * a.kv.P * a.kv.Hk, each = flat_share(all, kTeam);
     const int64_t x0 = blockIdx.x * each, x1 = min(x0 + each, all);
-    Cut* cut = cuts<D, S::C>(a, gridDim.x) + blockIdx.x;
+    Cut* cut = cuts<D, S::C>(a) + blockIdx.x;
     if (x0 >= x1) {
       if (threadIdx.x == 0) cut->parts = 0;
       return;
     }
-    int64_t hk = x0 / per_head;
+    int hk = (int)divide(x0, per_head);
     flat_find<64 * kTeam>(a, S::kShift, x0 - hk * per_head, mine, b0, b1, &found);
     __syncthreads();
     w.b = __builtin_amdgcn_readfirstlane(found.b);
@@ -628,21 +705,21 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
         if (++w.b == a.kv.B) w.b = 0, ++hk;
         continue;
       }
-      const int group = (int)((x - begin) / st.tiles);
+      const int group = (int)divide(x - begin, st.tiles);
       const int64_t unit = begin + (int64_t)group * st.tiles;
       const int t0 = (int)(x - unit), t1 = (int)(min(x1, unit + st.tiles) - unit);
       const int cols = seq.n * a.G, col0 = group << S::kShift;
       w.shard = hk / a.kv.Hk;
-      w.head = (int)(hk % a.kv.Hk);
+      w.head = hk % a.kv.Hk;
       w.c.load(a, seq, w.shard, w.head, col0, cols);
       w.run(st.first + t0 + wave, st.first + t1, kTeam);
       join_team<D, NT, kTeam, kStream>(
           a, w.c, seq, w.shard, w.head, col0, cols, t1 - t0 == st.tiles,
-          partial(a, 2 * (int64_t)blockIdx.x + (t0 == 0), 2 * (int64_t)gridDim.x, S::C, D));
+          partial(a, 2 * (int64_t)blockIdx.x + (t0 == 0), 2 * kStreamBlocks, S::C, D));
       x += t1 - t0;
       if (x >= x1 && threadIdx.x == 0) {
-        const int64_t last = (unit + st.tiles - 1) / each - blockIdx.x;   // blocks after this one
-        *cut = {t0 == 0 && last > 0 ? (int32_t)last + 1 : 0, w.b, (int32_t)hk, group};
+        const int64_t last = divide(unit + st.tiles - 1, each) - blockIdx.x;   // blocks after this one
+        *cut = {t0 == 0 && last > 0 ? (int32_t)last + 1 : 0, w.b, hk, group};
       }
     }
   }
@@ -660,12 +737,12 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
   constexpr int kTeams = kItems >= kJoinThreads ? 1 : kJoinThreads / kItems;
   __shared__ v4f sums[kTeams][kItems];
   __shared__ float stat[kTeams][kItems][2];
-  const Cut cut = cuts<D, C>(a, gridDim.x)[blockIdx.x];
+  const Cut cut = cuts<D, C>(a)[blockIdx.x];
   if (cut.parts == 0) return;
   const SeqRange seq = uniform(seq_range(a.kv, cut.b));
   const int cols = seq.n * a.G, first = blockIdx.y * kSpan, col0 = (cut.group << (NT == 1 ? 4 : 5)) + first;
   if (col0 >= cols) return;
-  const int64_t slots = 2 * (int64_t)gridDim.x;
+  const int64_t slots = 2 * kStreamBlocks;
   for (int i = threadIdx.x % (kTeams == 1 ? kJoinThreads : kItems); i < kItems;
        i += kTeams == 1 ? kJoinThreads : kItems) {
     const int team = kTeams == 1 ? 0 : threadIdx.x / kItems;
@@ -783,21 +860,20 @@ __device__ __forceinline__ void keys_seen(const AttnArgs& a, const SeqRange& s, 
 }
 
 template <int D, int NT>
-__global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, int64_t first_block,
-                                                                   int64_t items) {
+__global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, uint32_t first_item,
+                                                                   uint32_t items) {
   using S = ColsShape<D, NT>;
   constexpr int NS = S::NS, ND = S::ND, C = S::C;
   __shared__ typename S::Buffer buf[2];
   const int tid = threadIdx.x, lane = tid & 63, cl = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  const int64_t heads = a.kv.P * a.kv.Hk, id = first_block + blockIdx.x;
-  const int64_t hk = id % heads, rest = id / heads;
-  const int split = (int)(rest / items);
+  const int head = blockIdx.x;
+  const int64_t shard = blockIdx.y, heads = a.kv.P * a.kv.Hk, hk = shard * a.kv.Hk + head;
+  const uint32_t id = first_item + blockIdx.z;
+  const int split = (int)(id / items);
   // the last items of a causal batch see the most keys: they go first
-  const int64_t item = items - 1 - rest % items;
-  const int64_t shard = hk / a.kv.Hk;
-  const int head = (int)(hk % a.kv.Hk);
+  const int64_t item = items - 1 - (id - split * items);
   int64_t sub;
   SeqRange seq;
   const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub, &seq);
@@ -812,7 +888,7 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, i
 
   const int col0 = block_col + wave * C;
   const bool live = col0 < cols;    // a wave without columns loads and waits with the others
-  Columns<D, NT> c;
+  Columns<D, NT, false> c;
   c.load(a, seq, shard, head, live ? col0 : block_col, cols);
   uint32_t magic = 0x43004300u;
   opaque(magic);
@@ -917,7 +993,7 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, i
       keep_branch();
       hide(kNegInf);
     }
-    c.weights(a, t);
+    c.weights(t);
 #pragma unroll
     for (int k = 0; k < 16; k += 4) {
       const v4f vs = *(const v4f*)&in.vs[(k >> 3) * 32 + g * 8 + (k & 4)];
@@ -1007,13 +1083,12 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, i
 
 // Adds the splits of an item's columns, in their order.
 template <int D, int NT>
-__global__ __launch_bounds__(256) void attention_splits_kernel(AttnArgs a, int64_t first_block,
-                                                               int64_t items) {
+__global__ __launch_bounds__(256) void attention_splits_kernel(AttnArgs a, uint32_t first_item,
+                                                               uint32_t items) {
   using S = ColsShape<D, NT>;
-  const int64_t heads = a.kv.P * a.kv.Hk, id = first_block + blockIdx.x;
-  const int64_t hk = id % heads, item = id / heads;
-  const int64_t shard = hk / a.kv.Hk;
-  const int head = (int)(hk % a.kv.Hk);
+  const int head = blockIdx.x;
+  const int64_t shard = blockIdx.y, heads = a.kv.P * a.kv.Hk, item = first_item + blockIdx.z;
+  const int64_t id = item * heads + shard * a.kv.Hk + head;
   int64_t sub;
   SeqRange seq;
   const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub, &seq);
@@ -1050,37 +1125,37 @@ __global__ __launch_bounds__(256) void attention_splits_kernel(AttnArgs a, int64
   }
 }
 
-constexpr int64_t kMaxLaunch = int64_t(1) << 22;   // blocks of a launch
+// Calls f(first, n) for items in launches of as many as a grid's third axis holds.
+template <typename F>
+hipError_t each_launch(int64_t items, F f) {
+  for (int64_t i = 0; i < items; i += 65535) f((uint32_t)i, (unsigned)(items - i < 65535 ? items - i : 65535));
+  return hipGetLastError();
+}
 
 template <int D, int NT, int kTeam>
 hipError_t launch_keys(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
-  const int64_t blocks = plan.items * a.kv.P * a.kv.Hk;
-  for (int64_t b = 0; b < blocks; b += kMaxLaunch)
+  return each_launch(plan.items, [&](uint32_t first, unsigned n) {
     attention_keys_kernel<D, NT, kTeam, false>
-        <<<dim3((unsigned)(blocks - b < kMaxLaunch ? blocks - b : kMaxLaunch)), 64 * kTeam, 0, s>>>(
-            a, b, plan.items);
-  return hipGetLastError();
+        <<<dim3(a.kv.Hk, (unsigned)a.kv.P, n), 64 * kTeam, 0, s>>>(a, first);
+  });
 }
 template <int D, int NT>
-hipError_t launch_stream(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
-  attention_keys_kernel<D, NT, 4, true><<<dim3((unsigned)plan.splits), 256, 0, s>>>(a, 0, 0);
-  attention_join_kernel<D, NT><<<dim3((unsigned)plan.splits, 4), kJoinThreads, 0, s>>>(a);
+hipError_t launch_stream(const AttnArgs& a, hipStream_t s) {
+  attention_keys_kernel<D, NT, 4, true><<<dim3(kStreamBlocks), 256, 0, s>>>(a, 0);
+  attention_join_kernel<D, NT><<<dim3(kStreamBlocks, 4), kJoinThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 template <int D>
 hipError_t launch_columns(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
   constexpr int NT = D <= 128 ? 2 : 1;
-  const int64_t units = plan.items * a.kv.P * a.kv.Hk, blocks = units * plan.splits;
-  for (int64_t b = 0; b < blocks; b += kMaxLaunch)
-    attention_columns_kernel<D, NT>
-        <<<dim3((unsigned)(blocks - b < kMaxLaunch ? blocks - b : kMaxLaunch)), 256, 0, s>>>(
-            a, b, plan.items);
-  if (plan.splits > 1)
-    for (int64_t b = 0; b < units; b += kMaxLaunch)
-      attention_splits_kernel<D, NT>
-          <<<dim3((unsigned)(units - b < kMaxLaunch ? units - b : kMaxLaunch)), 256, 0, s>>>(
-              a, b, plan.items);
-  return hipGetLastError();
+  const uint32_t items = (uint32_t)plan.items;
+  const hipError_t e = each_launch(plan.items * plan.splits, [&](uint32_t first, unsigned n) {
+    attention_columns_kernel<D, NT><<<dim3(a.kv.Hk, (unsigned)a.kv.P, n), 256, 0, s>>>(a, first, items);
+  });
+  if (e != hipSuccess || plan.splits == 1) return e;
+  return each_launch(plan.items, [&](uint32_t first, unsigned n) {
+    attention_splits_kernel<D, NT><<<dim3(a.kv.Hk, (unsigned)a.kv.P, n), 256, 0, s>>>(a, first, items);
+  });
 }
 
 template <int D>
@@ -1089,7 +1164,7 @@ hipError_t launch_head(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     case kAttnKeys8:
       if constexpr (D <= 128) return launch_keys<D, 1, 8>(a, plan, s);
     case kAttnKeys4: return launch_keys<D, 1, 4>(a, plan, s);
-    case kAttnStream: return launch_stream<D, 1>(a, plan, s);
+    case kAttnStream: return launch_stream<D, 1>(a, s);
     default: return launch_columns<D>(a, plan, s);
   }
 }
@@ -1106,12 +1181,14 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
     // groups of columns that exist, as far as the host knows: each row has one at least
     const int64_t rows = T < B ? T : B;
     const int64_t units = (rows > columns / 16 ? rows : columns / 16) * heads;
-    if (max_length <= 1024 || units >= 4096) {
+    // A block takes a group of columns whole where that leaves none much longer than
+    // an equal share of a full chip: 512 blocks of up to 4096 keys, fewer of fewer.
+    const int64_t longest = units >= 512 ? 4096 : units * 8 > 1024 ? units * 8 : 1024;
+    if (max_length <= longest || units >= 4096) {
       p.kind = units <= 256 && D <= 128 ? kAttnKeys8 : kAttnKeys4;
     } else {
       p.kind = kAttnStream;
-      p.splits = 512;   // two blocks a CU
-      p.workspace = (size_t)(2 * p.splits * 16) * (D + 2) * 4 + p.splits * sizeof(Cut);
+      p.workspace = (size_t)(2 * kStreamBlocks * 16) * (D + 2) * 4 + kStreamBlocks * sizeof(Cut);
     }
     return p;
   }

@@ -144,12 +144,12 @@ __device__ __forceinline__ void load_run(const void* base, int64_t first, float 
 
 template <int D, int kType>
 __global__ __launch_bounds__(kThreads) void kv_append_heads_kernel(HeadRows k, HeadRows v,
-                                                                   RopeArgs rope, KvArgs a) {
+                                                                   RopeArgs rope, KvArgs a,
+                                                                   uint32_t first_item) {
   constexpr int W = D / 16, kPitch = D / 4 + 1;
   __shared__ uint32_t codes[kBlockTokens * kPitch];
-  const int64_t hk = blockIdx.x % (a.P * a.Hk), item = blockIdx.x / (a.P * a.Hk);
-  const int64_t shard = hk / a.Hk;
-  const int head = (int)(hk % a.Hk);
+  const int64_t shard = blockIdx.y, item = first_item + blockIdx.z;
+  const int head = blockIdx.x;
   Place at;
   if (!find_place(a, item, shard, head, &at)) return;
   const int t = threadIdx.x / 8, sub = threadIdx.x % 8;
@@ -257,25 +257,15 @@ __global__ __launch_bounds__(kThreads) void kv_append_heads_kernel(HeadRows k, H
   }
 }
 
-template <int D>
-hipError_t launch_append_heads(const HeadRows& k, const HeadRows& v, const RopeArgs& rope,
-                               const KvArgs& a, dim3 grid, hipStream_t s) {
-  if (k.type == kF32)
-    kv_append_heads_kernel<D, kF32><<<grid, kThreads, 0, s>>>(k, v, rope, a);
-  else
-    kv_append_heads_kernel<D, kBf16><<<grid, kThreads, 0, s>>>(k, v, rope, a);
-  return hipGetLastError();
-}
-
 template <int D, bool kVector>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(HeadRows k, HeadRows v, RopeArgs rope,
-                                                             KvArgs a, int64_t items) {
+                                                             KvArgs a,
+                                                             uint32_t first_item) {
   constexpr int E = D / 8, kPitch = D + 4;
   __shared__ float tile[2][kBlockTokens * kPitch];
   __shared__ uint32_t codes[kBlockTokens * (E * 2 + 1)];   // a row of D bytes and 4 more
-  const int64_t hk = blockIdx.x % (a.P * a.Hk), item = blockIdx.x / (a.P * a.Hk);
-  const int64_t shard = hk / a.Hk;
-  const int head = (int)(hk % a.Hk);
+  const int64_t shard = blockIdx.y, item = first_item + blockIdx.z;
+  const int head = blockIdx.x;
   Place at;
   if (!find_place(a, item, shard, head, &at) || at.at < 0) return;
   load_tile<kVector>(k, shard * k.shard + head * k.head, D, at, tile[0], kPitch);
@@ -371,12 +361,11 @@ __device__ __forceinline__ void store_rows(const HeadRows& r, int64_t e, const f
 
 template <int D, bool kVector>
 __global__ __launch_bounds__(kThreads) void kv_gather_kernel(HeadRows k, HeadRows v, KvArgs a,
-                                                             int64_t items) {
+                                                             uint32_t first_item) {
   constexpr int E = D / 8;
   __shared__ uint32_t codes[kBlockTokens * (E * 2 + 1)];
-  const int64_t hk = blockIdx.x % (a.P * a.Hk), item = blockIdx.x / (a.P * a.Hk);
-  const int64_t shard = hk / a.Hk;
-  const int head = (int)(hk % a.Hk);
+  const int64_t shard = blockIdx.y, item = first_item + blockIdx.z;
+  const int head = blockIdx.x;
   Place at;
   if (!find_place(a, item, shard, head, &at)) return;
   const uint8_t* block = a.cache + at.at;
@@ -417,59 +406,77 @@ __global__ __launch_bounds__(kThreads) void kv_gather_kernel(HeadRows k, HeadRow
   if (v.p) store_rows<kVector>(v, shard * v.shard + row * v.pitch + head * v.head + sub * E, vx, E);
 }
 
-// Blocks of 32 places that T rows of B sequences can touch (find_sequence).
-int64_t place_items(const KvArgs& a) { return a.T / kBlockTokens + 2 * (int64_t)a.B; }
-
-}  // namespace
-
-#define BTQ_FOR_HEAD(D, CALL)            \
-  switch (D) {                           \
-    case 32: CALL(32); break;            \
-    case 64: CALL(64); break;            \
-    case 96: CALL(96); break;            \
-    case 128: CALL(128); break;          \
-    case 160: CALL(160); break;          \
-    case 192: CALL(192); break;          \
-    case 224: CALL(224); break;          \
-    default: CALL(256); break;           \
-  }
-
-hipError_t launch_kv_append(const HeadRows& k, const HeadRows& v, const RopeArgs& rope,
-                            const KvArgs& a, hipStream_t s) {
-  const int64_t items = place_items(a);
-  const dim3 grid((unsigned)(items * a.P * a.Hk));
-  const bool vec = on16(k) && on16(v);
-  if (vec && a.D % 64 == 0 &&
-      (!rope.cos || (rope.dim == a.D && ((uintptr_t)rope.cos & 15) == 0 && ((uintptr_t)rope.sin & 15) == 0))) {
-    switch (a.D) {
-      case 64: return launch_append_heads<64>(k, v, rope, a, grid, s);
-      case 128: return launch_append_heads<128>(k, v, rope, a, grid, s);
-      case 192: return launch_append_heads<192>(k, v, rope, a, grid, s);
-      default: return launch_append_heads<256>(k, v, rope, a, grid, s);
-    }
-  }
-#define BTQ_CALL(N)                                                                      \
-  if (vec)                                                                               \
-    kv_append_kernel<N, true><<<grid, kThreads, 0, s>>>(k, v, rope, a, items);           \
-  else                                                                                   \
-    kv_append_kernel<N, false><<<grid, kThreads, 0, s>>>(k, v, rope, a, items)
-  BTQ_FOR_HEAD(a.D, BTQ_CALL)
-#undef BTQ_CALL
+// Launches over the blocks of 32 places that T rows of B sequences can touch
+// (find_sequence), as many at once as a grid's third axis holds.
+template <typename F>
+hipError_t each_launch(const KvArgs& a, F f) {
+  const int64_t items = a.T / kBlockTokens + 2 * (int64_t)a.B;
+  for (int64_t i = 0; i < items; i += 65535)
+    f(dim3(a.Hk, (unsigned)a.P, (unsigned)(items - i < 65535 ? items - i : 65535)), (uint32_t)i);
   return hipGetLastError();
 }
 
-hipError_t launch_kv_gather(const HeadRows& k, const HeadRows& v, const KvArgs& a, hipStream_t s) {
-  const int64_t items = place_items(a);
-  const dim3 grid((unsigned)(items * a.P * a.Hk));
+#define BTQ_FOR_HEAD(D, CALL)            \
+  switch (D) {                           \
+    case 32: return CALL(32);            \
+    case 64: return CALL(64);            \
+    case 96: return CALL(96);            \
+    case 128: return CALL(128);          \
+    case 160: return CALL(160);          \
+    case 192: return CALL(192);          \
+    case 224: return CALL(224);          \
+    default: return CALL(256);           \
+  }
+
+template <int D, int kType>
+hipError_t append_heads(const HeadRows& k, const HeadRows& v, const RopeArgs& rope, const KvArgs& a,
+                        hipStream_t s) {
+  return each_launch(a, [&](dim3 grid, uint32_t first) {
+    kv_append_heads_kernel<D, kType><<<grid, kThreads, 0, s>>>(k, v, rope, a, first);
+  });
+}
+template <int D, bool kVector>
+hipError_t append(const HeadRows& k, const HeadRows& v, const RopeArgs& rope, const KvArgs& a,
+                  hipStream_t s) {
+  return each_launch(a, [&](dim3 grid, uint32_t first) {
+    kv_append_kernel<D, kVector><<<grid, kThreads, 0, s>>>(k, v, rope, a, first);
+  });
+}
+template <int D, bool kVector>
+hipError_t gather(const HeadRows& k, const HeadRows& v, const KvArgs& a, hipStream_t s) {
+  return each_launch(a, [&](dim3 grid, uint32_t first) {
+    kv_gather_kernel<D, kVector><<<grid, kThreads, 0, s>>>(k, v, a, first);
+  });
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const HeadRows& k, const HeadRows& v, const RopeArgs& rope,
+                            const KvArgs& a, hipStream_t s) {
   const bool vec = on16(k) && on16(v);
-#define BTQ_CALL(N)                                                                      \
-  if (vec)                                                                               \
-    kv_gather_kernel<N, true><<<grid, kThreads, 0, s>>>(k, v, a, items);                 \
-  else                                                                                   \
-    kv_gather_kernel<N, false><<<grid, kThreads, 0, s>>>(k, v, a, items)
+  const bool whole = !rope.cos || (rope.dim == a.D && ((uintptr_t)rope.cos & 15) == 0 &&
+                                   ((uintptr_t)rope.sin & 15) == 0);
+  if (vec && whole && a.D % 64 == 0) {
+#define BTQ_CALL(N) \
+  (k.type == kF32 ? append_heads<N, kF32>(k, v, rope, a, s) : append_heads<N, kBf16>(k, v, rope, a, s))
+    switch (a.D) {
+      case 64: return BTQ_CALL(64);
+      case 128: return BTQ_CALL(128);
+      case 192: return BTQ_CALL(192);
+      default: return BTQ_CALL(256);
+    }
+#undef BTQ_CALL
+  }
+#define BTQ_CALL(N) (vec ? append<N, true>(k, v, rope, a, s) : append<N, false>(k, v, rope, a, s))
   BTQ_FOR_HEAD(a.D, BTQ_CALL)
 #undef BTQ_CALL
-  return hipGetLastError();
+}
+
+hipError_t launch_kv_gather(const HeadRows& k, const HeadRows& v, const KvArgs& a, hipStream_t s) {
+  const bool vec = on16(k) && on16(v);
+#define BTQ_CALL(N) (vec ? gather<N, true>(k, v, a, s) : gather<N, false>(k, v, a, s))
+  BTQ_FOR_HEAD(a.D, BTQ_CALL)
+#undef BTQ_CALL
 }
 
 }  // namespace btq
