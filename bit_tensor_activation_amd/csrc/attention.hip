@@ -30,6 +30,9 @@ namespace {
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef uint16_t v2s __attribute__((ext_vector_type(2)));
+typedef short v2i __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -INFINITY;
 
@@ -129,9 +132,10 @@ struct Columns {
   int all_lo, all_hi;        // keys that every column sees
   int any_lo, any_hi;        // keys that some column sees
 
-  // Columns [col0, col0 + 16*NT) of a sequence, of which those below cols exist.
-  __device__ __forceinline__ void load(const AttnArgs& a, const SeqRange& s, int64_t shard, int head,
-                                       int col0, int cols) {
+  // Columns [col0, col0 + 16*NT) of a sequence, of which those below cols exist, and
+  // their queries as they are, this lane's quarter of the features.
+  __device__ __forceinline__ void fetch(const AttnArgs& a, const SeqRange& s, int64_t shard, int head,
+                                        int col0, int cols, v4u (&w)[NT][NS]) {
     const int lane = thread_here() & 63, cl = lane & 15, g = lane >> 4;
     // (col0 the same in all lanes; col/G by a product, exact below 2^32/G)
     const int first = col0 / a.G, rest = col0 - first * a.G;
@@ -155,33 +159,21 @@ struct Columns {
                             (s.begin + (int64_t)qi) * a.q.pitch +
                             (head * (int64_t)a.G + (live ? col : col0) - (int64_t)qi * a.G) * a.q.head +
                             g * (D / 4);
-      v4u w[NS];
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         if (a.q_on16) {
-          w[i] = *(const v4u*)(row + 8 * i);
+          w[n][i] = *(const v4u*)(row + 8 * i);
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            w[i][j] = row[8 * i + 2 * j] | (uint32_t)row[8 * i + 2 * j + 1] << 16;
+            w[n][i][j] = row[8 * i + 2 * j] | (uint32_t)row[8 * i + 2 * j + 1] << 16;
         }
-        if (!live) w[i] = v4u{0, 0, 0, 0};
       }
-      if constexpr (kBytes) {
-        to_bytes(n, w);
-        unit[n] *= a.scale2;
-      } else {
-        float sum = 0.0f;
+    }
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            sum += __uint_as_float(w[i][j] << 16) + __uint_as_float(w[i][j] & 0xffff0000u);
-          q[n][i] = deal(w[i]);
-        }
-        qsum[n] = column_sum(sum);
-        unit[n] = a.scale2;
-      }
+    for (int n = 0; n < NT; ++n) {
       oz[n] = v4f{0, 0, 0, 0};
 #pragma unroll
       for (int d = 0; d < ND; ++d) o[n][d] = v4f{0, 0, 0, 0};
@@ -189,53 +181,65 @@ struct Columns {
       l[n] = 0.0f;
     }
   }
-
+  // (a column that does not exist repeats the first one; its results go nowhere)
+  __device__ __forceinline__ void take(float scale2, const v4u (&w)[NT][NS]) {
+    v2b ones;
+    ones[0] = ones[1] = (__bf16)1.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2b, (uint32_t)w[n][i][j]), ones, sum, false);
+      qsum[n] = column_sum(sum);
+      unit[n] = scale2;
+      if constexpr (kBytes) {
+        to_bytes(n, w[n]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) q[n][i] = deal(w[n][i]);
+      }
+    }
+  }
   __device__ __forceinline__ void to_bytes(int n, const v4u (&w)[NS]) {
-    float top = 0.0f;
-    bool bad = false;
+    v2s top2 = {0, 0};   // largest |q| of the even and of the odd features, as bits
 #pragma unroll
     for (int i = 0; i < NS; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float x = fabsf(__uint_as_float(h ? w[i][j] & 0xffff0000u : w[i][j] << 16));
-          top = fmaxf(top, x);
-          bad |= !(x < INFINITY);
-        }
-    top = column_max(top);
-    // 2^(7 - exponent of top), within the powers that have a reciprocal
-    const int e = clamp_int((int)(__float_as_uint(top) >> 23), 20, 254);
-    const float up = __uint_as_float((uint32_t)(254 + 7 - e) << 23);
-    unit[n] = 512.0f / up;
-    float sum = 0.0f;
+        top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(v2s, (uint32_t)w[i][j] & 0x7fff7fffu));
+    const float top = column_max(__uint_as_float((uint32_t)max(top2[0], top2[1]) << 16));
+    const uint32_t bits = __float_as_uint(top);
+    // 2^(exponent of top - 7), within the powers that have a reciprocal
+    const float down = __uint_as_float((uint32_t)(clamp_int((int)(bits >> 23), 20, 254) - 7) << 23);
+    unit[n] *= down * 512.0f;
+    // NaN and Inf in a query (NaN is above Inf as bits) make all its scores NaN
+    qsum[n] = bits < 0x7f800000u ? qsum[n] / down * 0x1p-9f : __uint_as_float(0x7fc00000u);
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       uint32_t r[2][2];   // [first, second float][even, odd features]
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float x[4];
-        int first = 0, second = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[j] = __uint_as_float(h ? w[i][j] & 0xffff0000u : w[i][j] << 16) * up;
-        first = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], first, false);
-        first = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], first, true);
-        const auto a0 = __builtin_amdgcn_cvt_pk_f32_fp8(first, false);
-        const auto a1 = __builtin_amdgcn_cvt_pk_f32_fp8(first, true);
-        second = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] - a0[0], x[1] - a0[1], second, false);
-        second = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] - a1[0], x[3] - a1[1], second, true);
-        const auto b0 = __builtin_amdgcn_cvt_pk_f32_fp8(second, false);
-        const auto b1 = __builtin_amdgcn_cvt_pk_f32_fp8(second, true);
-        sum += (a0[0] + b0[0]) + (a0[1] + b0[1]) + (a1[0] + b1[0]) + (a1[1] + b1[1]);
-        r[0][h] = (uint32_t)first;
-        r[1][h] = (uint32_t)second;
+        // features h, 2 + h, 4 + h and 6 + h
+        const uint32_t x01 = __builtin_amdgcn_perm(w[i][1], w[i][0], h ? 0x07060302u : 0x05040100u);
+        const uint32_t x23 = __builtin_amdgcn_perm(w[i][3], w[i][2], h ? 0x07060302u : 0x05040100u);
+        v2i first = {0, 0}, second = {0, 0};
+        first = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(first, __builtin_bit_cast(v2b, x01), down, false);
+        first = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(first, __builtin_bit_cast(v2b, x23), down, true);
+        r[0][h] = __builtin_bit_cast(uint32_t, first);
+        const auto a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(r[0][h], down, false);
+        const auto a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(r[0][h], down, true);
+        second = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(
+            second, __uint_as_float(x01 << 16) - a0[0], __uint_as_float(x01 & 0xffff0000u) - a0[1], down, false);
+        second = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(
+            second, __uint_as_float(x23 << 16) - a1[0], __uint_as_float(x23 & 0xffff0000u) - a1[1], down, true);
+        r[1][h] = __builtin_bit_cast(uint32_t, second);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) q8[n][i][k] = (long)((uint64_t)r[k][1] << 32 | r[k][0]);
     }
-    // NaN and Inf in a query make all its scores NaN
-    qsum[n] = column_sum(bad ? __uint_as_float(0x7fc00000u) : sum * 0x1p-9f);
   }
 
   // Scores t (value k is a key of the lane's) to weights p; l and the sums follow
@@ -284,6 +288,14 @@ __device__ __forceinline__ v8b weights_to_bf16(const float* p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16x2(p[i], p[4 + i]);
   return as_bf16(w);
+}
+
+// Keys that some column of [col0, col1) sees: [lo, hi).
+__device__ __forceinline__ void keys_seen(const AttnArgs& a, const SeqRange& s, int col0, int col1,
+                                          int* lo, int* hi) {
+  const int first = s.first() + col0 / a.G, last = s.first() + (col1 - 1) / a.G;
+  *hi = clamp_int(a.causal ? last + 1 : s.length, 0, s.length);
+  *lo = a.window ? min(max(first + 1 - a.window, 0), *hi) : 0;
 }
 
 // ---- results ----
@@ -363,11 +375,16 @@ struct KeysWave {
     return there;
   }
 
-  // Tiles begin, begin + step, .. of [begin, end).
-  __device__ __forceinline__ void run(int begin, int end, int step) {
+  // Tiles begin, begin + step, .. of [begin, end) of columns [col0, ..) of a sequence.
+  // The page numbers, the queries and the first tile load one behind the other.
+  __device__ __forceinline__ void run(const SeqRange& seq, int col0, int cols, int begin, int end,
+                                      int step) {
+    c.clear();
     if (begin >= end) return;
-    const int lane = threadIdx.x & 63, cl = lane & 15, g = lane >> 4;
+    const int lane = thread_here() & 63, cl = lane & 15, g = lane >> 4;
     int pk = page(begin, cl / 4), pv = page(begin, g);
+    v4u raw[NT][NS];
+    c.fetch(a, seq, shard, head, col0, cols, raw);
     int64_t kat, vat;
     place(begin, end, cl / 4, pk, &kat);
     bool there = place(begin, end, g, pv, &vat);
@@ -375,6 +392,9 @@ struct KeysWave {
     load_keys(kat);
     load_words(vat, kw, vw);
     load_values(vat);
+    c.take(a.scale2, raw);
+    // whether columns see different keys
+    const int uneven = c.all_lo > c.any_lo || c.all_hi < c.any_hi ? 2 : 0;
     for (int tile = begin; tile < end; tile += step) {
       const int key0 = tile * kTile;
       const bool full = key0 >= c.all_lo && key0 + kTile <= c.all_hi && __ballot(!there) == 0;
@@ -383,7 +403,7 @@ struct KeysWave {
       pk = page(tile + 2 * step, cl / 4), pv = page(tile + 2 * step, g);
       uint32_t kw_next[2], vw_next[2];
       load_words(vat, kw_next, vw_next);
-      compute(kat, vat, key0, there, __builtin_amdgcn_readfirstlane(!full));
+      compute(kat, vat, key0, there, uniform(full ? 0 : 1 | uneven));
 #pragma unroll
       for (int j = 0; j < 2; ++j) kw[j] = kw_next[j], vw[j] = vw_next[j];
       there = there_next;
@@ -422,6 +442,13 @@ struct KeysWave {
       ks[h] = __uint_as_float(kw[h] & 0xffff0000u);
       kz[h] = 128.0f - __uint_as_float(kw[h] << 16);
       vs[h] = __uint_as_float(vw[h] & 0xffff0000u);
+    }
+    if (mask) {   // places that no column sees may hold anything
+      keep_branch();
+      const int cl = threadIdx.x & 15, key = base + 8 * (cl >> 2) + (cl & 3);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (!there || key + 4 * h < c.any_lo || key + 4 * h >= c.any_hi) vs[h] = 0.0f;
     }
     const uint32_t vz = (vw[0] & 0xfu) | (vw[1] & 0xfu) << 16 | magic;
     static_for<0, 4, KS>([&](auto step) {
@@ -473,7 +500,7 @@ struct KeysWave {
 #pragma unroll
         for (int n = 0; n < NT; ++n) t[n][key] *= from_lane<L>(vs[key / 4 % 2]);
       });
-      if (mask) {   // the scale of a hidden value may be NaN
+      if (mask & 2) {   // the scale of a value that only others see may be NaN
         keep_branch();
         hide(0.0f);
       }
@@ -674,8 +701,9 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
     const int cols = seq.n * a.G;
     if ((sub << S::kShift) >= cols) return;
     const int col0 = (int)sub << S::kShift;
-    w.c.load(a, seq, w.shard, w.head, col0, cols);
-    w.run(w.c.any_lo / kTile + wave, (w.c.any_hi + kTile - 1) / kTile, kTeam);
+    int lo, hi;
+    keys_seen(a, seq, col0, min(col0 + S::C, cols), &lo, &hi);
+    w.run(seq, col0, cols, lo / kTile + wave, (hi + kTile - 1) / kTile, kTeam);
     join_team<D, NT, kTeam, kStream>(a, w.c, seq, w.shard, w.head, col0, cols, true, Partial{});
   } else {
     __shared__ int64_t scan[kTeam];
@@ -711,8 +739,7 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
       const int cols = seq.n * a.G, col0 = group << S::kShift;
       w.shard = hk / a.kv.Hk;
       w.head = hk % a.kv.Hk;
-      w.c.load(a, seq, w.shard, w.head, col0, cols);
-      w.run(st.first + t0 + wave, st.first + t1, kTeam);
+      w.run(seq, col0, cols, st.first + t0 + wave, st.first + t1, kTeam);
       join_team<D, NT, kTeam, kStream>(
           a, w.c, seq, w.shard, w.head, col0, cols, t1 - t0 == st.tiles,
           partial(a, 2 * (int64_t)blockIdx.x + (t0 == 0), 2 * kStreamBlocks, S::C, D));
@@ -851,14 +878,6 @@ __device__ __forceinline__ KeyTiles key_tiles(int lo, int hi, int split, int spl
   k.splits = max((n + each - 1) / each, 1);
   return k;
 }
-// Keys that some column of [col0, col1) sees: [lo, hi).
-__device__ __forceinline__ void keys_seen(const AttnArgs& a, const SeqRange& s, int col0, int col1,
-                                          int* lo, int* hi) {
-  const int first = s.first() + col0 / a.G, last = s.first() + (col1 - 1) / a.G;
-  *hi = clamp_int(a.causal ? last + 1 : s.length, 0, s.length);
-  *lo = a.window ? min(max(first + 1 - a.window, 0), *hi) : 0;
-}
-
 template <int D, int NT>
 __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, uint32_t first_item,
                                                                    uint32_t items) {
@@ -889,7 +908,12 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
   const int col0 = block_col + wave * C;
   const bool live = col0 < cols;    // a wave without columns loads and waits with the others
   Columns<D, NT, false> c;
-  c.load(a, seq, shard, head, live ? col0 : block_col, cols);
+  {
+    v4u raw[NT][NS];
+    c.fetch(a, seq, shard, head, live ? col0 : block_col, cols, raw);
+    c.clear();
+    c.take(a.scale2, raw);
+  }
   uint32_t magic = 0x43004300u;
   opaque(magic);
 
