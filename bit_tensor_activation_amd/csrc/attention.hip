@@ -262,7 +262,7 @@ struct Columns {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float m = fmaxf(m2[n], top[n]);
-        const float f = m == kNegInf ? 1.0f : exp2f(m2[n] - m);
+        const float f = m == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m2[n] - m);
         m2[n] = m;
         l[n] *= f;
         oz[n] *= f;
@@ -305,15 +305,18 @@ __device__ __forceinline__ void store_out2(const AttnArgs& a, int64_t at, float 
   else
     *(float2*)((float*)a.out + at) = make_float2(x, y);
 }
-// Row of out and lse of a column.
+// Row of out and lse of a column. (col/G by a product where that is exact.)
 __device__ __forceinline__ int64_t out_row(const AttnArgs& a, const SeqRange& s, int64_t shard,
                                            int head, int col) {
-  return (shard * a.kv.T + s.begin + col / a.G) * a.Hq + head * a.G + col % a.G;
+  const int q = a.G == 1 ? col
+                         : (int64_t)col * a.G < (int64_t(1) << 32) ? (int)__umulhi((uint32_t)col, a.G_inverse)
+                                                                   : col / a.G;
+  return (shard * a.kv.T + s.begin + q) * a.Hq + head * a.G + (col - q * a.G);
 }
 // Factor of sums relative to the maximum m2 when they join others under m. Where
 // no score was above -Inf the sum of p is 0, or NaN if the scores were.
 __device__ __forceinline__ float share(float m2, float sum, float m) {
-  return m2 == kNegInf ? sum : exp2f(m2 - m);
+  return m2 == kNegInf ? sum : __builtin_amdgcn_exp2f(m2 - m);
 }
 __device__ __forceinline__ float lse_of(float m2, float l) {
   return l > 0.0f || l != l ? 0.6931471805599453f * (m2 + log2f(l)) : kNegInf;
@@ -336,12 +339,10 @@ __device__ __forceinline__ Partial partial(const AttnArgs& a, int64_t slot, int6
 constexpr int kTile = 128;
 constexpr int kTileBlocks = kTile / kBlockTokens;
 
-template <int D, int NT, int kTeam, bool kStream>
+template <int NT>
 struct KeysShape {
   static constexpr int C = 16 * NT;
   static constexpr int kShift = NT == 1 ? 4 : 5;
-  static constexpr int kChunkMax = 128 * 4 / (kTeam * NT);   // features of a round of the join
-  static constexpr int kChunk = D < kChunkMax ? D : kChunkMax;
 };
 
 template <int D, int NT>
@@ -602,69 +603,59 @@ __device__ __forceinline__ int64_t flat_share(int64_t all, int team) {
   return n < team ? team : n;
 }
 
-// The team's sums, each relative to the common maximum, added in the waves' order;
-// to `out` where they are whole, else to a partial result.
+// The sums of the team's first `waves` waves (the others had no tile), each relative
+// to the common maximum, added in the waves' order; to `out` where they are whole,
+// else to a partial result.
 template <int D, int NT, int kTeam, bool kStream>
 __device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, NT, true>& c, const SeqRange& seq,
-                                          int64_t shard, int head, int col0, int cols, bool whole,
+                                          int64_t shard, int head, int col0, int cols, int waves, bool whole,
                                           const Partial& part) {
-  using S = KeysShape<D, NT, kTeam, kStream>;
-  __shared__ float stat[kTeam][S::C][2];
-  __shared__ float sums[kTeam][S::C][S::kChunk + 4];
+  constexpr int C = 16 * NT, kVec = D / 4;
+  __shared__ float2 stat[kTeam][C];       // maximum and sum of p
+  __shared__ float factor[C];             // 1/sum of all, or 1
+  __shared__ v4f sums[kTeam][C][kVec + 1];
   const int tid = thread_here(), lane = tid & 63, wave = tid >> 6, cl = lane & 15, g = lane >> 4;
+  const int live = min(C, cols - col0);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const float sum = column_sum(c.l[n]);
-    if (g == 0) {
-      stat[wave][n * 16 + cl][0] = c.m2[n];
-      stat[wave][n * 16 + cl][1] = sum;
+    if (g == 0) stat[wave][n * 16 + cl] = make_float2(c.m2[n], sum);
+  }
+  lds_barrier();
+  if (wave < waves) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = n * 16 + cl;
+      float m = kNegInf;
+      for (int w = 0; w < waves; ++w) m = fmaxf(m, stat[w][col].x);
+      const float f = share(c.m2[n], stat[wave][col].y, m);
+      if (col < live) {
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) sums[wave][col][d * 4 + g] = (c.o[n][d] - c.oz[n]) * f;
+      }
+      if (wave == 0 && g == 0 && col < live) {
+        float sum = 0.0f;
+        for (int w = 0; w < waves; ++w) sum += stat[w][col].y * share(stat[w][col].x, stat[w][col].y, m);
+        factor[col] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (!whole)
+          *(float2*)(part.stats + 2 * col) = make_float2(m, sum);
+        else if (a.lse)
+          a.lse[out_row(a, seq, shard, head, col0 + col)] = lse_of(m, sum);
+      }
     }
   }
   lds_barrier();
-  auto top = [&](int col) {
-    float m = stat[0][col][0];
-#pragma unroll
-    for (int w = 1; w < kTeam; ++w) m = fmaxf(m, stat[w][col][0]);
-    return m;
-  };
-  float f[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) f[n] = share(c.m2[n], stat[wave][n * 16 + cl][1], top(n * 16 + cl));
-#pragma unroll
-  for (int d0 = 0; d0 < D; d0 += S::kChunk) {
-    if (d0) lds_barrier();
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d)
-        if (d * 16 >= d0 && d * 16 < d0 + S::kChunk)
-          *(v4f*)&sums[wave][n * 16 + cl][d * 16 - d0 + g * 4] = (c.o[n][d] - c.oz[n]) * f[n];
-    lds_barrier();
-    const int width = min(S::kChunk, D - d0), live = min(S::C, cols - col0);
-    for (int i = tid; i < live * (width / 2); i += 64 * kTeam) {
-      const int col = i / (width / 2), d = (i - col * (width / 2)) * 2;
-      const float m = top(col);
-      float sum = 0.0f, x = 0.0f, y = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kTeam; ++w) {
-        const float l = stat[w][col][1];
-        sum += l * share(stat[w][col][0], l, m);
-        const float2 v = *(const float2*)&sums[w][col][d];
-        x += v.x;
-        y += v.y;
-      }
-      if (whole) {
-        const int64_t at = out_row(a, seq, shard, head, col0 + col);
-        const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
-        store_out2(a, at * D + d0 + d, x * r, y * r);
-        if (a.lse && d0 + d == 0) a.lse[at] = lse_of(m, sum);
-      } else {
-        *(float2*)(part.sums + (int64_t)col * D + d0 + d) = make_float2(x, y);
-        if (d0 + d == 0) {
-          part.stats[2 * col] = m;
-          part.stats[2 * col + 1] = sum;
-        }
-      }
+  for (int i = tid; i < live * kVec; i += 64 * kTeam) {
+    const int col = i / kVec, d = i - col * kVec;
+    v4f x = sums[0][col][d];
+    for (int w = 1; w < waves; ++w) x += sums[w][col][d];
+    if (whole) {
+      x *= factor[col];
+      const int64_t at = out_row(a, seq, shard, head, col0 + col) * D + 4 * d;
+      store_out2(a, at, x[0], x[1]);
+      store_out2(a, at + 2, x[2], x[3]);
+    } else {
+      *(v4f*)(part.sums + (int64_t)col * D + 4 * d) = x;
     }
   }
   if (kStream) lds_barrier();   // the next segment writes stat and sums again
@@ -688,7 +679,7 @@ __device__ __forceinline__ Cut* cuts(const AttnArgs& a) {
 template <int D, int NT, int kTeam, bool kStream>
 __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_kernel(AttnArgs a,
                                                                                      uint32_t first_item) {
-  using S = KeysShape<D, NT, kTeam, kStream>;
+  using S = KeysShape<NT>;
   const int wave = uniform((int)threadIdx.x >> 6);
   KeysWave<D, NT> w(a);
   if constexpr (!kStream) {
@@ -703,8 +694,10 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
     const int col0 = (int)sub << S::kShift;
     int lo, hi;
     keys_seen(a, seq, col0, min(col0 + S::C, cols), &lo, &hi);
-    w.run(seq, col0, cols, lo / kTile + wave, (hi + kTile - 1) / kTile, kTeam);
-    join_team<D, NT, kTeam, kStream>(a, w.c, seq, w.shard, w.head, col0, cols, true, Partial{});
+    const int t0 = lo / kTile, t1 = (hi + kTile - 1) / kTile;
+    w.run(seq, col0, cols, t0 + wave, t1, kTeam);
+    join_team<D, NT, kTeam, kStream>(a, w.c, seq, w.shard, w.head, col0, cols, clamp_int(t1 - t0, 1, kTeam),
+                                     true, Partial{});
   } else {
     __shared__ int64_t scan[kTeam];
     __shared__ Flat found;
@@ -741,7 +734,7 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
       w.head = hk % a.kv.Hk;
       w.run(seq, col0, cols, st.first + t0 + wave, st.first + t1, kTeam);
       join_team<D, NT, kTeam, kStream>(
-          a, w.c, seq, w.shard, w.head, col0, cols, t1 - t0 == st.tiles,
+          a, w.c, seq, w.shard, w.head, col0, cols, min(t1 - t0, kTeam), t1 - t0 == st.tiles,
           partial(a, 2 * (int64_t)blockIdx.x + (t0 == 0), 2 * kStreamBlocks, S::C, D));
       x += t1 - t0;
       if (x >= x1 && threadIdx.x == 0) {
