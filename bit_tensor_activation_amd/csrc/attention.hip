@@ -33,6 +33,7 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef uint16_t v2s __attribute__((ext_vector_type(2)));
 typedef short v2i __attribute__((ext_vector_type(2)));
+typedef int v8i __attribute__((ext_vector_type(8)));
 
 constexpr float kNegInf = -INFINITY;
 
@@ -455,26 +456,61 @@ struct KeysWave {
     static_for<0, 4, KS>([&](auto step) {
       constexpr int S0 = decltype(step)::value;
       float t[NT][8 * KS];   // value 8*s + 4*h + i is key 8*(S0 + s) + 4*h + i of the lane's block
-      static_for<0, 2 * KS, 1>([&](auto group) {
-        constexpr int SH = decltype(group)::value, s = SH / 2, h = SH % 2;
-        v4f acc[NT];
+      static_for<0, KS, 1>([&](auto index) {
+        constexpr int s = decltype(index)::value;
+        // both halves together: a product waits for the one before it in its own
+        v4f acc[2][NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] = v4f{0, 0, 0, 0};
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int w = 0; w < NS; ++w) {
-          const uint32_t x = k[S0 + s][h][w];
-          const long kc = (long)((uint64_t)(x >> 4 & 0x0f0f0f0fu) << 32 | (x & 0x0f0f0f0fu));
+          for (int n = 0; n < NT; ++n) acc[h][n] = v4f{0, 0, 0, 0};
+        if constexpr (NS % 4 == 0) {
+          // 128 features an instruction, at twice the rate of 32
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int w = 0; w < NS; w += 4)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(kc, c.q8[n][w][j], acc[n], 0, 0, 0);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                v8i kc;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t x = k[S0 + s][h][w + i];
+                  kc[2 * i] = (int)(x & 0x0f0f0f0fu);
+                  kc[2 * i + 1] = (int)(x >> 4 & 0x0f0f0f0fu);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  v8i qc;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    qc[2 * i] = (int)(uint32_t)c.q8[n][w + i][j];
+                    qc[2 * i + 1] = (int)((uint64_t)c.q8[n][w + i][j] >> 32);
+                  }
+                  // (e4m3 both; block scales of 1)
+                  acc[h][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kc, qc, acc[h][n], 0, 0, 0,
+                                                                             127, 0, 127);
+                }
+              }
+        } else {
+#pragma unroll
+          for (int w = 0; w < NS; ++w)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t x = k[S0 + s][h][w];
+                const long kc = (long)((uint64_t)(x >> 4 & 0x0f0f0f0fu) << 32 | (x & 0x0f0f0f0fu));
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  acc[h][n] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(kc, c.q8[n][w][j], acc[h][n], 0, 0, 0);
+              }
         }
-        static_for<0, 4, 1>([&](auto index) {
-          constexpr int i = decltype(index)::value, L = 4 * (S0 + s) + i;
+        static_for<0, 8, 1>([&](auto value) {
+          constexpr int h = decltype(value)::value / 4, i = decltype(value)::value % 4, L = 4 * (S0 + s) + i;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            t[n][8 * s + 4 * h + i] = (acc[n][i] + from_lane<L>(kz[h]) * c.qsum[n]) * from_lane<L>(ks[h]);
+            t[n][8 * s + 4 * h + i] = (acc[h][n][i] + from_lane<L>(kz[h]) * c.qsum[n]) * from_lane<L>(ks[h]);
         });
       });
       if constexpr (S0 + KS == 4) {
