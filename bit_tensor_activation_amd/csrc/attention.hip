@@ -34,6 +34,8 @@ typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef uint16_t v2s __attribute__((ext_vector_type(2)));
 typedef short v2i __attribute__((ext_vector_type(2)));
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -INFINITY;
 
@@ -115,15 +117,16 @@ __device__ __forceinline__ void static_for(F f) {
 // ---- what a wave keeps of its columns: 16*NT of them, column n*16 + lane%16 in
 // the 4 lanes of that number ----
 //
-// Queries are operand B of the first product: bf16 as they come (kBytes false), or
-// the sum of two 8-bit floats, for keys as 8-bit floats. The latter takes them by a
-// power of 2 to below 256 (a column's largest to 128 or more); the first float holds
-// 4 bits of a value and the second the other 4 of bf16, down to 2^-10. So a query is
-// off by 2^-18 of its largest feature at most.
-template <int D, int NT, bool kBytes>
+// Queries are operand B of the first product. For keys as 8-bit floats they
+// are the sum of two of those: taken by a power of 2 to below 256 (a column's largest
+// to 128 or more), the first float holds 4 bits of a value and the second the other 4
+// of bf16, down to 2^-10, so a query is off by 2^-18 of its largest feature at most.
+// For keys as fp16 they are fp16, taken by a power of 2 to a largest of 2^13 or more:
+// exact down to 2^-27 of that.
+template <int D, int NT>
 struct Columns {
   static constexpr int NS = D / 32, ND = D / 16;
-  v8b q[NT][NS];
+  v8h q[NT][NS];
   long q8[NT][NS][2];
   float qsum[NT];            // in the units of the first product
   float unit[NT];            // what it takes to powers of 2 of p
@@ -183,7 +186,7 @@ struct Columns {
     }
   }
   // (a column that does not exist repeats the first one; its results go nowhere)
-  __device__ __forceinline__ void take(float scale2, const v4u (&w)[NT][NS]) {
+  __device__ __forceinline__ void take_bytes(float scale2, const v4u (&w)[NT][NS]) {
     v2b ones;
     ones[0] = ones[1] = (__bf16)1.0f;
 #pragma unroll
@@ -196,13 +199,45 @@ struct Columns {
           sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2b, (uint32_t)w[n][i][j]), ones, sum, false);
       qsum[n] = column_sum(sum);
       unit[n] = scale2;
-      if constexpr (kBytes) {
-        to_bytes(n, w[n]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) q[n][i] = deal(w[n][i]);
-      }
+      to_bytes(n, w[n]);
     }
+  }
+  // The largest finite |q| of the lane's features, as fp32 bits.
+  static __device__ __forceinline__ uint32_t top_of(const v4u (&w)[NT][NS]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = (h ? w[n][i][j] : w[n][i][j] << 16) & 0x7fff0000u;
+            top = max(top, x < 0x7f800000u ? x : 0u);
+          }
+    return top;
+  }
+  // q*up as fp16. NaN and Inf in a query make all its scores NaN.
+  __device__ __forceinline__ void take_halves(float up, const v4u (&w)[NT][NS]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const v4u x = __builtin_bit_cast(v4u, deal(w[n][i]));
+        v4u y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float f[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            f[h] = __uint_as_float(h ? x[j] & 0xffff0000u : x[j] << 16);
+            f[h] = fabsf(f[h]) < INFINITY ? f[h] * up : __uint_as_float(0x7fc00000u);
+          }
+          y[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(f[0], f[1]));
+        }
+        q[n][i] = __builtin_bit_cast(v8h, y);
+      }
   }
   __device__ __forceinline__ void to_bytes(int n, const v4u (&w)[NS]) {
     v2s top2 = {0, 0};   // largest |q| of the even and of the odd features, as bits
@@ -349,7 +384,7 @@ struct KeysShape {
 template <int D, int NT>
 struct KeysWave {
   static constexpr int NS = D / 32, ND = D / 16;
-  Columns<D, NT, true> c;
+  Columns<D, NT> c;
   const AttnArgs& a;
   int b, head;
   int64_t shard;
@@ -394,7 +429,7 @@ struct KeysWave {
     load_keys(kat);
     load_words(vat, kw, vw);
     load_values(vat);
-    c.take(a.scale2, raw);
+    c.take_bytes(a.scale2, raw);
     // whether columns see different keys
     const int uneven = c.all_lo > c.any_lo || c.all_hi < c.any_hi ? 2 : 0;
     for (int tile = begin; tile < end; tile += step) {
@@ -643,7 +678,7 @@ __device__ __forceinline__ int64_t flat_share(int64_t all, int team) {
 // to the common maximum, added in the waves' order; to `out` where they are whole,
 // else to a partial result.
 template <int D, int NT, int kTeam, bool kStream>
-__device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, NT, true>& c, const SeqRange& seq,
+__device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, NT>& c, const SeqRange& seq,
                                           int64_t shard, int head, int col0, int cols, int waves, bool whole,
                                           const Partial& part) {
   constexpr int C = 16 * NT, kVec = D / 4;
@@ -871,22 +906,25 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
 
 // ---- many columns: a block's 4 waves take 16*NT columns each ----
 //
-// A tile of 64 keys goes from HBM through registers, as bf16 128 + code, to LDS, in
-// the order in which the matrix instructions' operands are read: 64 lanes of 16
-// consecutive bytes. Two tiles of LDS: while one is used the next is converted,
-// and the one after is on its way from memory.
+// A tile of 64 keys (2 blocks, each loaded by 2 waves) goes from HBM through
+// registers to LDS, in the order in which the matrix instructions' operands are read:
+// 64 lanes of 16 consecutive bytes. Keys go as the exact fp16 code - z (a nibble or-ed
+// into the mantissa of 1024, less 1024 + z), values as bf16 128 + code. Two tiles of
+// LDS: while one is used the next is converted, and the one after is on its way from
+// memory. A score then takes one multiply-add from the product to the exponent, which
+// is relative to the maximum of the tiles before.
 constexpr int kColsTile = 64;
 
 template <int D, int NT>
 struct ColsShape {
   static constexpr int NS = D / 32, ND = D / 16, C = 16 * NT, kCols = 4 * C;
   static constexpr int kShift = NT == 1 ? 6 : 7;
-  static constexpr int kKeyFrags = 4 * NS, kValueFrags = 2 * ND;   // of 1 KB
-  static constexpr int VN = (2 * D + 255) / 256;                   // value rows a thread
+  static constexpr int VN = (D + 127) / 128;   // rows of values a thread
   struct Buffer {
-    v4u k[kKeyFrags][64], v[kValueFrags][64];
-    float ks[64], kz[64], vs[64];
+    v4u k[4 * NS][64], v[2 * ND][64];
+    float ks[64], vs[64];                      // scales: of keys in powers of 2 of p
     uint16_t vz[64];
+    int there[2];
   };
 };
 
@@ -913,8 +951,9 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
   using S = ColsShape<D, NT>;
   constexpr int NS = S::NS, ND = S::ND, C = S::C;
   __shared__ typename S::Buffer buf[2];
+  __shared__ uint32_t tops[4];
   const int tid = threadIdx.x, lane = tid & 63, cl = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = uniform(tid >> 6);
 
   const int head = blockIdx.x;
   const int64_t shard = blockIdx.y, heads = a.kv.P * a.kv.Hk, hk = shard * a.kv.Hk + head;
@@ -936,91 +975,98 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
 
   const int col0 = block_col + wave * C;
   const bool live = col0 < cols;    // a wave without columns loads and waits with the others
-  Columns<D, NT, false> c;
+  Columns<D, NT> c;
+  float unit;                       // from the first product to powers of 2 of p
   {
     v4u raw[NT][NS];
     c.fetch(a, seq, shard, head, live ? col0 : block_col, cols, raw);
     c.clear();
-    c.take(a.scale2, raw);
+    const uint32_t top = wave_combine(c.top_of(raw), [](uint32_t x, uint32_t y) { return max(x, y); });
+    if (lane == 0) tops[wave] = top;
+    lds_barrier();
+    const uint32_t all = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+    // 2^(13 - exponent of the block's largest |q|), within the powers that have a reciprocal
+    const float up = __uint_as_float((uint32_t)(254 + 13 - clamp_int((int)(all >> 23), 20, 254)) << 23);
+    unit = a.scale2 / up;
+    c.take_halves(up, raw);
   }
-  uint32_t magic = 0x43004300u;
+  uint32_t magic = 0x43004300u, magic16 = 0x64006400u;
   opaque(magic);
+  opaque(magic16);
 
-  // loads: a thread takes a quarter (wave) of a key's row, and rows of values
-  const int kq = lane >> 4, krow = 8 * ((lane & 15) >> 2) + 4 * (kq & 1) + (lane & 3);
-  uint32_t kreg[NS], word = 0;
+  // Loads: waves 2*j and 2*j + 1 take block j of a tile; a thread takes a quarter of a
+  // key's row and its word, rows of values, and the word of a value.
+  const int block = wave >> 1, krow = lane & 31, quarter = 2 * (wave & 1) + (lane >> 5);
+  const int kfrag = block * 2 + (krow >> 2 & 1), kslot = quarter * 16 + (krow >> 3) * 4 + (krow & 3);
+  const int vrow = (wave & 1) * 64 + lane;
+  uint32_t kreg[NS], kword, vword;
   v4u vreg[S::VN];
-  // page numbers of a tile's blocks, a step before its loads
-  int pages[2];
+  int page, there = 0;              // the page number is looked up a tile ahead
   auto look_up = [&](int tile) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int slot = min((2 * tile + j) >> a.kv.page_shift, (int)a.kv.max_pages - 1);
-      pages[j] = a.kv.table[(int64_t)b * a.kv.max_pages + slot];
-    }
+    const int slot = min((2 * tile + block) >> a.kv.page_shift, (int)a.kv.max_pages - 1);
+    page = a.kv.table[(int64_t)b * a.kv.max_pages + slot];
   };
-  int there = 0;   // bit j: block j of the tile loaded last has a page
+  int loaded = 0;                   // first place of the block loaded last
   auto load = [&](int tile) {
-    const int t = min(tile, kt.end - 1), shift = a.kv.page_shift;
-    int64_t at[2];
-    there = 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int page = uniform(pages[j]), block = 2 * t + j;
-      const bool ok = (block >> shift) < a.kv.max_pages && page >= 0 && page < a.kv.pages;
-      at[j] = ok ? ((((shard * a.kv.pages + page) * a.kv.Hk + head) << shift) +
-                    (block & ((1 << shift) - 1))) * kv_block_bytes(D)
-                 : 0;   // (the mask hides what a block without a page seems to hold)
-      there |= ok << j;
-    }
+    const int t = min(tile, kt.end - 1), shift = a.kv.page_shift, at = 2 * t + block, p = uniform(page);
+    there = (at >> shift) < a.kv.max_pages && p >= 0 && p < a.kv.pages;
+    // (the mask hides what a block without a page seems to hold)
+    const int64_t offset = there ? ((((shard * a.kv.pages + p) * a.kv.Hk + head) << shift) +
+                                    (at & ((1 << shift) - 1))) * kv_block_bytes(D)
+                                 : 0;
+    loaded = at * kBlockTokens;
     look_up(tile + 1);
-    const int64_t ka = at[kq >> 1];
-    __builtin_memcpy(kreg, a.kv.cache + ka + krow * (D / 2) + wave * (D / 8), 4 * NS);
+    const uint8_t* from = a.kv.cache + offset;
+    __builtin_memcpy(kreg, from + (uint32_t)(krow * (D / 2) + quarter * (D / 8)), 4 * NS);
+    kword = *(const uint32_t*)(from + (uint32_t)(32 * D + krow * 4));
+    vword = *(const uint32_t*)(from + (uint32_t)(32 * D + 128 + krow * 4));
 #pragma unroll
-    for (int i = 0; i < S::VN; ++i) {
-      const int r = min(i * 256 + tid, 2 * D - 1);
-      vreg[i] = *(const v4u*)(a.kv.cache + (r < D ? at[0] : at[1]) + 16 * D + (r < D ? r : r - D) * 16);
-    }
-    // words: waves 0 and 1 those of keys and of values
-    if (wave < 2) {
-      word = *(const uint32_t*)(a.kv.cache + (lane < 32 ? at[0] : at[1]) + 32 * D + 128 * wave +
-                                (lane & 31) * 4);
-      // a place that holds nothing: 0, so that it stays a number
-      if (!(there >> (lane >> 5) & 1) || t * kColsTile + lane >= seq.length) word = kZeroWord;
-    }
+    for (int i = 0; i < S::VN; ++i)
+      vreg[i] = *(const v4u*)(from + (uint32_t)(16 * D + min(vrow + 128 * i, D - 1) * 16));
   };
   auto write = [&](typename S::Buffer& o) {
+    const v2h zero = __builtin_bit_cast(v2h, (kword & 0xfu) * 0x10001u | magic16);   // 1024 + z, twice
 #pragma unroll
-    for (int w = 0; w < NS; ++w) o.k[kq * NS + w][wave * 16 + (lane & 15)] = codes_to_bf16(kreg[w], magic);
+    for (int w = 0; w < NS; ++w) {
+      const v4u x = codes_to_bf16(kreg[w], magic16);   // 1024 + code, in the same order
+      v4u y;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, (uint32_t)x[j]) - zero);
+      o.k[kfrag * NS + w][kslot] = y;
+    }
 #pragma unroll
     for (int i = 0; i < S::VN; ++i) {
-      const int r = i * 256 + tid;
-      if (2 * D % 256 != 0 && r >= 2 * D) break;
-      const int j = r < D ? 0 : 1, d = r < D ? r : r - D;
+      const int d = vrow + 128 * i;
+      if (D % 128 == 0 || d < D) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        o.v[j * ND + (d >> 4)][q * 16 + (d & 15)] = codes_to_bf16(vreg[i][q], magic);
+        for (int q = 0; q < 4; ++q)
+          o.v[block * ND + (d >> 4)][q * 16 + (d & 15)] = codes_to_bf16(vreg[i][q], magic);
+      }
     }
-    if (wave == 0) {
-      o.ks[lane] = __uint_as_float(word & 0xffff0000u);
-      o.kz[lane] = __uint_as_float(word << 16);
-    } else if (wave == 1) {
-      o.vs[lane] = __uint_as_float(word & 0xffff0000u);
-      o.vz[(lane & 32) + (lane & 24) + (lane & 3) * 2 + ((lane >> 2) & 1)] = (uint16_t)word;
+    if (quarter == 0) {
+      o.ks[block * 32 + krow] = __uint_as_float(kword & 0xffff0000u) * unit;
+    } else if (quarter == 2) {
+      // a place that holds nothing gets scale 0, so that it stays a number
+      const bool held = there && loaded + krow < seq.length;
+      o.vs[block * 32 + krow] = held ? __uint_as_float(vword & 0xffff0000u) : 0.0f;
+      o.vz[block * 32 + (krow & 24) + (krow & 3) * 2 + (krow >> 2 & 1)] = (uint16_t)(0x4300u | (vword & 0xfu));
+      if (krow == 0) o.there[block] = there;
     }
   };
-  auto compute = [&](const typename S::Buffer& in, int key0, int blocks, int mask) {
-    float t[NT][16];
+  auto compute = [&](const typename S::Buffer& in, int key0, int mask) {
+    float t[NT][16], off[NT];
     auto hide = [&](float with) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int key = key0 + (k >> 3) * 32 + g * 8 + (k & 7);
-          const bool seen = key >= c.lo[n] && key < c.hi[n] && (blocks >> (k >> 3) & 1);
+          const bool seen = key >= c.lo[n] && key < c.hi[n] && (mask >> (1 + (k >> 3)) & 1);
           t[n][k] = seen ? t[n][k] : with;
         }
     };
+#pragma unroll
+    for (int n = 0; n < NT; ++n) off[n] = c.m2[n] == kNegInf ? 0.0f : c.m2[n];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -1030,23 +1076,55 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
         for (int n = 0; n < NT; ++n) acc[n] = v4f{0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < NS; ++w) {
-          const v8b kc = as_bf16(in.k[(j * 2 + h) * NS + w][lane]);
+          const v8h kc = __builtin_bit_cast(v8h, in.k[(j * 2 + h) * NS + w][lane]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) acc[n] = mfma(kc, c.q[n][w], acc[n]);
+          for (int n = 0; n < NT; ++n)
+            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kc, c.q[n][w], acc[n], 0, 0, 0);
         }
         const v4f ks = *(const v4f*)&in.ks[j * 32 + g * 8 + h * 4];
-        const v4f kz = *(const v4f*)&in.kz[j * 32 + g * 8 + h * 4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            t[n][8 * j + 4 * h + i] = __builtin_fmaf(-kz[i], c.qsum[n], acc[n][i]) * ks[i];
+          for (int i = 0; i < 4; ++i) t[n][8 * j + 4 * h + i] = __builtin_fmaf(acc[n][i], ks[i], -off[n]);
       }
-    if (mask) {
+    if (mask & 1) {
       keep_branch();
       hide(kNegInf);
     }
-    c.weights(t);
+    // the running maximum, as in Columns::weights, but t is relative to it already
+    float top[NT];
+    bool raise = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float m = t[n][0];
+#pragma unroll
+      for (int k = 1; k < 16; ++k) m = fmaxf(m, t[n][k]);
+      top[n] = column_max(m);
+      raise |= top[n] > 8.0f || (c.m2[n] == kNegInf && top[n] > kNegInf);
+    }
+    if (__ballot(raise)) {
+      keep_branch();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const bool first = c.m2[n] == kNegInf;
+        const float up = first ? (top[n] == kNegInf ? 0.0f : top[n]) : fmaxf(top[n], 0.0f);
+        const float f = first ? 1.0f : __builtin_amdgcn_exp2f(-up);   // (nothing to scale at first)
+        c.m2[n] = first ? top[n] : c.m2[n] + up;
+        c.l[n] *= f;
+        c.oz[n] *= f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) c.o[n][d] *= f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) t[n][k] -= up;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        t[n][k] = __builtin_amdgcn_exp2f(t[n][k]);   // hidden: 0
+        c.l[n] += t[n][k];
+      }
 #pragma unroll
     for (int k = 0; k < 16; k += 4) {
       const v4f vs = *(const v4f*)&in.vs[(k >> 3) * 32 + g * 8 + (k & 4)];
@@ -1055,7 +1133,7 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[n][k + i] *= vs[i];
     }
-    if (mask) {   // the scale of a hidden value may be NaN
+    if (mask & 1) {   // the scale of a hidden value may be NaN
       keep_branch();
       hide(0.0f);
     }
@@ -1077,26 +1155,23 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
     }
   };
 
-  int there_now = 0;
   if (kt.begin < kt.end) {
     look_up(kt.begin);
     load(kt.begin);
-    there_now = there;
     write(buf[0]);
     load(kt.begin + 1);
     lds_barrier();
   }
   for (int tile = kt.begin; tile < kt.end; ++tile) {
     const int even = (tile - kt.begin) & 1;
-    const int there_next = there;
     if (tile + 1 < kt.end) {
       write(buf[even ^ 1]);
       load(tile + 2);
     }
     const int key0 = tile * kColsTile;
-    const bool full = there_now == 3 && key0 >= c.all_lo && key0 + kColsTile <= c.all_hi;
-    compute(buf[even], key0, there_now, uniform(!full));
-    there_now = there_next;
+    const int blocks = uniform(buf[even].there[0] | buf[even].there[1] << 1);
+    const bool full = blocks == 3 && key0 >= c.all_lo && key0 + kColsTile <= c.all_hi;
+    compute(buf[even], key0, blocks << 1 | (full ? 0 : 1));
     lds_barrier();
   }
   if (!live) return;
