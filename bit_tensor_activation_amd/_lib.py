@@ -11,6 +11,7 @@ import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libbtq.so")
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
 
 # Every function that include/btq.h declares: (name, restype, argtypes).
 _c = ctypes
@@ -110,6 +111,27 @@ def load() -> ctypes.CDLL:
                     fn.argtypes = args
                 _lib = lib
     return _lib
+
+
+_binding = None
+
+
+def binding():
+    """The C++ part of the Python binding (once per process)."""
+    global _binding
+    if _binding is None:
+        load()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it first "
+                               "(python -m bit_tensor_activation_amd.build)")
+        import importlib.machinery
+        import importlib.util
+        loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _binding = module
+    return _binding
 
 
 def check(status: int, what: str) -> None:

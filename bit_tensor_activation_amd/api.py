@@ -579,57 +579,19 @@ def btq_block_norm(y: Optional[torch.Tensor], residual: torch.Tensor, post: str 
     return (residual_out, n, n_scale) if int8 else (residual_out, n)
 
 
-_ROPES = {"half": _lib.BTQ_ROPE_HALF, "pairs": _lib.BTQ_ROPE_PAIRS}
-_I32, _U8 = (torch.int32,), (torch.uint8,)
-_BF16_ONLY = (torch.bfloat16, torch.int16)
+# The calls of the attention group check and pass their tensors in C++
+# (csrc/binding.cpp): with some 30 arguments each, Python takes longer for that than
+# the shortest of them run.
 
-
-def _head_rows(x: torch.Tensor, name: str, dtypes):
-    """(P or None, T, heads, D, shard, pitch and head strides) of heads [T,heads,D]
-    or [P,T,heads,D] whose last dimension is contiguous."""
-    if x.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {x.dtype}, expected one of {dtypes}")
-    shape, strides = x.shape, x.stride()
-    n = len(shape)
-    if n != 3 and n != 4:
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected [T,heads,D] or [P,T,heads,D]")
-    if strides[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    if n == 4:
-        return (*shape, *strides[:3])
-    return (None, *shape, 0, strides[0], strides[1])
-
-
-def _like_rows(x: torch.Tensor, name: str, dtypes, shape, idx: int):
-    """Strides of heads that must have `shape`, on device idx."""
-    if x.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if x.get_device() != idx:
-        raise ValueError(f"{name}: on {x.device}, expected cuda:{idx}")
-    return _head_rows(x, name, dtypes)[4:]
-
-
-def _rope_args(cos, sin, rope, idx: int):
-    """(cos, sin, rows, dim, style) of tables [rows, dim/2], or none."""
-    if rope not in _ROPES:
-        raise ValueError(f"rope must be among {sorted(_ROPES)}")
-    if cos is None and sin is None:
-        return None, None, 0, 0, _ROPES[rope]
-    if cos is None or sin is None or cos.dim() != 2:
-        raise ValueError("cos and sin: both or neither, [rows, rope_dim/2]")
-    shape = cos.shape
-    return (_at(cos, "cos", _F32, shape, idx), _at(sin, "sin", _F32, shape, idx), shape[0],
-            2 * shape[1], _ROPES[rope])
-
-
-def _weight_args(w, name: str, P, heads: int, D: int, idx: int):
-    """(pointer, shard stride, head stride) of weights [D] or one row a head."""
-    if w is None:
-        return None, 0, 0
-    if w.dim() == 1:
-        return _at(w, name, _F32, (D,), idx), 0, 0
-    shape = (heads, D) if P is None else (P, heads, D)
-    return _at(w, name, _F32, shape, idx), heads * D, D
+def _bound(name: str, index_of, stream, *args):
+    """Calls the C++ binding on torch's current stream of the device, or on `stream`
+    with it current, so that what the call allocates belongs to it."""
+    fn = getattr(_lib.binding(), name)
+    if stream is None:
+        return fn(*args, None)
+    handle, ctx = _launch(_device(index_of), stream)
+    with ctx:
+        return fn(*args, handle)
 
 
 def btq_head_norm_rope(x: torch.Tensor, q_heads: int, norm: str = "rms",
@@ -644,34 +606,13 @@ def btq_head_norm_rope(x: torch.Tensor, q_heads: int, norm: str = "rms",
     x [T,heads,D] or [P,T,heads,D], float32 or bf16, any strides but the last:
     the first q_heads are query heads, the others key heads (a slice of a fused
     projection's rows, say). norm "rms", "layer" or "none"; weights float32 [D], or
-    a row for each head, [heads,D] or [P,heads,D]. cos and sin float32 [rows, rope_dim/2] with
-    positions int32 [T], or neither. rope pairs feature i with i + rope_dim/2
-    ("half") or 2i with 2i+1 ("pairs"). out (by default x's type, contiguous) may
-    be x itself.
+    a row for each head, [heads,D] or [P,heads,D]. cos and sin float32
+    [rows, rope_dim/2] with positions int32 [T], or neither. rope pairs feature i
+    with i + rope_dim/2 ("half") or 2i with 2i+1 ("pairs"). out (by default x's
+    type, contiguous) may be x itself.
     """
-    idx = _index(x)
-    P, T, heads, D, xs, xp, xh = _head_rows(x, "x", _VALUES)
-    if norm not in _NORMS:
-        raise ValueError(f"norm must be among {sorted(_NORMS)}")
-    if not 0 <= q_heads <= heads:
-        raise ValueError(f"q_heads: {q_heads} of {heads} heads")
-    qw, qws, qwh = _weight_args(q_weight, "q_weight", P, q_heads, D, idx)
-    kw, kws, kwh = _weight_args(k_weight, "k_weight", P, heads - q_heads, D, idx)
-    cp, sp, rows, dim, style = _rope_args(cos, sin, rope, idx)
-    pp = None
-    if cp is not None:
-        if positions is None:
-            raise ValueError("positions: needed with cos and sin")
-        pp = _at(positions, "positions", _I32, (T,), idx)
-    sh, ctx = _stream_of(idx, stream)
-    if out is None:
-        out = _empty(x.shape, out_dtype or x.dtype, idx, ctx)
-    ys, yp, yh = _like_rows(out, "out", _VALUES, x.shape, idx)
-    _run(_lib.load().btq_head_norm_rope, idx, x.data_ptr(), _T[x.dtype], xs, xp, xh,
-         1 if P is None else P, T, q_heads, heads - q_heads, D, _NORMS[norm], qw, qws, qwh, kw,
-         kws, kwh, eps, pp, cp, sp, rows, dim, style, out.data_ptr(), _T[out.dtype], ys, yp, yh,
-         sh)
-    return out
+    return _bound("head_norm_rope", x, stream, x, q_heads, norm, q_weight, k_weight, eps, positions,
+                  cos, sin, rope, out, out_dtype)
 
 
 def btq_kv_block_bytes(D: int) -> int:
@@ -680,28 +621,6 @@ def btq_kv_block_bytes(D: int) -> int:
     if n == 0:
         raise ValueError(f"invalid D={D}")
     return n
-
-
-def _batch(seq_starts, lengths, page_table, cache, P, idx: int):
-    """(starts, lengths, B, table, max_pages, cache, pages, page size, Hk, D)."""
-    shape = cache.shape
-    if len(shape) != (4 if P is None else 5):
-        raise ValueError(f"cache: shape {tuple(shape)}, expected "
-                         f"[{'' if P is None else 'P,'}pages,Hk,page_size/32,block bytes]")
-    if P is not None and shape[0] != P:
-        raise ValueError(f"cache: {shape[0]} shards, the heads have {P}")
-    pages, Hk, blocks, size = shape[-4:]
-    B = lengths.shape[0] if lengths.dim() == 1 else -1
-    max_pages = page_table.shape[1] if page_table.dim() == 2 else -1
-    return (_at(seq_starts, "seq_starts", _I32, (B + 1,), idx),
-            _at(lengths, "lengths", _I32, (B,), idx), B,
-            _at(page_table, "page_table", _I32, (B, max_pages), idx), max_pages,
-            _at(cache, "cache", _U8, shape, idx), pages, 32 * blocks, Hk, (size - 256) // 32)
-
-
-def _check_heads(name, Hk, D, cache_heads, cache_D):
-    if Hk != cache_heads or D != cache_D:
-        raise ValueError(f"{name}: {Hk} heads of {D}, the cache has {cache_heads} of {cache_D}")
 
 
 def btq_kv_append(k: torch.Tensor, v: torch.Tensor, seq_starts: torch.Tensor,
@@ -717,16 +636,7 @@ def btq_kv_append(k: torch.Tensor, v: torch.Tensor, seq_starts: torch.Tensor,
     btq_kv_block_bytes(D)], without P where k has none. cos and sin as in
     btq_head_norm_rope.
     """
-    idx = _index(k)
-    P, T, Hk, D, ks, kp, kh = _head_rows(k, "k", _VALUES)
-    vs, vp, vh = _like_rows(v, "v", (k.dtype,), k.shape, idx)
-    st, ln, B, tb, mp, cp, pages, size, ch, cd = _batch(seq_starts, lengths, page_table, cache, P,
-                                                        idx)
-    _check_heads("k", Hk, D, ch, cd)
-    sh, _ = _stream_of(idx, stream)
-    _run(_lib.load().btq_kv_append, idx, k.data_ptr(), v.data_ptr(), _T[k.dtype], ks, kp, kh, vs,
-         vp, vh, 1 if P is None else P, T, Hk, D, st, ln, B, tb, mp,
-         *_rope_args(cos, sin, rope, idx), cp, pages, size, sh)
+    _bound("kv_append", k, stream, k, v, seq_starts, lengths, page_table, cache, cos, sin, rope)
 
 
 def btq_kv_gather(seq_starts: torch.Tensor, lengths: torch.Tensor, page_table: torch.Tensor,
@@ -736,32 +646,8 @@ def btq_kv_gather(seq_starts: torch.Tensor, lengths: torch.Tensor, page_table: t
     """(k, v): what the cache holds for the batch's rows, as btq_kv_append's arguments
     name them. Without k and v both are made, [P,tokens,Hk,D] of `dtype` (zeros in
     rows of no sequence); with one of them only that one is filled."""
-    idx = _index(cache)
-    sharded = cache.dim() == 5
-    P = cache.shape[0] if sharded else None
-    st, ln, B, tb, mp, cp, pages, size, Hk, D = _batch(seq_starts, lengths, page_table, cache, P,
-                                                       idx)
-    sh, ctx = _stream_of(idx, stream)
-    if k is None and v is None:
-        if tokens is None:
-            raise ValueError("tokens: needed without k and v")
-        shape = (P, tokens, Hk, D) if sharded else (tokens, Hk, D)
-        with ctx or contextlib.nullcontext():
-            k = torch.zeros(shape, dtype=dtype, device=idx)
-            v = torch.zeros(shape, dtype=dtype, device=idx)
-    x = k if k is not None else v
-    T = x.shape[-3] if x.dim() >= 3 else -1
-    shape = (P, T, Hk, D) if sharded else (T, Hk, D)
-    ks = vs = (0, 0, 0)
-    if k is not None:
-        ks = _like_rows(k, "k", _VALUES, shape, idx)
-    if v is not None:
-        vs = _like_rows(v, "v", (x.dtype,) if k is not None else _VALUES, shape, idx)
-    _run(_lib.load().btq_kv_gather, idx, st, ln, B, tb, mp, cp, pages, size,
-         1 if P is None else P, T, Hk, D,
-         None if k is None else k.data_ptr(), None if v is None else v.data_ptr(), _T[x.dtype],
-         *ks, *vs, sh)
-    return k, v
+    return _bound("kv_gather", cache, stream, seq_starts, lengths, page_table, cache, tokens, k, v,
+                  dtype)
 
 
 def btq_kv_attention_workspace_bytes(P: int, T: int, Hq: int, Hk: int, D: int, B: int,
@@ -786,35 +672,8 @@ def btq_kv_attention(q: torch.Tensor, seq_starts: torch.Tensor, lengths: torch.T
     (q's form of it) or float32, contiguous (zeros in rows of no sequence where
     it is made here); lse float32 [P,T,Hq] is filled if given.
     """
-    idx = _index(q)
-    P, T, Hq, D, qs, qp, qh = _head_rows(q, "q", _BF16_ONLY)
-    st, ln, B, tb, mp, cp, pages, size, Hk, cd = _batch(seq_starts, lengths, page_table, cache, P,
-                                                        idx)
-    if D != cd or Hk < 1 or Hq % Hk:
-        raise ValueError(f"q: {Hq} heads of {D}, the cache has {Hk} of {cd}")
-    shape = (T, Hq * D) if P is None else (P, T, Hq * D)
-    sh, ctx = _stream_of(idx, stream)
-    if out is None:
-        with ctx or contextlib.nullcontext():
-            out = torch.zeros(shape, dtype=out_dtype or q.dtype, device=idx)
-    op = _at(out, "out", _VALUES, shape, idx)
-    lp = None if lse is None else _at(lse, "lse", _F32, shape[:-1] + (Hq,), idx)
-    P = 1 if P is None else P
-    lib = _lib.load()
-    need = lib.btq_kv_attention_workspace_bytes(P, T, Hq, Hk, D, B, mp, size, max_length)
-    if workspace is None:
-        wp, wb = None, 0
-        if need:
-            workspace = _empty(need, torch.uint8, idx, ctx)
-            wp, wb = workspace.data_ptr(), need
-    else:
-        if workspace.get_device() != idx or not workspace.is_contiguous():
-            raise ValueError(f"workspace: must be contiguous and on {q.device}")
-        wp, wb = workspace.data_ptr(), workspace.nbytes
-    _run(lib.btq_kv_attention, idx, q.data_ptr(), qs, qp, qh, P, T, Hq, Hk, D, st, ln, B, tb, mp,
-         cp, pages, size, D ** -0.5 if scale is None else scale, causal, window, max_length, op,
-         _T[out.dtype], lp, wp, wb, sh)
-    return out
+    return _bound("kv_attention", q, stream, q, seq_starts, lengths, page_table, cache, scale, causal,
+                  window, max_length, out, out_dtype, lse, workspace)
 
 
 def btq_status_str(status: int) -> str:

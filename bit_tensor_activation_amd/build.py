@@ -25,6 +25,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbtq.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = "gfx950"
 
 COMMON_FLAGS = [
@@ -59,7 +60,8 @@ def _run(cmd, verbose):
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into bit_tensor_activation_amd/libbtq.so.
+    """Compile every HIP source into bit_tensor_activation_amd/libbtq.so, and the
+    binding next to it.
 
     Each source compiles to an object of its own, in parallel (every kernel
     is launched from its own translation unit, so no device linking is
@@ -74,7 +76,28 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile the C++ part of the Python binding (host code) against this torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cxx = os.environ.get("CXX") or shutil.which("g++") or hipcc()
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    include = [f"-I{d}" for d in (INCLUDE, sysconfig.get_paths()["include"],
+                                  *cpp_extension.include_paths()) if os.path.isdir(d)]
+    tmp = BINDING + ".tmp"
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-DUSE_ROCM=1", "-D__HIP_PLATFORM_AMD__=1",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *include,
+          os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{PKG}", "-l:libbtq.so", f"-L{lib}",
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"],
+         verbose)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def device_asm(out_dir: str) -> list:
