@@ -604,6 +604,10 @@ struct KeysWave {
 // (All column tiles count the same; a mask hides what a causal one does not see.)
 struct SeqTiles {
   int first, tiles, groups;   // first tile, tiles, column groups of 2^shift
+  // A group's length in the flat order: its tiles, and what it costs a block to begin
+  // with another group and to join its sums.
+  int begin;
+  __device__ __forceinline__ int length() const { return tiles + begin; }
 };
 __device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, const SeqRange& s, int shift) {
   SeqTiles r;
@@ -613,6 +617,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const AttnArgs& a, const SeqRange&
   const int lo = a.window ? min(max(s.first() + 1 - a.window, 0), max(hi - 1, 0)) : 0;
   r.first = lo / kTile;
   r.tiles = max((hi + kTile - 1) / kTile - r.first, 1);
+  r.begin = a.begin;
   return r;
 }
 
@@ -632,7 +637,7 @@ __device__ __forceinline__ int64_t flat_total(const AttnArgs& a, int shift, int6
   int64_t sum = 0;
   for (int b = *b0; b < *b1; ++b) {
     const SeqTiles t = seq_tiles(a, seq_range(a.kv, b), shift);
-    sum += (int64_t)t.groups * t.tiles;
+    sum += (int64_t)t.groups * t.length();
   }
   int64_t inc = sum;   // inclusive sum over the wave
   for (int d = 1; d < 64; d *= 2) {
@@ -654,7 +659,7 @@ __device__ __forceinline__ void flat_find(const AttnArgs& a, int shift, int64_t 
                                           int b1, Flat* out) {
   for (int b = b0; b < b1; ++b) {
     const SeqTiles t = seq_tiles(a, seq_range(a.kv, b), shift);
-    const int64_t n = (int64_t)t.groups * t.tiles;
+    const int64_t n = (int64_t)t.groups * t.length();
     if (at >= mine && at < mine + n) {
       out->b = b;
       out->begin = mine;
@@ -662,16 +667,16 @@ __device__ __forceinline__ void flat_find(const AttnArgs& a, int shift, int64_t 
     mine += n;
   }
 }
-constexpr int64_t kStreamBlocks = 512;   // two a CU
+constexpr int64_t kStreamBlocks = 256;   // one a CU
 // a/b, in 32 bits where they fit (a 64-bit division takes some 150 instructions).
 __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   if ((uint64_t)(a | b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
   return a / b;
 }
-// Tiles of a block: an equal share of all, and a step for each wave at least.
-__device__ __forceinline__ int64_t flat_share(int64_t all, int team) {
+// The flat order is cut into equal shares, of 4 tiles and a beginning at least.
+__device__ __forceinline__ int64_t flat_share(int64_t all, int begin) {
   const int64_t n = (all + kStreamBlocks - 1) / kStreamBlocks;
-  return n < team ? team : n;
+  return n < begin + 4 ? begin + 4 : n;
 }
 
 // The sums of the team's first `waves` waves (the others had no tile), each relative
@@ -776,7 +781,7 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
     int b0, b1;
     const int64_t per_head =
         uniform(flat_total<64 * kTeam>(a, S::kShift, scan, &mine, &b0, &b1));
-    const int64_t all = per_head * a.kv.P * a.kv.Hk, each = flat_share(all, kTeam);
+    const int64_t all = per_head * a.kv.P * a.kv.Hk, each = flat_share(all, a.begin);
     const int64_t x0 = blockIdx.x * each, x1 = min(x0 + each, all);
     Cut* cut = cuts<D, S::C>(a) + blockIdx.x;
     if (x0 >= x1) {
@@ -788,18 +793,21 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
     __syncthreads();
     w.b = __builtin_amdgcn_readfirstlane(found.b);
     int64_t begin = hk * per_head + uniform(found.begin);   // of sequence w.b of head hk
+    int parts = 0, cut_group = 0;
     for (int64_t x = x0; x < x1;) {
       const SeqRange seq = uniform(seq_range(a.kv, w.b));
       const SeqTiles st = seq_tiles(a, seq, S::kShift);
-      const int64_t n = (int64_t)st.groups * st.tiles;
+      const int64_t n = (int64_t)st.groups * st.length();
       if (x >= begin + n) {   // on to the next sequence, or the next head's first
         begin += n;
         if (++w.b == a.kv.B) w.b = 0, ++hk;
         continue;
       }
-      const int group = (int)divide(x - begin, st.tiles);
-      const int64_t unit = begin + (int64_t)group * st.tiles;
-      const int t0 = (int)(x - unit), t1 = (int)(min(x1, unit + st.tiles) - unit);
+      const int group = (int)divide(x - begin, st.length());
+      const int64_t unit = begin + (int64_t)group * st.length(), tiles = unit + st.begin;
+      const int t0 = (int)(max(x, tiles) - tiles), t1 = (int)(min(x1, unit + st.length()) - tiles);
+      x = unit + st.length();
+      if (t1 <= t0) continue;   // a share that ends in a beginning leaves it to the next
       const int cols = seq.n * a.G, col0 = group << S::kShift;
       w.shard = hk / a.kv.Hk;
       w.head = hk % a.kv.Hk;
@@ -807,19 +815,20 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
       join_team<D, NT, kTeam, kStream>(
           a, w.c, seq, w.shard, w.head, col0, cols, min(t1 - t0, kTeam), t1 - t0 == st.tiles,
           partial(a, 2 * (int64_t)blockIdx.x + (t0 == 0), 2 * kStreamBlocks, S::C, D));
-      x += t1 - t0;
-      if (x >= x1 && threadIdx.x == 0) {
-        const int64_t last = divide(unit + st.tiles - 1, each) - blockIdx.x;   // blocks after this one
-        *cut = {t0 == 0 && last > 0 ? (int32_t)last + 1 : 0, w.b, hk, group};
+      if (x > x1 && t0 == 0) {
+        parts = (int)(divide(x - 1, each) - blockIdx.x) + 1;
+        cut_group = group;
       }
     }
+    // (the last group that this block began, if it goes on)
+    if (threadIdx.x == 0) *cut = {parts, w.b, hk, cut_group};
   }
 }
 
 // Adds the partial results of a cut group: blockIdx.x is the block that it begins
 // in, blockIdx.y a part of its columns. Threads by (team, column, 4 features), the
 // blocks of a cut shared out over teams.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 template <int D, int NT>
 __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a) {
   constexpr int C = 16 * NT, kVec = D / 4;
@@ -1269,7 +1278,9 @@ hipError_t launch_keys(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
 }
 template <int D, int NT>
 hipError_t launch_stream(const AttnArgs& a, hipStream_t s) {
-  attention_keys_kernel<D, NT, 4, true><<<dim3(kStreamBlocks), 256, 0, s>>>(a, 0);
+  // 8 waves a block as far as their registers go: fewer, longer shares leave less to join
+  constexpr int kTeam = D <= 128 ? 8 : 4;
+  attention_keys_kernel<D, NT, kTeam, true><<<dim3(kStreamBlocks), 64 * kTeam, 0, s>>>(a, 0);
   attention_join_kernel<D, NT><<<dim3(kStreamBlocks, 4), kJoinThreads, 0, s>>>(a);
   return hipGetLastError();
 }
@@ -1316,6 +1327,9 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
       p.kind = units <= 256 && D <= 128 ? kAttnKeys8 : kAttnKeys4;
     } else {
       p.kind = kAttnStream;
+      // some 5 us, or 12 tiles of 8 waves; with fewer groups than that a block has one
+      // beginning or two, all alike
+      p.begin = units <= kStreamBlocks / 2 ? 0 : 12;
       p.workspace = (size_t)(2 * kStreamBlocks * 16) * (D + 2) * 4 + kStreamBlocks * sizeof(Cut);
     }
     return p;

@@ -345,13 +345,14 @@ struct AttnArgs {
   int out_type;
   float* lse;               // [P,T,Hq] or null
   float* ws;
-  int splits;
+  int splits, begin;        // of the plan
 };
 // How a call of these sizes runs (attention.hip).
 enum AttnKind { kAttnKeys4, kAttnKeys8, kAttnStream, kAttnColumns };
 struct AttnPlan {
   AttnKind kind;
-  int splits;               // kAttnColumns: of the keys; kAttnStream: blocks
+  int splits;               // kAttnColumns: of the keys
+  int begin;                // kAttnStream: what a group of columns costs to begin, in tiles
   int64_t items;            // groups of columns of one head that are set aside
   size_t workspace;
 };
