@@ -580,7 +580,7 @@ def btq_block_norm(y: Optional[torch.Tensor], residual: torch.Tensor, post: str 
 
 
 # The calls of the attention group check and pass their tensors in C++
-# (csrc/binding.cpp): with some 30 arguments each, Python takes longer for that than
+# (binding/binding.cpp): with some 30 arguments each, Python takes longer for that than
 # the shortest of them run.
 
 def _bound(name: str, index_of, stream, *args):

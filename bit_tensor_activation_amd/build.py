@@ -93,7 +93,7 @@ def build_binding(verbose: bool = False) -> str:
     tmp = BINDING + ".tmp"
     _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-DUSE_ROCM=1", "-D__HIP_PLATFORM_AMD__=1",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *include,
-          os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{PKG}", "-l:libbtq.so", f"-L{lib}",
+          os.path.join(PKG, "binding", "binding.cpp"), "-o", tmp, f"-L{PKG}", "-l:libbtq.so", f"-L{lib}",
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"],
          verbose)
     os.replace(tmp, BINDING)

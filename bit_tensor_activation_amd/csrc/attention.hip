@@ -22,7 +22,7 @@
 // LDS) and a block's waves share out the keys. attention_columns_kernel, for many,
 // is bound by instructions: a block's waves take columns of their own and share
 // the conversion of the codes through LDS.
-#include "kv.hpp"
+#include "common.hpp"
 
 namespace btq {
 namespace {
@@ -920,9 +920,14 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
 // 64 lanes of 16 consecutive bytes. Keys go as the exact fp16 code - z (a nibble or-ed
 // into the mantissa of 1024, less 1024 + z), values as bf16 128 + code. Two tiles of
 // LDS: while one is used the next is converted, and the one after is on its way from
-// memory. A score then takes one multiply-add from the product to the exponent, which
+// memory. A score takes one multiply-add from the product to the exponent, which
 // is relative to the maximum of the tiles before.
+// A matrix instruction that waits for its unit holds up the vector instructions of
+// the SIMD's other waves (measured: a wave of the one kind and a wave of the other
+// take as long as both one after the other), so the two overlap only where one wave
+// alternates them; 2 multiply-adds behind each cost next to nothing.
 constexpr int kColsTile = 64;
+constexpr int kRing = 4;
 
 template <int D, int NT>
 struct ColsShape {
@@ -1033,25 +1038,22 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
     for (int i = 0; i < S::VN; ++i)
       vreg[i] = *(const v4u*)(from + (uint32_t)(16 * D + min(vrow + 128 * i, D - 1) * 16));
   };
-  auto write = [&](typename S::Buffer& o) {
-    const v2h zero = __builtin_bit_cast(v2h, (kword & 0xfu) * 0x10001u | magic16);   // 1024 + z, twice
-#pragma unroll
-    for (int w = 0; w < NS; ++w) {
-      const v4u x = codes_to_bf16(kreg[w], magic16);   // 1024 + code, in the same order
+  // Piece i of a tile's conversion: a dword of 8 codes of a key, or of a feature's values.
+  constexpr int kPieces = NS + 4 * S::VN;
+  auto write_piece = [&](typename S::Buffer& o, int i) {
+    if (i < NS) {
+      const v2h zero = __builtin_bit_cast(v2h, (kword & 0xfu) * 0x10001u | magic16);   // 1024 + z, twice
+      const v4u x = codes_to_bf16(kreg[i], magic16);   // 1024 + code, in the same order
       v4u y;
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, (uint32_t)x[j]) - zero);
-      o.k[kfrag * NS + w][kslot] = y;
+      o.k[kfrag * NS + i][kslot] = y;
+    } else {
+      const int r = (i - NS) >> 2, q = (i - NS) & 3, d = vrow + 128 * r;
+      if (D % 128 == 0 || d < D) o.v[block * ND + (d >> 4)][q * 16 + (d & 15)] = codes_to_bf16(vreg[r][q], magic);
     }
-#pragma unroll
-    for (int i = 0; i < S::VN; ++i) {
-      const int d = vrow + 128 * i;
-      if (D % 128 == 0 || d < D) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          o.v[block * ND + (d >> 4)][q * 16 + (d & 15)] = codes_to_bf16(vreg[i][q], magic);
-      }
-    }
+  };
+  auto write_words = [&](typename S::Buffer& o) {
     if (quarter == 0) {
       o.ks[block * 32 + krow] = __uint_as_float(kword & 0xffff0000u) * unit;
     } else if (quarter == 2) {
@@ -1062,7 +1064,7 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
       if (krow == 0) o.there[block] = there;
     }
   };
-  auto compute = [&](const typename S::Buffer& in, int key0, int mask) {
+  auto compute = [&](const typename S::Buffer& in, typename S::Buffer& next, int key0, int mask) {
     float t[NT][16], off[NT];
     auto hide = [&](float with) {
 #pragma unroll
@@ -1076,26 +1078,48 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
     };
 #pragma unroll
     for (int n = 0; n < NT; ++n) off[n] = c.m2[n] == kNegInf ? 0.0f : c.m2[n];
+    // Fragment f of the keys, 4*NS of them, then of the values: kAhead of them are on
+    // their way from LDS. Each is a slot of NT matrix instructions with a few others
+    // behind, fenced so that they stay there (see the header of this kernel).
+    v4u ring[kRing];
+    auto read = [&](int f) {
+      if (f < 4 * NS)
+        ring[f % kRing] = in.k[f][lane];
+      else if (f < 8 * NS)
+        ring[f % kRing] = in.v[f - 4 * NS][lane];
+    };
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int f = 0; f < kRing - 1; ++f) read(f);
+    v4f ks[2], acc[2][NT];
+    ks[0] = *(const v4f*)&in.ks[g * 8];
+    // group j*2 + h: keys 8*g + 4*h .. of block j
+    auto scores = [&](int group, int i) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v4f acc[NT];
+      for (int n = 0; n < NT; ++n)
+        t[n][4 * group + i] = __builtin_fmaf(acc[group & 1][n][i], ks[group & 1][i], -off[n]);
+    };
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] = v4f{0, 0, 0, 0};
+    for (int group = 0; group < 4; ++group) {
 #pragma unroll
-        for (int w = 0; w < NS; ++w) {
-          const v8h kc = __builtin_bit_cast(v8h, in.k[(j * 2 + h) * NS + w][lane]);
+      for (int n = 0; n < NT; ++n) acc[group & 1][n] = v4f{0, 0, 0, 0};
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kc, c.q[n][w], acc[n], 0, 0, 0);
-        }
-        const v4f ks = *(const v4f*)&in.ks[j * 32 + g * 8 + h * 4];
+      for (int w = 0; w < NS; ++w) {
+        const int f = group * NS + w;
+        read(f + kRing - 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t[n][8 * j + 4 * h + i] = __builtin_fmaf(acc[n][i], ks[i], -off[n]);
+          acc[group & 1][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              __builtin_bit_cast(v8h, ring[f % kRing]), c.q[n][w], acc[group & 1][n], 0, 0, 0);
+        if (group > 0 && NS >= 4 && w < 4) scores(group - 1, w);
+        issue_fence();
       }
+      if (NS < 4 && group > 0)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scores(group - 1, i);
+      if (group < 3) ks[(group + 1) & 1] = *(const v4f*)&in.ks[((group + 1) >> 1) * 32 + g * 8 + ((group + 1) & 1) * 4];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scores(3, i);
     if (mask & 1) {
       keep_branch();
       hide(kNegInf);
@@ -1127,60 +1151,66 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
         for (int k = 0; k < 16; ++k) t[n][k] -= up;
       }
     }
+    v4f vs[4];
+    v4u z[2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) vs[k] = *(const v4f*)&in.vs[(k >> 1) * 32 + g * 8 + (k & 1) * 4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) z[j] = *(const v4u*)&in.vz[j * 32 + g * 8];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         t[n][k] = __builtin_amdgcn_exp2f(t[n][k]);   // hidden: 0
         c.l[n] += t[n][k];
+        t[n][k] *= vs[k >> 2][k & 3];
       }
-#pragma unroll
-    for (int k = 0; k < 16; k += 4) {
-      const v4f vs = *(const v4f*)&in.vs[(k >> 3) * 32 + g * 8 + (k & 4)];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[n][k + i] *= vs[i];
-    }
     if (mask & 1) {   // the scale of a hidden value may be NaN
       keep_branch();
       hide(0.0f);
     }
+    write_words(next);
+    v8b p[2][NT];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      v8b p[NT];
-      const v8b z = as_bf16(*(const v4u*)&in.vz[j * 32 + g * 8]);
+    for (int n = 0; n < NT; ++n) p[0][n] = weights_to_bf16(&t[n][0]);
+    issue_fence();
+    // the second product, and between its instructions the conversion of the next tile
+    // (behind the last one nobody reads it)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        p[n] = weights_to_bf16(&t[n][8 * j]);
-        c.oz[n] = mfma(z, p[n], c.oz[n]);
-      }
+    for (int f = 0; f < 4 * NS; ++f) {
+      const int j = f / ND, d = f % ND;
+      read(4 * NS + f + kRing - 1);
 #pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const v8b vc = as_bf16(in.v[j * ND + d][lane]);
+      for (int n = 0; n < NT; ++n) c.o[n][d] = mfma(as_bf16(ring[f % kRing]), p[j][n], c.o[n][d]);
+      if (f % 2 == 0 && f / 2 < kPieces) write_piece(next, f / 2);
+      if (f == 1)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) c.o[n][d] = mfma(vc, p[n], c.o[n][d]);
-      }
+        for (int n = 0; n < NT; ++n) p[1][n] = weights_to_bf16(&t[n][8]);
+      if (d == ND - 1)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) c.oz[n] = mfma(as_bf16(z[j]), p[j][n], c.oz[n]);
+      issue_fence();
     }
+#pragma unroll
+    for (int i = 2 * NS; i < kPieces; ++i) write_piece(next, i);
   };
 
   if (kt.begin < kt.end) {
     look_up(kt.begin);
     load(kt.begin);
-    write(buf[0]);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) write_piece(buf[0], i);
+    write_words(buf[0]);
     load(kt.begin + 1);
     lds_barrier();
   }
   for (int tile = kt.begin; tile < kt.end; ++tile) {
     const int even = (tile - kt.begin) & 1;
-    if (tile + 1 < kt.end) {
-      write(buf[even ^ 1]);
-      load(tile + 2);
-    }
     const int key0 = tile * kColsTile;
     const int blocks = uniform(buf[even].there[0] | buf[even].there[1] << 1);
     const bool full = blocks == 3 && key0 >= c.all_lo && key0 + kColsTile <= c.all_hi;
-    compute(buf[even], key0, blocks << 1 | (full ? 0 : 1));
+    compute(buf[even], buf[even ^ 1], key0, blocks << 1 | (full ? 0 : 1));
+    load(tile + 2);
     lds_barrier();
   }
   if (!live) return;

@@ -1,6 +1,6 @@
 // btq_kv_append and btq_kv_gather: rows of new keys and values into the paged
 // 4-bit cache, and what the cache holds back into rows.
-#include "kv.hpp"
+#include "common.hpp"
 
 namespace btq {
 namespace {
