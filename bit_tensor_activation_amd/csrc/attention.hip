@@ -6,11 +6,14 @@
 //   out = sum_key p*s'[key]*(code'[key,:] - z'[key]) / sum_key p.
 // Both products run on the matrix cores on the codes themselves, and z is taken off
 // after: from S as a product with the sum of q, from out as one more row of V^T
-// that holds z', whose product sees the same rounded p*s' as the codes do. A nibble
-// or-ed into the mantissa of bf16 128 is the exact bf16 128 + code, 7 instructions
-// for the 8 codes of a dword; a nibble in a byte of its own is the exact 8-bit float
-// (e4m3) code*2^-9, its subnormal numbers and first binade being evenly spaced: 3
-// instructions. p*s' is rounded to bf16, as a weight of the second product.
+// that holds 128 + z', whose product sees the same rounded p*s' as the codes do. A
+// nibble or-ed into the mantissa of bf16 128 is the exact bf16 128 + code, 7
+// instructions for the 8 codes of a dword. (Where many columns share the conversion,
+// keys take 4 more to the exact fp16 code - z.) p*s' is rounded to bf16, as a weight
+// of the second product. Codes as 8-bit floats, which a nibble in a byte of its own
+// is, with queries as sums of two, take 3 instructions, but those products are summed
+// to fewer bits: lse was off by 3.5e-6 of itself, and 1e-7 this way, which costs
+// up to 7% (64 sequences of up to 4095 tokens 40 -> 43 us).
 //
 // S is computed transposed (keys down, columns across), so that the 4 values of a
 // column that a lane holds of two 16-key tiles are the 8 consecutive keys of the
@@ -30,10 +33,7 @@ namespace {
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
-typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef uint16_t v2s __attribute__((ext_vector_type(2)));
-typedef short v2i __attribute__((ext_vector_type(2)));
-typedef int v8i __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
@@ -117,19 +117,14 @@ __device__ __forceinline__ void static_for(F f) {
 // ---- what a wave keeps of its columns: 16*NT of them, column n*16 + lane%16 in
 // the 4 lanes of that number ----
 //
-// Queries are operand B of the first product. For keys as 8-bit floats they
-// are the sum of two of those: taken by a power of 2 to below 256 (a column's largest
-// to 128 or more), the first float holds 4 bits of a value and the second the other 4
-// of bf16, down to 2^-10, so a query is off by 2^-18 of its largest feature at most.
-// For keys as fp16 they are fp16, taken by a power of 2 to a largest of 2^13 or more:
-// exact down to 2^-27 of that.
+// Queries are operand B of the first product: bf16 as they come, or, for keys as
+// fp16, fp16 taken by a power of 2 to a largest of 2^13 or more: exact down to 2^-27
+// of that.
 template <int D, int NT>
 struct Columns {
   static constexpr int NS = D / 32, ND = D / 16;
-  v8h q[NT][NS];
-  long q8[NT][NS][2];
-  float qsum[NT];            // in the units of the first product
-  float unit[NT];            // what it takes to powers of 2 of p
+  v8h q[NT][NS];             // bits of either type
+  float qsum[NT];
   int lo[NT], hi[NT];        // keys that the column sees
   v4f o[NT][ND], oz[NT];     // sums of p*s'*(128 + code) of 4 features, and of p*s'*(128 + z')
   float m2[NT], l[NT];       // running maximum times scale*log2(e); sum of p of this lane's keys
@@ -186,20 +181,22 @@ struct Columns {
     }
   }
   // (a column that does not exist repeats the first one; its results go nowhere)
-  __device__ __forceinline__ void take_bytes(float scale2, const v4u (&w)[NT][NS]) {
-    v2b ones;
-    ones[0] = ones[1] = (__bf16)1.0f;
+  __device__ __forceinline__ void take(const v4u (&w)[NT][NS]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float sum = 0.0f;
+      v2s top = {0, 0};   // largest |q| of the even and of the odd features, as bits
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
+      for (int i = 0; i < NS; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2b, (uint32_t)w[n][i][j]), ones, sum, false);
-      qsum[n] = column_sum(sum);
-      unit[n] = scale2;
-      to_bytes(n, w[n]);
+        for (int j = 0; j < 4; ++j) {
+          sum += __uint_as_float(w[n][i][j] << 16) + __uint_as_float(w[n][i][j] & 0xffff0000u);
+          top = __builtin_elementwise_max(top, __builtin_bit_cast(v2s, (uint32_t)w[n][i][j] & 0x7fff7fffu));
+        }
+        q[n][i] = __builtin_bit_cast(v8h, deal(w[n][i]));
+      }
+      // NaN and Inf in a query make all its scores NaN
+      qsum[n] = column_sum(max(top[0], top[1]) < 0x7f80 ? sum : __uint_as_float(0x7fc00000u));
     }
   }
   // The largest finite |q| of the lane's features, as fp32 bits.
@@ -239,50 +236,11 @@ struct Columns {
         q[n][i] = __builtin_bit_cast(v8h, y);
       }
   }
-  __device__ __forceinline__ void to_bytes(int n, const v4u (&w)[NS]) {
-    v2s top2 = {0, 0};   // largest |q| of the even and of the odd features, as bits
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(v2s, (uint32_t)w[i][j] & 0x7fff7fffu));
-    const float top = column_max(__uint_as_float((uint32_t)max(top2[0], top2[1]) << 16));
-    const uint32_t bits = __float_as_uint(top);
-    // 2^(exponent of top - 7), within the powers that have a reciprocal
-    const float down = __uint_as_float((uint32_t)(clamp_int((int)(bits >> 23), 20, 254) - 7) << 23);
-    unit[n] *= down * 512.0f;
-    // NaN and Inf in a query (NaN is above Inf as bits) make all its scores NaN
-    qsum[n] = bits < 0x7f800000u ? qsum[n] / down * 0x1p-9f : __uint_as_float(0x7fc00000u);
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      uint32_t r[2][2];   // [first, second float][even, odd features]
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // features h, 2 + h, 4 + h and 6 + h
-        const uint32_t x01 = __builtin_amdgcn_perm(w[i][1], w[i][0], h ? 0x07060302u : 0x05040100u);
-        const uint32_t x23 = __builtin_amdgcn_perm(w[i][3], w[i][2], h ? 0x07060302u : 0x05040100u);
-        v2i first = {0, 0}, second = {0, 0};
-        first = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(first, __builtin_bit_cast(v2b, x01), down, false);
-        first = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(first, __builtin_bit_cast(v2b, x23), down, true);
-        r[0][h] = __builtin_bit_cast(uint32_t, first);
-        const auto a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(r[0][h], down, false);
-        const auto a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(r[0][h], down, true);
-        second = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(
-            second, __uint_as_float(x01 << 16) - a0[0], __uint_as_float(x01 & 0xffff0000u) - a0[1], down, false);
-        second = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(
-            second, __uint_as_float(x23 << 16) - a1[0], __uint_as_float(x23 & 0xffff0000u) - a1[1], down, true);
-        r[1][h] = __builtin_bit_cast(uint32_t, second);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) q8[n][i][k] = (long)((uint64_t)r[k][1] << 32 | r[k][0]);
-    }
-  }
-
   // Scores t (value k is a key of the lane's) to weights p; l and the sums follow
   // the running maximum. It is raised only when a new one is 8 powers of 2 above
   // it: p stays below 2^8, and the sums are rarely rescaled.
   template <int kValues>
-  __device__ __forceinline__ void weights(float (&t)[NT][kValues]) {
+  __device__ __forceinline__ void weights(float scale2, float (&t)[NT][kValues]) {
     float top[NT];
     bool raise = false;
 #pragma unroll
@@ -290,7 +248,7 @@ struct Columns {
       float m = t[n][0];
 #pragma unroll
       for (int k = 1; k < kValues; ++k) m = fmaxf(m, t[n][k]);
-      top[n] = column_max(m) * unit[n];
+      top[n] = column_max(m) * scale2;
       raise |= top[n] > m2[n] + 8.0f || (m2[n] == kNegInf && top[n] > kNegInf);
     }
     if (__ballot(raise)) {
@@ -311,7 +269,7 @@ struct Columns {
       const float off = m2[n] == kNegInf ? 0.0f : m2[n];
 #pragma unroll
       for (int k = 0; k < kValues; ++k) {
-        t[n][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(t[n][k], unit[n], -off));   // hidden: 0
+        t[n][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(t[n][k], scale2, -off));   // hidden: 0
         l[n] += t[n][k];
       }
     }
@@ -429,7 +387,7 @@ struct KeysWave {
     load_keys(kat);
     load_words(vat, kw, vw);
     load_values(vat);
-    c.take_bytes(a.scale2, raw);
+    c.take(raw);
     // whether columns see different keys
     const int uneven = c.all_lo > c.any_lo || c.all_hi < c.any_hi ? 2 : 0;
     for (int tile = begin; tile < end; tile += step) {
@@ -477,7 +435,7 @@ struct KeysWave {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       ks[h] = __uint_as_float(kw[h] & 0xffff0000u);
-      kz[h] = 128.0f - __uint_as_float(kw[h] << 16);
+      kz[h] = -__uint_as_float(kw[h] << 16);
       vs[h] = __uint_as_float(vw[h] & 0xffff0000u);
     }
     if (mask) {   // places that no column sees may hold anything
@@ -499,48 +457,14 @@ struct KeysWave {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int n = 0; n < NT; ++n) acc[h][n] = v4f{0, 0, 0, 0};
-        if constexpr (NS % 4 == 0) {
-          // 128 features an instruction, at twice the rate of 32
 #pragma unroll
-          for (int w = 0; w < NS; w += 4)
+        for (int w = 0; w < NS; ++w)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+          for (int h = 0; h < 2; ++h) {
+            const v8b kc = as_bf16(codes_to_bf16(k[S0 + s][h][w], magic));
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                v8i kc;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t x = k[S0 + s][h][w + i];
-                  kc[2 * i] = (int)(x & 0x0f0f0f0fu);
-                  kc[2 * i + 1] = (int)(x >> 4 & 0x0f0f0f0fu);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  v8i qc;
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    qc[2 * i] = (int)(uint32_t)c.q8[n][w + i][j];
-                    qc[2 * i + 1] = (int)((uint64_t)c.q8[n][w + i][j] >> 32);
-                  }
-                  // (e4m3 both; block scales of 1)
-                  acc[h][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kc, qc, acc[h][n], 0, 0, 0,
-                                                                             127, 0, 127);
-                }
-              }
-        } else {
-#pragma unroll
-          for (int w = 0; w < NS; ++w)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t x = k[S0 + s][h][w];
-                const long kc = (long)((uint64_t)(x >> 4 & 0x0f0f0f0fu) << 32 | (x & 0x0f0f0f0fu));
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                  acc[h][n] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(kc, c.q8[n][w][j], acc[h][n], 0, 0, 0);
-              }
-        }
+            for (int n = 0; n < NT; ++n) acc[h][n] = mfma(kc, __builtin_bit_cast(v8b, c.q[n][w]), acc[h][n]);
+          }
         static_for<0, 8, 1>([&](auto value) {
           constexpr int h = decltype(value)::value / 4, i = decltype(value)::value % 4, L = 4 * (S0 + s) + i;
 #pragma unroll
@@ -566,7 +490,7 @@ struct KeysWave {
         keep_branch();
         hide(kNegInf);
       }
-      c.weights(t);
+      c.weights(a.scale2, t);
       static_for<0, 8 * KS, 1>([&](auto index) {
         constexpr int key = decltype(index)::value, L = 4 * (S0 + key / 8) + key % 4;
 #pragma unroll

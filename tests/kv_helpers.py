@@ -161,12 +161,8 @@ def attention(batch, cache, q, Hk, D, scale, causal=True, window=0):
 
     The kernel's first product adds D terms q*(128 + c), and the sum of q times 128
     + z goes off it: 143*sum|q| bounds every term and partial sum of both, each
-    off by U a step of the D + 16, and the score is that times scale*s. (Without the
-    128 both are smaller.) A query may enter as the sum of two 8-bit floats: scaled by
-    a power of 2 to a largest feature of 128 or more, a feature's first float leaves
-    at most 4 bits, which the second holds down to its smallest number 2^-9, so each
-    feature that is not 0 is off by 2^-10, that is 2^-17 of the largest, and times
-    |c - z| of at most 15 it moves the score. p is then off by that much of itself (and by 8U for exp2 and its argument, of up to
+    off by U a step of the D + 16, and the score is that times scale*s. (Keys as
+    exact fp16 code - z make both smaller.) p is then off by that much of itself (and by 8U for exp2 and its argument, of up to
     |t|*log2(e)), and p*s' rounded to bf16 by 2^-8. The sum over keys adds at most
     U a step of at most L/128*32 + 64 more. Like the scores, the second product is
     the difference of sums of p*s'*(128 + code) and of p*s'*(128 + z), so those steps
@@ -207,9 +203,7 @@ def attention(batch, cache, q, Hk, D, scale, causal=True, window=0):
                     e = np.exp(t - m)
                     total = e.sum()
                     out[p, row, h] = e @ v[seen] / total
-                    eps = (scale * st[seen].max() * (143 * np.abs(x).sum() * (D + 16) * U
-                                                     + 15 * 2.0 ** -17 * np.abs(x).max()
-                                                     * np.count_nonzero(x))
+                    eps = (scale * st[seen].max() * 143 * np.abs(x).sum() * (D + 16) * U
                            + (8 + 2 * np.abs(t).max()) * U + (len(js) / 4 + 64) * U)
                     tol[p, row, h] = ((2.0 ** -8 + 2 * eps) * (e @ np.abs(v[seen]) / total)
                                       + 2 * 143 * (len(js) / 4 + 64) * U * (e @ vst[seen]) / total)

@@ -14,8 +14,17 @@ codec its calibration once, before the step. The script times the step and
 each call of it, and measures y, the residual and z against the same layer
 computed from the unquantized values in float64.
 
+With --cached C the activations x come from the attention before that layer: B
+sequences, each with C tokens in a paged 4-bit cache, of which T/B new ones go
+through the block. Every shard has K/D query heads and --kv_heads key heads:
+
+    h [T,H] --btq_int8_linear--> queries, keys, values [P,T,heads,D]
+      --btq_head_norm_rope--> norm and rotation, in place
+      --btq_kv_append--> cache       --btq_kv_attention--> x [P,T,K]
+
     python tp_block.py                        # P=8 T=2048 H=4096 K=512 N=2048
     python tp_block.py --T 8 --H 8192 --K 1024 --N 1024
+    python tp_block.py --T 32 --H 8192 --K 1024 --N 1024 --cached 2000 --B 32
 
 It prints one JSON line.
 """
@@ -62,6 +71,84 @@ def prepare(P: int, T: int, H: int, K: int, N: int, k: int, seed: int = 1,
     s["x"] = rnd(P, T, K).to(torch.bfloat16)
     s["residual"] = rnd(T, H).to(torch.bfloat16)
     return s
+
+
+def prepare_attention(s: dict, B_: int, cached: int, kv_heads: int, D: int = 128,
+                      page: int = 64, seed: int = 2) -> None:
+    """Adds to s what the attention before the block needs: B_ sequences whose pages
+    hold `cached` random tokens each, and the projection of their new ones."""
+    P, T, H, K = s["P"], s["T"], s["H"], s["K"]
+    if K % D or T % B_:
+        raise ValueError("K must be a multiple of D, and T of the sequences")
+    dev = s["residual"].device
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+
+    def rnd(*shape):
+        return torch.randn(shape, generator=g, device=dev)
+    n, heads = T // B_, K // D
+    s["heads"], s["kv_heads"], s["D"], s["length"] = heads, kv_heads, D, cached + n
+    s["w0_exact"] = rnd(P, (heads + 2 * kv_heads) * D, H) * H ** -0.5
+    s["w0"], s["w0_scale"] = B.btq_quantize_rows(s["w0_exact"])
+    s["h"] = rnd(T, H).to(torch.bfloat16)
+    s["q_weight"], s["k_weight"] = 1 + 0.1 * rnd(D), 1 + 0.1 * rnd(D)
+    freq = 10000.0 ** (-torch.arange(0, D, 2, device=dev, dtype=torch.float64) / D)
+    angle = torch.arange(s["length"], device=dev, dtype=torch.float64)[:, None] * freq
+    s["cos"], s["sin"] = torch.cos(angle).float(), torch.sin(angle).float()
+
+    pages = -(-s["length"] // page)
+    s["table"] = torch.randperm(B_ * pages, generator=g, device=dev).int().view(B_, pages)
+    s["cache"] = torch.zeros((P, B_ * pages, kv_heads, page // 32, B.btq_kv_block_bytes(D)),
+                             dtype=torch.uint8, device=dev)
+    s["starts"] = torch.arange(0, T + 1, n, device=dev, dtype=torch.int32)
+    s["lengths"] = torch.full((B_,), s["length"], dtype=torch.int32, device=dev)
+    s["positions"] = (torch.arange(T, device=dev) % n + cached).int()
+    if cached:
+        old = torch.arange(0, B_ * cached + 1, cached, device=dev, dtype=torch.int32)
+        kv = rnd(2, P, B_ * cached, kv_heads, D).to(torch.bfloat16)
+        B.btq_kv_append(kv[0], kv[1], old, torch.full_like(s["lengths"], cached), s["table"],
+                        s["cache"])
+
+
+def attend(s):
+    """x [P,T,K] of the new tokens, which are in the cache after it."""
+    P, T, D, Hq, Hk = s["P"], s["T"], s["D"], s["heads"], s["kv_heads"]
+    qkv = B.btq_int8_linear(s["h"], s["w0"], s["w0_scale"]).view(P, T, Hq + 2 * Hk, D)
+    qk = qkv[:, :, :Hq + Hk]
+    B.btq_head_norm_rope(qk, Hq, q_weight=s["q_weight"], k_weight=s["k_weight"], eps=EPS,
+                         positions=s["positions"], cos=s["cos"], sin=s["sin"], out=qk)
+    B.btq_kv_append(qk[:, :, Hq:], qkv[:, :, Hq + Hk:], s["starts"], s["lengths"], s["table"],
+                    s["cache"])
+    return B.btq_kv_attention(qk[:, :, :Hq], s["starts"], s["lengths"], s["table"], s["cache"],
+                              max_length=s["length"])
+
+
+def exact_attention(s):
+    """x in float64 from the unquantized projection; the keys and values are those
+    that the cache holds."""
+    P, T, D, Hq, Hk = s["P"], s["T"], s["D"], s["heads"], s["kv_heads"]
+    n, L = T // len(s["lengths"]), s["length"]
+    every = torch.arange(0, len(s["lengths"]) * L + 1, L, device=s["h"].device, dtype=torch.int32)
+    k, v = B.btq_kv_gather(every, s["lengths"], s["table"], s["cache"], tokens=int(every[-1]),
+                           dtype=torch.float32)
+    out = []
+    for p in range(P):
+        q = s["h"].double() @ s["w0_exact"][p, :Hq * D].double().t().contiguous()
+        q = q.view(T, Hq, D)
+        q = q * torch.rsqrt((q * q).mean(-1, keepdim=True) + EPS) * s["q_weight"].double()
+        c, sn = (s[t][s["positions"].long()].double()[:, None] for t in ("cos", "sin"))
+        a, b = q[..., :D // 2], q[..., D // 2:]
+        q = torch.cat((a * c - b * sn, b * c + a * sn), -1)
+        rows = []
+        for i in range(T // n):
+            seen = (torch.arange(L, device=q.device)
+                    <= torch.arange(L - n, L, device=q.device)[:, None])
+            for h in range(Hq):
+                kk, vv = (x[p, i * L:(i + 1) * L, h // (Hq // Hk)].double() for x in (k, v))
+                t = q[i * n:(i + 1) * n, h] @ kk.t().contiguous() * D ** -0.5
+                rows.append(torch.softmax(t.masked_fill(~seen, -float("inf")), -1) @ vv)
+        out.append(torch.stack(rows).view(T // n, Hq, n, D).transpose(1, 2).reshape(T, Hq * D))
+    return torch.stack(out)
 
 
 def linear(s):
@@ -128,7 +215,7 @@ def time_us(fn, steps: int) -> float:
 def main() -> int:
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     for name, value in (("P", 8), ("T", 2048), ("H", 4096), ("K", 512), ("N", 2048), ("k", 64),
-                        ("steps", 50)):
+                        ("steps", 50), ("cached", -1), ("B", 1), ("kv_heads", 1)):
         ap.add_argument(f"--{name}", type=int, default=value)
     a = ap.parse_args()
     if not torch.cuda.is_available():
@@ -143,6 +230,16 @@ def main() -> int:
     calls = {"int8_linear": lambda: linear(s), "compress_pack": lambda: send(s, sums),
              "decompress_reduce": lambda: receive(s, *message), "block_norm": lambda: norm(s, y),
              "int8_matmul": lambda: project(s, q, q_scale)}
+    if a.cached >= 0:
+        prepare_attention(s, a.B, a.cached, a.kv_heads)
+        s["x"] = attend(s).view(torch.bfloat16)
+        print(json.dumps({
+            "config": {**{n: s[n] for n in "PTHKNk"}, "B": a.B, "cached": a.cached,
+                       "heads": s["heads"], "kv_heads": s["kv_heads"]},
+            "attention_us": round(time_us(lambda: attend(s), a.steps), 1),
+            "step_us": round(time_us(lambda: (s.update(x=attend(s)), step(s)), a.steps), 1),
+            "relative_error": {"x": round(relative_error(s["x"].view(torch.bfloat16), exact_attention(s)), 5)}}))
+        return 0
     print(json.dumps({
         "config": {n: s[n] for n in "PTHKNk"},
         "step_us": round(time_us(lambda: step(s), a.steps), 1),
