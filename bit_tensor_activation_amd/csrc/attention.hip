@@ -1223,11 +1223,13 @@ hipError_t each_launch(int64_t items, F f) {
   return hipGetLastError();
 }
 
-template <int D, int NT, int kTeam>
+// 4 waves a block: 8 of them take longer at any one length (256 groups of 2000 keys 30
+// against 24 us, of 250 keys 12.6 against 8.9; 128 of 1000 10.3 against 9.7), and only
+// less where a few of some 256 groups are much longer (500 to 2000 keys 21 against 23).
+template <int D, int NT>
 hipError_t launch_keys(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
   return each_launch(plan.items, [&](uint32_t first, unsigned n) {
-    attention_keys_kernel<D, NT, kTeam, false>
-        <<<dim3(a.kv.Hk, (unsigned)a.kv.P, n), 64 * kTeam, 0, s>>>(a, first);
+    attention_keys_kernel<D, NT, 4, false><<<dim3(a.kv.Hk, (unsigned)a.kv.P, n), 256, 0, s>>>(a, first);
   });
 }
 template <int D, int NT>
@@ -1254,9 +1256,7 @@ hipError_t launch_columns(const AttnArgs& a, const AttnPlan& plan, hipStream_t s
 template <int D>
 hipError_t launch_head(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
   switch (plan.kind) {
-    case kAttnKeys8:
-      if constexpr (D <= 128) return launch_keys<D, 1, 8>(a, plan, s);
-    case kAttnKeys4: return launch_keys<D, 1, 4>(a, plan, s);
+    case kAttnKeys: return launch_keys<D, 1>(a, plan, s);
     case kAttnStream: return launch_stream<D, 1>(a, s);
     default: return launch_columns<D>(a, plan, s);
   }
@@ -1274,11 +1274,13 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
     // groups of columns that exist, as far as the host knows: each row has one at least
     const int64_t rows = T < B ? T : B;
     const int64_t units = (rows > columns / 16 ? rows : columns / 16) * heads;
-    // A block takes a group of columns whole where that leaves none much longer than
-    // an equal share of a full chip: 512 blocks of up to 4096 keys, fewer of fewer.
-    const int64_t longest = units >= 512 ? 4096 : units * 8 > 1024 ? units * 8 : 1024;
+    // A block takes a group of columns whole where that leaves none much longer than an
+    // equal share of a full chip: up to 4096 keys with 512 groups, up to 2048 with 256
+    // or fewer, whose second launch would cost more (128 groups of 2000 keys 15 us whole,
+    // 18 in shares; of 4000 24 in shares).
+    const int64_t longest = units >= 512 ? 4096 : units > 256 ? units * 8 : 2048;
     if (max_length <= longest || units >= 4096) {
-      p.kind = units <= 256 && D <= 128 ? kAttnKeys8 : kAttnKeys4;
+      p.kind = kAttnKeys;
     } else {
       p.kind = kAttnStream;
       // some 5 us, or 12 tiles of 8 waves; with fewer groups than that a block has one

@@ -348,7 +348,7 @@ struct AttnArgs {
   int splits, begin;        // of the plan
 };
 // How a call of these sizes runs (attention.hip).
-enum AttnKind { kAttnKeys4, kAttnKeys8, kAttnStream, kAttnColumns };
+enum AttnKind { kAttnKeys, kAttnStream, kAttnColumns };
 struct AttnPlan {
   AttnKind kind;
   int splits;               // kAttnColumns: of the keys

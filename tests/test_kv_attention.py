@@ -265,7 +265,7 @@ def test_long_cache_offsets_pass_32_bits():
 def test_capture_and_replay():
     # one graph replayed over a growing sequence, whose lengths and pages it reads
     D, page = 128, 64
-    b = Batch([1, 1], [2000, 2000], page=page)
+    b = Batch([1, 1], [2200, 2200], page=page)
     cache = torch.from_numpy(random_cache(b, 2, 1, D)).to(DEV)
     starts, lengths, tb = b.dev()
     q = torch.randn((2, 2, 8, D), device=DEV).to(BF16)
