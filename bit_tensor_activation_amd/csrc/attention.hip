@@ -1269,7 +1269,13 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
   const int G = Hq / Hk;
   const int64_t heads = P * Hk, columns = T * G;
   p.splits = 1;
-  if (columns <= (int64_t)32 * B) {   // 32 columns a sequence on average
+  // Columns of a sequence, on average, up to which the keys' kernels are faster, with
+  // D = 128 and 8 heads, us by keys against by columns: 64 sequences of 3000 keys with 96
+  // columns each 169 against 191, with 128 204 against 241, with 192 299 against 242; one
+  // of 16000 with 128 columns 40 against 144. Over short contexts the groups' beginnings
+  // weigh more: 64 of 300 keys with 64 columns 36 against 40, with 96 52 against 43.
+  const int64_t few = max_length > 512 ? 128 : 64;
+  if (columns <= few * B) {
     p.items = columns / 16 + B;
     // groups of columns that exist, as far as the host knows: each row has one at least
     const int64_t rows = T < B ? T : B;

@@ -22,10 +22,12 @@
  * between devices is the identity: the buffers written by btq_compress_pack
  * are the ones read by btq_decompress_reduce. The other calls widen the path:
  * a bf16-output receiver, other readings of the selection step and a packed
- * row pitch. The last group covers what stands next to the path in a
+ * row pitch. Two more groups cover what stands next to the path in a
  * transformer: the 8-bit linear layer whose partial sums the sender takes
- * (btq_quantize_rows, btq_int8_matmul, btq_int8_linear) and the norms that
- * read the receiver's sum (btq_block_norm).
+ * (btq_quantize_rows, btq_int8_matmul, btq_int8_linear) with the norms that
+ * read the receiver's sum (btq_block_norm), and what lies between two linear
+ * layers of an attention block: btq_head_norm_rope, a paged 4-bit cache
+ * (btq_kv_append, btq_kv_gather) and btq_kv_attention over it.
  *
  * Conventions shared by every call
  *  - Tensor pointers are DEVICE pointers (hipMalloc'd or from PyTorch) to
@@ -604,19 +606,24 @@ int btq_kv_gather(const int32_t *seq_starts, const int32_t *lengths, int64_t B,
  * Scores and sums are fp32; the weight exp(t - max)*(scale of v[j]) is rounded to
  * bf16 for the second product. NaN or Inf in a query gives NaN; a NaN key or value
  * gives NaN to the queries that see it and to no others.
+ * With many queries a sequence, those of up to 128 (query, head) pairs are held as fp16
+ * relative to the largest of them: exact down to 2^-27 of it.
  *   q         bf16 [P,T,Hq,D] in; fastest with heads on 16 bytes
  *   scale     > 0 and finite
  *   max_length  an upper bound of lengths (0: the table's places) by which the
  *             keys are split over the chip. Longer sequences are as correct,
  *             and may be slower.
- *   out       fp32 or bf16 [P,T,Hq*D] out, contiguous: an x of btq_int8_linear
+ *   out       fp32 (8-byte aligned) or bf16 (4-byte aligned) [P,T,Hq*D] out,
+ *             contiguous: an x of btq_int8_linear
  *   lse       fp32 [P,T,Hq] out, or NULL
  *   workspace at least btq_kv_attention_workspace_bytes bytes of the same sizes,
  *             16-byte aligned, with no initial value (NULL if that is 0). Calls at
  *             the same time need one each.
- * One launch, or two where keys are split. The result does not depend on the
- * other sequences of the batch beyond their number, and the same call gives the
- * same bits.
+ * One launch, or two where keys are split. The same call gives the same bits. By
+ * which kernel and in which pieces keys are summed is chosen by the sizes, and where
+ * equal shares of a batch's keys are taken also by all its lengths, so the last bits
+ * of a sequence's result may differ between batches; the contents of other sequences
+ * do not matter.
  */
 int btq_kv_attention(const void *q, int64_t q_shard, int64_t q_pitch, int64_t q_head,
                      int64_t P, int64_t T, int64_t Hq, int64_t Hk, int64_t D,

@@ -332,6 +332,108 @@ def test_python_refusals():
             B.btq_kv_attention(**{**args, **kw})
 
 
+# Many columns a sequence, which share the keys that a block stages: the same questions
+# once more, with keys in one piece (first two) and in several.
+WIDE = [Batch([150], [150]), Batch([70, 1, 0, 200], [300, 90, 5, 200], page=64, before=1, behind=2),
+        Batch([50, 1, 90], [200, 900, 90], page=64, slack=1), Batch([33, 280], [1500, 1200], page=128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", range(len(WIDE)))
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_many_columns(n, D):
+    say(f"case: kv attention many columns {n} D={D}")
+    check(WIDE[n], 1, 8, 1, D, dt=F32)
+    check(WIDE[n], 2, 16, 2, D, causal=n % 2 == 0, window=100, lse=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk", [(5, 1), (17, 1), (40, 2), (12, 4), (64, 1)])
+def test_many_columns_in_head_groups(Hq, Hk):
+    for n in (1, 2):
+        check(WIDE[n], 1, Hq, Hk, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sigma,q_sigma,scale", [(1.0, 20.0, None), (30.0, 4.0, None), (1.0, 1.0, 3.0)])
+def test_many_columns_flat_and_sharp(sigma, q_sigma, scale):
+    for n in (1, 3):
+        check(WIDE[n], 1, 8, 1, 128, sigma=sigma, q_sigma=q_sigma, dt=F32, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift,gap", [(1, 0), (3, 5), (8, 64)])
+def test_many_columns_strides_and_alignment(shift, gap):
+    check(WIDE[1], 2, 8, 2, 64, shift=shift, gap=gap)
+
+
+@pytest.mark.gpu
+def test_many_columns_missing_pages():
+    b = Batch([60, 130], [700, 300], page=32)
+    b.table[0, [0, 3, 4, 5, 6, 11]] = -1
+    b.table[1, 5] = b.pages
+    b.table[1, 2] = -2 ** 31
+    check(b, 1, 8, 1, 128)
+    check(b, 1, 8, 1, 128, window=60)
+    b.table[:] = -1
+    out, lse, _ = check(b, 1, 8, 1, 128)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.gpu
+def test_many_columns_nan():
+    # a key or value that is NaN reaches the rows that see it, a query that is NaN its row
+    D = 64
+    b = Batch([160, 50], [180, 60], page=32)
+    g = np.random.default_rng(3)
+    q = torch.from_numpy(g.standard_normal((1, b.T, 8, D)).astype(np.float32)).to(DEV).to(BF16)
+    clean = random_cache(b, 1, 2, D)
+    starts, lengths, tb = b.dev()
+    a = B.btq_kv_attention(q, starts, lengths, tb, torch.from_numpy(clean).to(DEV))
+    assert torch.isfinite(a).all()
+    for value in (0, 128):
+        dirty = clean.copy()
+        page, block, t = b.where(0, 100)
+        at = 32 * D + value + 4 * t
+        dirty[:, page, :, block, at:at + 4] = np.frombuffer(np.uint32(NAN_WORD).tobytes(), np.uint8)
+        d = B.btq_kv_attention(q, starts, lengths, tb, torch.from_numpy(dirty).to(DEV))
+        sees = torch.zeros(b.T, dtype=torch.bool)
+        sees[80:160] = True                                # row 80 is place 100
+        assert torch.isnan(d[0, sees]).all() and torch.equal(d[0, ~sees], a[0, ~sees])
+    bad = q.clone()
+    bad[0, 20, 3, 7], bad[0, 170, 0, 0] = float("nan"), float("inf")
+    d = B.btq_kv_attention(bad, starts, lengths, tb, torch.from_numpy(clean).to(DEV)).view(1, b.T, 8, D)
+    hit = torch.zeros((b.T, 8), dtype=torch.bool)
+    hit[20, 3] = hit[170, 0] = True
+    assert torch.isnan(d[0, hit]).all() and torch.equal(d[0, ~hit], a.view(1, b.T, 8, D)[0, ~hit])
+
+
+@pytest.mark.gpu
+def test_many_columns_captured():
+    D, page = 128, 64
+    b = Batch([20, 60], [1800, 1800], page=page)
+    cache = torch.from_numpy(random_cache(b, 1, 1, D)).to(DEV)
+    starts, lengths, tb = b.dev()
+    q = torch.randn((1, 80, 8, D), device=DEV).to(BF16)
+    out = torch.zeros((1, 80, 8 * D), dtype=BF16, device=DEV)
+    need = B.btq_kv_attention_workspace_bytes(1, 80, 8, 1, D, 2, tb.shape[1], page)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    B.btq_kv_attention(q, starts, lengths, tb, cache, out=out, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.btq_kv_attention(q, starts, lengths, tb, cache, out=out, workspace=ws)
+    for n in (20, 700, 1800, 0, 63):
+        lengths.copy_(torch.tensor([n, max(n - 300, 0)], dtype=torch.int32))
+        q.normal_()
+        eager = torch.empty_like(out)
+        B.btq_kv_attention(q, starts, lengths, tb, cache, out=eager)
+        ws.fill_(0xff)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), n
+
+
 # ---- CPU: all return before any HIP call ---------------------------------------
 
 A = 0x10000
