@@ -687,7 +687,7 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
     w.shard = blockIdx.y;
     int64_t sub;
     SeqRange seq;
-    w.b = find_sequence(a.kv, a.G, S::kShift, 1, first_item + blockIdx.z, &sub, &seq);
+    w.b = find_sequence(a.kv, a.G, S::kShift, part_extra(a.G, S::kShift), first_item + blockIdx.z, &sub, &seq);
     if (w.b < 0) return;
     const int cols = seq.n * a.G;
     if ((sub << S::kShift) >= cols) return;
@@ -901,7 +901,7 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
   const int64_t item = items - 1 - (id - split * items);
   int64_t sub;
   SeqRange seq;
-  const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub, &seq);
+  const int b = find_sequence(a.kv, a.G, S::kShift, part_extra(a.G, S::kShift), item, &sub, &seq);
   if (b < 0) return;
   const int cols = seq.n * a.G;
   if ((sub << S::kShift) >= cols) return;
@@ -1182,7 +1182,7 @@ __global__ __launch_bounds__(256) void attention_splits_kernel(AttnArgs a, uint3
   const int64_t id = item * heads + shard * a.kv.Hk + head;
   int64_t sub;
   SeqRange seq;
-  const int b = find_sequence(a.kv, a.G, S::kShift, 1, item, &sub, &seq);
+  const int b = find_sequence(a.kv, a.G, S::kShift, part_extra(a.G, S::kShift), item, &sub, &seq);
   if (b < 0) return;
   const int cols = seq.n * a.G;
   if ((sub << S::kShift) >= cols) return;
@@ -1276,7 +1276,7 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
   // weigh more: 64 of 300 keys with 64 columns 36 against 40, with 96 52 against 43.
   const int64_t few = max_length > 512 ? 128 : 64;
   if (columns <= few * B) {
-    p.items = columns / 16 + B;
+    p.items = (columns + (int64_t)B * part_extra(G, 4)) / 16;
     // groups of columns that exist, as far as the host knows: each row has one at least
     const int64_t rows = T < B ? T : B;
     const int64_t units = (rows > columns / 16 ? rows : columns / 16) * heads;
@@ -1298,7 +1298,7 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
   }
   p.kind = kAttnColumns;
   const int64_t cols = D <= 128 ? 128 : 64;
-  p.items = columns / cols + B;
+  p.items = (columns + (int64_t)B * part_extra(G, D <= 128 ? 7 : 6)) / cols;
   // blocks that fill the chip
   const int64_t units = (columns + cols - 1) / cols * heads;
   const int64_t most = (max_length + kColsTile * kMinTiles - 1) / (kColsTile * kMinTiles);

@@ -409,10 +409,16 @@ __device__ __forceinline__ SeqRange uniform(const SeqRange& s) {
 }
 
 // Work items lie sequence after sequence. An item covers 2^shift of a sequence's
-// rows*mul, so b's begin at most at floor(starts[b]*mul / 2^shift) + b*extra, and
-// that many are set aside: with extra 1 for parts that begin at the first row, 2
-// for parts that begin at a multiple of 2^shift in the sequence. The grid then
-// follows from T and the number of sequences, which the host knows.
+// rows*mul, and b's begin at floor((starts[b]*mul + b*extra) / 2^shift). That leaves
+// each sequence as many as it needs with extra 2^shift less the largest power of 2 up to
+// 2^shift that divides mul (part_extra), for parts that begin at the first row, and with
+// 2*2^shift for parts that begin at a multiple of 2^shift in the sequence. The grid then
+// follows from T and the number of sequences, which the host knows; of parts no item is
+// without work where each sequence has one row.
+__host__ __device__ inline int part_extra(int mul, int shift) {
+  const int two = mul & -mul, all = 1 << shift;
+  return all - (two < all ? two : all);
+}
 // Returns the sequence of `item` (a whole wave asks for one item) with its rows and
 // length, and leaves the item's number in it; or -1. 64 sequences a step; the last
 // step has loaded the rows and lengths of all it looks at, so they cost no load of
@@ -426,14 +432,13 @@ __device__ __forceinline__ int find_sequence(const KvArgs& a, int mul, int shift
     const int b = lo + lane * step;
     const int at = min(b, a.B - 1);
     const int start = a.starts[at], next = a.starts[at + 1], length = a.lengths[at];
-    const int64_t first = (((int64_t)start * mul) >> shift) + (int64_t)b * extra;
+    const int64_t first = ((int64_t)start * mul + (int64_t)b * extra) >> shift;
     const int n = __popcll(__ballot(b < hi && first <= item));
     if (n == 0) return -1;
     lo += (n - 1) * step;
     hi = min(hi, lo + step);
     if (step == 1) {
-      *sub = item - (((int64_t)__builtin_amdgcn_readlane(start, n - 1) * mul) >> shift) -
-             (int64_t)lo * extra;
+      *sub = item - (((int64_t)__builtin_amdgcn_readlane(start, n - 1) * mul + (int64_t)lo * extra) >> shift);
       *range = cut_range(a, __builtin_amdgcn_readlane(start, n - 1),
                          __builtin_amdgcn_readlane(next, n - 1),
                          __builtin_amdgcn_readlane(length, n - 1));

@@ -21,7 +21,7 @@ __device__ __forceinline__ bool find_place(const KvArgs& a, int64_t item, int64_
                                            Place* o) {
   int64_t sub;
   SeqRange s;
-  const int b = find_sequence(a, 1, 5, 2, item, &sub, &s);
+  const int b = find_sequence(a, 1, 5, 2 * kBlockTokens, item, &sub, &s);
   if (b < 0) return false;
   const int block = (s.first() >> 5) + (int)sub;
   o->first = block * kBlockTokens;
