@@ -1281,10 +1281,11 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
     const int64_t rows = T < B ? T : B;
     const int64_t units = (rows > columns / 16 ? rows : columns / 16) * heads;
     // A block takes a group of columns whole where that leaves none much longer than an
-    // equal share of a full chip: up to 4096 keys with 512 groups, up to 2048 with 256
-    // or fewer, whose second launch would cost more (128 groups of 2000 keys 15 us whole,
-    // 18 in shares; of 4000 24 in shares).
-    const int64_t longest = units >= 512 ? 4096 : units > 256 ? units * 8 : 2048;
+    // equal share of a full chip, which costs a second launch and a beginning for every
+    // cut. D = 128, us whole against in shares: 128 groups of 2000 keys 15 against 18, of
+    // up to 4000 24 against 31, 256 of 4000 29 against 34, of up to 6000 37 against 36,
+    // 512 of up to 8000 73 against 67; 64 groups of 4000 26 against 21.
+    const int64_t longest = units >= 128 ? 4096 : 2048;
     if (max_length <= longest || units >= 4096) {
       p.kind = kAttnKeys;
     } else {
