@@ -252,7 +252,7 @@ hipError_t launch_head_norm_rope(const HeadArgs& a, hipStream_t s) {
   if (a.D % 16 == 0 && a.D <= 1024 && dim % 16 == 0 && on16(a.x) && on16(a.y) &&
       weight_on16(a.q_weight, a.qw_shard, a.qw_head) &&
       weight_on16(a.k_weight, a.kw_shard, a.kw_head) && ((uintptr_t)a.rope.cos & 15) == 0 &&
-      ((uintptr_t)a.rope.sin & 15) == 0 && items < (int64_t(1) << 23)) {
+      ((uintptr_t)a.rope.sin & 15) == 0 && items < (int64_t(1) << 25)) {   // (2^31 threads)
     if (a.D <= 32) return launch_types<2>(a, s);
     if (a.D <= 64) return launch_types<4>(a, s);
     if (a.D <= 128) return launch_types<8>(a, s);

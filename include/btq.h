@@ -544,7 +544,7 @@ int64_t btq_kv_block_bytes(int64_t D);
  * 1 <= D <= 65536, q_heads and k_heads >= 0, one of them at least. NaN and Inf
  * spread to their head as the formulas give them. The vector kernel takes
  * D <= 1024, D and rope_dim multiples of 16, heads, weights and tables on 16
- * bytes, and fewer than 2^23 heads a shard; others take a general one.
+ * bytes, and fewer than 2^25 heads a shard; others take a general one.
  */
 int btq_head_norm_rope(const void *x, int x_type, int64_t x_shard, int64_t x_pitch, int64_t x_head,
                        int64_t P, int64_t T, int64_t q_heads, int64_t k_heads, int64_t D,
