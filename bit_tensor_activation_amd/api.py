@@ -24,6 +24,14 @@ Layouts (contiguous, row-major, last index fastest):
   y             float32 [T,H]  (bf16 bits, int16 [T,H], for bf16 output)
 The 8-bit linear layer and the block norm take bf16 tensors in both forms too,
 and return bf16 as torch.bfloat16 where they are given torch.bfloat16.
+
+Attention between two linear layers (a shard's dimension P may be left out of all
+tensors of a call):
+  q, k, v       bf16 (k, v and heads to norm: float32 too) [P,T,heads,D], any strides
+                with D contiguous: slices of a fused projection's rows
+  seq_starts    int32 [B+1];  lengths int32 [B];  page_table int32 [B,max_pages]
+  cache         uint8 [P,pages,Hk,page_size/32,32*D+256], zeros at first or not
+  cos, sin      float32 [positions,rope_dim/2]
 """
 from __future__ import annotations
 
