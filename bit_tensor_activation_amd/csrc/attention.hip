@@ -1223,9 +1223,9 @@ hipError_t each_launch(int64_t items, F f) {
   return hipGetLastError();
 }
 
-// 4 waves a block: 8 of them take longer at any one length (256 groups of 2000 keys 30
-// against 24 us, of 250 keys 12.6 against 8.9; 128 of 1000 10.3 against 9.7), and only
-// less where a few of some 256 groups are much longer (500 to 2000 keys 21 against 23).
+// 4 waves a block: a SIMD that has one wave is kept busy by its instructions (some 2 us a
+// tile of 128 keys at D = 128), so 8 of them, us against 4, take 26 against 27 for 128
+// groups of 4000 keys, but 22 against 20 for 256 of 2000 and 37 against 31 for 512.
 template <int D, int NT>
 hipError_t launch_keys(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
   return each_launch(plan.items, [&](uint32_t first, unsigned n) {
