@@ -622,7 +622,7 @@ int btq_kv_attention(const void* q, int64_t q_shard, int64_t q_pitch, int64_t q_
   if (st == BTQ_OK) st = check_head_rows(P, T, Hq, D, q_shard, q_pitch, q_head);
   if (st != BTQ_OK) return st;
   if (window < 0) return BTQ_ERR_SHAPE;
-  if (!value_type(out_type) || !(scale > 0.0f && scale < INFINITY)) return BTQ_ERR_ARG;
+  if (!value_type(out_type) || !(scale > 0.0f && scale <= 0x1p127f)) return BTQ_ERR_ARG;
   if (T > 0 && B > 0 && (!q || !out)) return BTQ_ERR_ARG;
   if (!aligned(q, 2) || !aligned(out, out_type == BTQ_T_F32 ? 8 : 4) || !aligned(lse, 4) ||
       !aligned(workspace, 16))

@@ -458,7 +458,7 @@ def test_refusals():
         assert call(**kw) == SHAPE, kw
     for kw in (dict(q=None), dict(out=None), dict(starts=None), dict(lengths=None), dict(tb=None),
                dict(cache=None), dict(ot=2), dict(scale=0.0), dict(scale=-1.0),
-               dict(scale=float("inf")), dict(scale=float("nan"))):
+               dict(scale=float("inf")), dict(scale=1.8e38), dict(scale=float("nan"))):
         assert call(**kw) == ARG, kw
     for kw in (dict(q=A + 1), dict(out=A + 2), dict(ot=0, out=A + 4), dict(lse=A + 2), dict(ws=A + 8),
                dict(cache=A + 8), dict(starts=A + 1)):
