@@ -82,6 +82,12 @@ __device__ __forceinline__ float from_lane(float x) {
   return __uint_as_float(row_lane<kLane>(__float_as_uint(x)));
 }
 
+// x of lane kLane of each quad.
+template <int kLane>
+__device__ __forceinline__ float from_quad(float x) {
+  return __uint_as_float(dpp<0x55 * kLane>(__float_as_uint(x)));
+}
+
 // x combined over the 4 lanes that hold one column.
 template <typename F>
 __device__ __forceinline__ float column_combine(float v, F f) {
@@ -132,7 +138,9 @@ struct Columns {
   int any_lo, any_hi;        // keys that some column sees
 
   // Columns [col0, col0 + 16*NT) of a sequence, of which those below cols exist, and
-  // their queries as they are, this lane's quarter of the features.
+  // their queries as they are, this lane's quarter of the features. Of W = 8 columns
+  // lanes 8 .. 15 have the same ones as lanes 0 .. 7.
+  template <int W = 16 * NT>
   __device__ __forceinline__ void fetch(const AttnArgs& a, const SeqRange& s, int64_t shard, int head,
                                         int col0, int cols, v4u (&w)[NT][NS]) {
     const int lane = thread_here() & 63, cl = lane & 15, g = lane >> 4;
@@ -142,14 +150,14 @@ struct Columns {
       const uint32_t x = (uint32_t)(rest + col - col0);
       return first + (int)(a.G == 1 ? x : __umulhi(x, a.G_inverse));
     };
-    const int last = query(min(col0 + 16 * NT, cols) - 1);
+    const int last = query(min(col0 + W, cols) - 1);
     all_hi = a.causal ? min(s.first() + first + 1, s.length) : s.length;
     all_lo = a.window ? s.first() + last + 1 - a.window : 0;
     any_hi = a.causal ? clamp_int(s.first() + last + 1, 0, s.length) : s.length;
     any_lo = a.window ? max(s.first() + first + 1 - a.window, 0) : 0;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int col = col0 + n * 16 + cl;
+      const int col = col0 + n * 16 + (W < 16 ? cl % W : cl);
       const bool live = col < cols;
       const int qi = query(live ? col : col0), pos = s.first() + qi;
       hi[n] = a.causal ? min(pos + 1, s.length) : s.length;
@@ -333,22 +341,27 @@ __device__ __forceinline__ Partial partial(const AttnArgs& a, int64_t slot, int6
 constexpr int kTile = 128;
 constexpr int kTileBlocks = kTile / kBlockTokens;
 
-template <int NT>
-struct KeysShape {
-  static constexpr int C = 16 * NT;
-  static constexpr int kShift = NT == 1 ? 4 : 5;
-};
-
-template <int D, int NT>
+//
+// A group has W = 16 columns, or 8 where sequences have no more on average. Those
+// take the matrix instruction's 16 columns twice: as 0 .. 7 for one step of 32 keys and
+// as 8 .. 15 for the next, with zeros for queries (and later weights) in the other half,
+// so both steps' scores add up in one accumulator and a lane has half as many to
+// turn into weights (771 -> 590 vector instructions a tile). The halves' sums join at
+// the end.
+template <int D, int W>
 struct KeysWave {
+  static constexpr int NT = 1;
   static constexpr int NS = D / 32, ND = D / 16;
   Columns<D, NT> c;
   const AttnArgs& a;
   int b, head;
   int64_t shard;
   uint32_t magic;
-  uint32_t k[4][2][NS], kw[2], vw[2];
+  // words of the lane's keys and values: KW pairs, h-th of a pair 4 keys further
+  static constexpr int KW = W == 8 ? 2 : 1;
+  uint32_t k[4][2][NS], kw[KW][2], vw[KW][2];
   v4u v[ND];
+  v8h q_high[W == 8 ? NS : 1];   // W = 8: queries as columns 8 .. 15; c.q has the others
 
   __device__ __forceinline__ explicit KeysWave(const AttnArgs& args) : a(args) {
     magic = 0x43004300u;
@@ -379,7 +392,7 @@ struct KeysWave {
     const int lane = thread_here() & 63, cl = lane & 15, g = lane >> 4;
     int pk = page(begin, cl / 4), pv = page(begin, g);
     v4u raw[NT][NS];
-    c.fetch(a, seq, shard, head, col0, cols, raw);
+    c.template fetch<W>(a, seq, shard, head, col0, cols, raw);
     int64_t kat, vat;
     place(begin, end, cl / 4, pk, &kat);
     bool there = place(begin, end, g, pv, &vat);
@@ -388,6 +401,15 @@ struct KeysWave {
     load_words(vat, kw, vw);
     load_values(vat);
     c.take(raw);
+    if constexpr (W == 8) {
+      const uint32_t low = cl < 8 ? 0xffffffffu : 0u;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const v4u x = __builtin_bit_cast(v4u, c.q[0][i]);
+        c.q[0][i] = __builtin_bit_cast(v8h, x & low);
+        q_high[i] = __builtin_bit_cast(v8h, x & ~low);
+      }
+    }
     // whether columns see different keys
     const int uneven = c.all_lo > c.any_lo || c.all_hi < c.any_hi ? 2 : 0;
     for (int tile = begin; tile < end; tile += step) {
@@ -396,12 +418,40 @@ struct KeysWave {
       place(tile + step, end, cl / 4, pk, &kat);
       const bool there_next = place(tile + step, end, g, pv, &vat);
       pk = page(tile + 2 * step, cl / 4), pv = page(tile + 2 * step, g);
-      uint32_t kw_next[2], vw_next[2];
+      uint32_t kw_next[KW][2], vw_next[KW][2];
       load_words(vat, kw_next, vw_next);
       compute(kat, vat, key0, there, uniform(full ? 0 : 1 | uneven));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) kw[j] = kw_next[j], vw[j] = vw_next[j];
+      for (int p = 0; p < KW; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) kw[p][j] = kw_next[p][j], vw[p][j] = vw_next[p][j];
       there = there_next;
+    }
+    if constexpr (W == 8) join_halves();
+  }
+  // Columns 8 .. 15 added to 0 .. 7, whose they are.
+  __device__ __forceinline__ void join_halves() {
+    auto other = [](float x) { return __uint_as_float(dpp<0x128>(__float_as_uint(x))); };
+    const float m = fmaxf(c.m2[0], other(c.m2[0]));
+    // (where there was no score above -Inf the sums are 0 or NaN)
+    const float f = c.m2[0] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(c.m2[0] - m);
+    auto join = [&](float& x) {
+      x *= f;
+      x += other(x);
+    };
+    c.m2[0] = m;
+    join(c.l[0]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float z = c.oz[0][i];
+      join(z);
+      c.oz[0][i] = z;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        float x = c.o[0][d][i];
+        join(x);
+        c.o[0][d][i] = x;
+      }
     }
   }
   __device__ __forceinline__ void load_keys(int64_t at) {
@@ -412,11 +462,21 @@ struct KeysWave {
 #pragma unroll
       for (int h = 0; h < 2; ++h) __builtin_memcpy(k[s][h], p + (8 * s + 4 * h) * (D / 2), 4 * NS);
   }
-  // words of keys and values 8*(cl/4) + cl%4 and 4 further of the lane's block
-  __device__ __forceinline__ void load_words(int64_t at, uint32_t (&x)[2], uint32_t (&y)[2]) {
+  // The first key of the lane's words, of its block: that of step cl/4, or, of pair p, of
+  // step 2*p + cl/8.
+  static __device__ __forceinline__ int word_key(int cl, int p) {
+    return (W == 8 ? 16 * p + (cl & 8) : 8 * (cl >> 2)) + (cl & 3);
+  }
+  __device__ __forceinline__ void load_words(int64_t at, uint32_t (&x)[KW][2], uint32_t (&y)[KW][2]) {
     const int cl = threadIdx.x & 15;
-    const uint32_t* p = (const uint32_t*)(a.kv.cache + at + 32 * D) + 8 * (cl >> 2) + (cl & 3);
-    x[0] = p[0], x[1] = p[4], y[0] = p[32], y[1] = p[36];
+    const uint32_t* from = (const uint32_t*)(a.kv.cache + at + 32 * D);
+#pragma unroll
+    for (int p = 0; p < KW; ++p)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        x[p][h] = from[word_key(cl, p) + 4 * h];
+        y[p][h] = from[word_key(cl, p) + 4 * h + 32];
+      }
   }
   __device__ __forceinline__ void load_values(int64_t at) {
     const uint8_t* p = a.kv.cache + at + 16 * D + (threadIdx.x & 15) * 16;
@@ -427,49 +487,70 @@ struct KeysWave {
   // One tile; the next one's keys load when the first product is done with these,
   // its values after the second.
   __device__ __forceinline__ void compute(int64_t kat, int64_t vat, int key0, bool there, int mask) {
-    constexpr int KS = NT == 1 ? 2 : 1;   // steps of 32 keys whose scores are held at once
+    // Passes of KS steps of 32 keys, of which a lane has scores of KL.
+    constexpr int KS = W == 8 ? 4 : 2, KL = 2;
+    const int cl = threadIdx.x & 15;
     const int base = key0 + ((threadIdx.x & 63) >> 4) * kBlockTokens;
-    // of the lane's 2 keys and values; a step's products take them from the lanes
+    // of the lane's keys and values; a step's products take them from the lanes
     // that have them. Whatever stands in a place that holds nothing, z' is a number.
-    float ks[2], kz[2], vs[2];
+    float ks[KW][2], kz[KW][2], vs[KW][2];
+    uint32_t vz[KW];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      ks[h] = __uint_as_float(kw[h] & 0xffff0000u);
-      kz[h] = -__uint_as_float(kw[h] << 16);
-      vs[h] = __uint_as_float(vw[h] & 0xffff0000u);
+    for (int p = 0; p < KW; ++p) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ks[p][h] = __uint_as_float(kw[p][h] & 0xffff0000u);
+        kz[p][h] = -__uint_as_float(kw[p][h] << 16);
+        vs[p][h] = __uint_as_float(vw[p][h] & 0xffff0000u);
+      }
+      vz[p] = (vw[p][0] & 0xfu) | (vw[p][1] & 0xfu) << 16 | magic;
     }
     if (mask) {   // places that no column sees may hold anything
       keep_branch();
-      const int cl = threadIdx.x & 15, key = base + 8 * (cl >> 2) + (cl & 3);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (!there || key + 4 * h < c.any_lo || key + 4 * h >= c.any_hi) vs[h] = 0.0f;
+      for (int p = 0; p < KW; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = base + word_key(cl, p) + 4 * h;
+          if (!there || key < c.any_lo || key >= c.any_hi) vs[p][h] = 0.0f;
+        }
     }
-    const uint32_t vz = (vw[0] & 0xfu) | (vw[1] & 0xfu) << 16 | magic;
-    static_for<0, 4, KS>([&](auto step) {
-      constexpr int S0 = decltype(step)::value;
-      float t[NT][8 * KS];   // value 8*s + 4*h + i is key 8*(S0 + s) + 4*h + i of the lane's block
-      static_for<0, KS, 1>([&](auto index) {
+    // A value of the lane's key 4*h + i of its step s of the pass
+    static_for<0, 4, KS>([&](auto pass) {
+      constexpr int S0 = decltype(pass)::value;
+      auto of_key = [&](const float (&x)[KW][2], auto index, auto value) {
+        constexpr int s = decltype(index)::value, h = decltype(value)::value / 4, i = decltype(value)::value % 4;
+        if constexpr (W == 8)
+          return from_quad<i>(x[s][h]);
+        else
+          return from_lane<4 * (S0 + s) + i>(x[0][h]);
+      };
+      // Value 8*s + 4*h + i: key 4*h + i of the block's step S0 + s, or 2*s and, in lanes
+      // 8 .. 15, 2*s + 1
+      float t[1][8 * KL];
+      static_for<0, KL, 1>([&](auto index) {
         constexpr int s = decltype(index)::value;
         // both halves together: a product waits for the one before it in its own
-        v4f acc[2][NT];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) acc[h][n] = v4f{0, 0, 0, 0};
+        v4f acc[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
 #pragma unroll
         for (int w = 0; w < NS; ++w)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const v8b kc = as_bf16(codes_to_bf16(k[S0 + s][h][w], magic));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) acc[h][n] = mfma(kc, __builtin_bit_cast(v8b, c.q[n][w]), acc[h][n]);
+            const v8b kc = as_bf16(codes_to_bf16(k[W == 8 ? 2 * s : S0 + s][h][w], magic));
+            acc[h] = mfma(kc, __builtin_bit_cast(v8b, c.q[0][w]), acc[h]);
           }
-        static_for<0, 8, 1>([&](auto value) {
-          constexpr int h = decltype(value)::value / 4, i = decltype(value)::value % 4, L = 4 * (S0 + s) + i;
+        if constexpr (W == 8) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            t[n][8 * s + 4 * h + i] = (acc[h][n][i] + from_lane<L>(kz[h]) * c.qsum[n]) * from_lane<L>(ks[h]);
+          for (int w = 0; w < NS; ++w)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const v8b kc = as_bf16(codes_to_bf16(k[2 * s + 1][h][w], magic));
+              acc[h] = mfma(kc, __builtin_bit_cast(v8b, q_high[w]), acc[h]);
+            }
+        }
+        static_for<0, 8, 1>([&](auto value) {
+          constexpr int h = decltype(value)::value / 4, i = decltype(value)::value % 4;
+          t[0][8 * s + 4 * h + i] = (acc[h][i] + of_key(kz, index, value) * c.qsum[0]) * of_key(ks, index, value);
         });
       });
       if constexpr (S0 + KS == 4) {
@@ -478,12 +559,12 @@ struct KeysWave {
         issue_fence();
       }
       auto hide = [&](float with) {
+        const int first = base + 8 * S0 + (W == 8 ? (threadIdx.x & 8) : 0);
+        const int from = there ? c.lo[0] - first : 32, to = c.hi[0] - first;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int from = there ? c.lo[n] - base - 8 * S0 : 32, to = c.hi[n] - base - 8 * S0;
-#pragma unroll
-          for (int key = 0; key < 8 * KS; ++key)
-            t[n][key] = key >= from && key < to ? t[n][key] : with;
+        for (int v = 0; v < 8 * KL; ++v) {
+          const int key = W == 8 ? (v >> 3) * 16 + (v & 7) : v;
+          t[0][v] = key >= from && key < to ? t[0][v] : with;
         }
       };
       if (mask) {
@@ -491,30 +572,29 @@ struct KeysWave {
         hide(kNegInf);
       }
       c.weights(a.scale2, t);
-      static_for<0, 8 * KS, 1>([&](auto index) {
-        constexpr int key = decltype(index)::value, L = 4 * (S0 + key / 8) + key % 4;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) t[n][key] *= from_lane<L>(vs[key / 4 % 2]);
+      static_for<0, KL, 1>([&](auto index) {
+        static_for<0, 8, 1>([&](auto value) {
+          t[0][8 * decltype(index)::value + decltype(value)::value] *= of_key(vs, index, value);
+        });
       });
       if (mask & 2) {   // the scale of a value that only others see may be NaN
         keep_branch();
         hide(0.0f);
       }
       static_for<0, KS, 1>([&](auto index) {
-        constexpr int s = decltype(index)::value, L = 4 * (S0 + s);
-        const v8b z = as_bf16(v4u{row_lane<L>(vz), row_lane<L + 1>(vz), row_lane<L + 2>(vz), row_lane<L + 3>(vz)});
-        v8b p[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          p[n] = weights_to_bf16(&t[n][8 * s]);
-          c.oz[n] = mfma(z, p[n], c.oz[n]);
+        constexpr int s = decltype(index)::value;
+        constexpr int L = W == 8 ? 8 * (s % 2) : 4 * (S0 + s), p = W == 8 ? s / 2 : 0;
+        const v8b z = as_bf16(v4u{row_lane<L>(vz[p]), row_lane<L + 1>(vz[p]), row_lane<L + 2>(vz[p]),
+                                  row_lane<L + 3>(vz[p])});
+        v8b weight = weights_to_bf16(&t[0][8 * (W == 8 ? s / 2 : s)]);
+        if constexpr (W == 8) {
+          const uint32_t mine = (threadIdx.x & 8) == (s % 2 ? 8u : 0u) ? 0xffffffffu : 0u;
+          weight = as_bf16(__builtin_bit_cast(v4u, weight) & mine);
         }
+        c.oz[0] = mfma(z, weight, c.oz[0]);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          const v8b vc = as_bf16(codes_to_bf16(v[d][S0 + s], magic));
-#pragma unroll
-          for (int n = 0; n < NT; ++n) c.o[n][d] = mfma(vc, p[n], c.o[n][d]);
-        }
+        for (int d = 0; d < ND; ++d)
+          c.o[0][d] = mfma(as_bf16(codes_to_bf16(v[d][S0 + s], magic)), weight, c.o[0][d]);
       });
     });
     issue_fence();
@@ -606,42 +686,33 @@ __device__ __forceinline__ int64_t flat_share(int64_t all, int begin) {
 // The sums of the team's first `waves` waves (the others had no tile), each relative
 // to the common maximum, added in the waves' order; to `out` where they are whole,
 // else to a partial result.
-template <int D, int NT, int kTeam, bool kStream>
-__device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, NT>& c, const SeqRange& seq,
+template <int D, int W, int kTeam, bool kStream>
+__device__ __forceinline__ void join_team(const AttnArgs& a, const Columns<D, 1>& c, const SeqRange& seq,
                                           int64_t shard, int head, int col0, int cols, int waves, bool whole,
                                           const Partial& part) {
-  constexpr int C = 16 * NT, kVec = D / 4;
+  constexpr int C = W, kVec = D / 4;
   __shared__ float2 stat[kTeam][C];       // maximum and sum of p
   __shared__ float factor[C];             // 1/sum of all, or 1
   __shared__ v4f sums[kTeam][C][kVec + 1];
   const int tid = thread_here(), lane = tid & 63, wave = tid >> 6, cl = lane & 15, g = lane >> 4;
   const int live = min(C, cols - col0);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const float sum = column_sum(c.l[n]);
-    if (g == 0) stat[wave][n * 16 + cl] = make_float2(c.m2[n], sum);
-  }
+  const float own = column_sum(c.l[0]);
+  if (g == 0 && cl < C) stat[wave][cl] = make_float2(c.m2[0], own);
   lds_barrier();
-  if (wave < waves) {
+  if (wave < waves && cl < live) {
+    float m = kNegInf;
+    for (int w = 0; w < waves; ++w) m = fmaxf(m, stat[w][cl].x);
+    const float f = share(c.m2[0], own, m);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = n * 16 + cl;
-      float m = kNegInf;
-      for (int w = 0; w < waves; ++w) m = fmaxf(m, stat[w][col].x);
-      const float f = share(c.m2[n], stat[wave][col].y, m);
-      if (col < live) {
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) sums[wave][col][d * 4 + g] = (c.o[n][d] - c.oz[n]) * f;
-      }
-      if (wave == 0 && g == 0 && col < live) {
-        float sum = 0.0f;
-        for (int w = 0; w < waves; ++w) sum += stat[w][col].y * share(stat[w][col].x, stat[w][col].y, m);
-        factor[col] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (!whole)
-          *(float2*)(part.stats + 2 * col) = make_float2(m, sum);
-        else if (a.lse)
-          a.lse[out_row(a, seq, shard, head, col0 + col)] = lse_of(m, sum);
-      }
+    for (int d = 0; d < D / 16; ++d) sums[wave][cl][d * 4 + g] = (c.o[0][d] - c.oz[0]) * f;
+    if (wave == 0 && g == 0) {
+      float sum = 0.0f;
+      for (int w = 0; w < waves; ++w) sum += stat[w][cl].y * share(stat[w][cl].x, stat[w][cl].y, m);
+      factor[cl] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (!whole)
+        *(float2*)(part.stats + 2 * cl) = make_float2(m, sum);
+      else if (a.lse)
+        a.lse[out_row(a, seq, shard, head, col0 + cl)] = lse_of(m, sum);
     }
   }
   lds_barrier();
@@ -676,51 +747,51 @@ __device__ __forceinline__ Cut* cuts(const AttnArgs& a) {
 // lengths fills the chip evenly; a group of columns that a cut divides leaves
 // partial results (slot 2*block + 1 where it begins in the block, else 2*block),
 // which attention_join_kernel adds. Else a block takes one group of columns.
-template <int D, int NT, int kTeam, bool kStream>
+template <int D, int W, int kTeam, bool kStream>
 __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_kernel(AttnArgs a,
                                                                                      uint32_t first_item) {
-  using S = KeysShape<NT>;
+  constexpr int kShift = W == 8 ? 3 : 4;
   const int wave = uniform((int)threadIdx.x >> 6);
-  KeysWave<D, NT> w(a);
+  KeysWave<D, W> w(a);
   if constexpr (!kStream) {
     w.head = blockIdx.x;
     w.shard = blockIdx.y;
     int64_t sub;
     SeqRange seq;
-    w.b = find_sequence(a.kv, a.G, S::kShift, part_extra(a.G, S::kShift), first_item + blockIdx.z, &sub, &seq);
+    w.b = find_sequence(a.kv, a.G, kShift, part_extra(a.G, kShift), first_item + blockIdx.z, &sub, &seq);
     if (w.b < 0) return;
     const int cols = seq.n * a.G;
-    if ((sub << S::kShift) >= cols) return;
-    const int col0 = (int)sub << S::kShift;
+    if ((sub << kShift) >= cols) return;
+    const int col0 = (int)sub << kShift;
     int lo, hi;
-    keys_seen(a, seq, col0, min(col0 + S::C, cols), &lo, &hi);
+    keys_seen(a, seq, col0, min(col0 + W, cols), &lo, &hi);
     const int t0 = lo / kTile, t1 = (hi + kTile - 1) / kTile;
     w.run(seq, col0, cols, t0 + wave, t1, kTeam);
-    join_team<D, NT, kTeam, kStream>(a, w.c, seq, w.shard, w.head, col0, cols, clamp_int(t1 - t0, 1, kTeam),
-                                     true, Partial{});
+    join_team<D, W, kTeam, kStream>(a, w.c, seq, w.shard, w.head, col0, cols, clamp_int(t1 - t0, 1, kTeam),
+                                    true, Partial{});
   } else {
     __shared__ int64_t scan[kTeam];
     __shared__ Flat found;
     int64_t mine;
     int b0, b1;
     const int64_t per_head =
-        uniform(flat_total<64 * kTeam>(a, S::kShift, scan, &mine, &b0, &b1));
+        uniform(flat_total<64 * kTeam>(a, kShift, scan, &mine, &b0, &b1));
     const int64_t all = per_head * a.kv.P * a.kv.Hk, each = flat_share(all, a.begin);
     const int64_t x0 = blockIdx.x * each, x1 = min(x0 + each, all);
-    Cut* cut = cuts<D, S::C>(a) + blockIdx.x;
+    Cut* cut = cuts<D, W>(a) + blockIdx.x;
     if (x0 >= x1) {
       if (threadIdx.x == 0) cut->parts = 0;
       return;
     }
     int hk = (int)divide(x0, per_head);
-    flat_find<64 * kTeam>(a, S::kShift, x0 - hk * per_head, mine, b0, b1, &found);
+    flat_find<64 * kTeam>(a, kShift, x0 - hk * per_head, mine, b0, b1, &found);
     __syncthreads();
     w.b = __builtin_amdgcn_readfirstlane(found.b);
     int64_t begin = hk * per_head + uniform(found.begin);   // of sequence w.b of head hk
     int parts = 0, cut_group = 0;
     for (int64_t x = x0; x < x1;) {
       const SeqRange seq = uniform(seq_range(a.kv, w.b));
-      const SeqTiles st = seq_tiles(a, seq, S::kShift);
+      const SeqTiles st = seq_tiles(a, seq, kShift);
       const int64_t n = (int64_t)st.groups * st.length();
       if (x >= begin + n) {   // on to the next sequence, or the next head's first
         begin += n;
@@ -732,13 +803,13 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
       const int t0 = (int)(max(x, tiles) - tiles), t1 = (int)(min(x1, unit + st.length()) - tiles);
       x = unit + st.length();
       if (t1 <= t0) continue;   // a share that ends in a beginning leaves it to the next
-      const int cols = seq.n * a.G, col0 = group << S::kShift;
+      const int cols = seq.n * a.G, col0 = group << kShift;
       w.shard = hk / a.kv.Hk;
       w.head = hk % a.kv.Hk;
       w.run(seq, col0, cols, st.first + t0 + wave, st.first + t1, kTeam);
-      join_team<D, NT, kTeam, kStream>(
+      join_team<D, W, kTeam, kStream>(
           a, w.c, seq, w.shard, w.head, col0, cols, min(t1 - t0, kTeam), t1 - t0 == st.tiles,
-          partial(a, 2 * (int64_t)blockIdx.x + (t0 == 0), 2 * kStreamBlocks, S::C, D));
+          partial(a, 2 * (int64_t)blockIdx.x + (t0 == 0), 2 * kStreamBlocks, W, D));
       if (x > x1 && t0 == 0) {
         parts = (int)(divide(x - 1, each) - blockIdx.x) + 1;
         cut_group = group;
@@ -753,9 +824,9 @@ __global__ __launch_bounds__(64 * kTeam, D <= 128 ? 2 : 1) void attention_keys_k
 // in, blockIdx.y a part of its columns. Threads by (team, column, 4 features), the
 // blocks of a cut shared out over teams.
 constexpr int kJoinThreads = 512;
-template <int D, int NT>
+template <int D>
 __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a) {
-  constexpr int C = 16 * NT, kVec = D / 4;
+  constexpr int C = 16, kVec = D / 4;
   constexpr int kSpan = C / 4;                                       // columns of a block
   constexpr int kItems = kSpan * kVec;
   constexpr int kTeams = kItems >= kJoinThreads ? 1 : kJoinThreads / kItems;
@@ -764,7 +835,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
   const Cut cut = cuts<D, C>(a)[blockIdx.x];
   if (cut.parts == 0) return;
   const SeqRange seq = uniform(seq_range(a.kv, cut.b));
-  const int cols = seq.n * a.G, first = blockIdx.y * kSpan, col0 = (cut.group << (NT == 1 ? 4 : 5)) + first;
+  const int cols = seq.n * a.G, first = blockIdx.y * kSpan, col0 = (cut.group << 4) + first;
   if (col0 >= cols) return;
   const int64_t slots = 2 * kStreamBlocks;
   for (int i = threadIdx.x % (kTeams == 1 ? kJoinThreads : kItems); i < kItems;
@@ -1226,18 +1297,18 @@ hipError_t each_launch(int64_t items, F f) {
 // 4 waves a block: a SIMD that has one wave is kept busy by its instructions (some 2 us a
 // tile of 128 keys at D = 128), so 8 of them, us against 4, take 26 against 27 for 128
 // groups of 4000 keys, but 22 against 20 for 256 of 2000 and 37 against 31 for 512.
-template <int D, int NT>
+template <int D, int W>
 hipError_t launch_keys(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
   return each_launch(plan.items, [&](uint32_t first, unsigned n) {
-    attention_keys_kernel<D, NT, 4, false><<<dim3(a.kv.Hk, (unsigned)a.kv.P, n), 256, 0, s>>>(a, first);
+    attention_keys_kernel<D, W, 4, false><<<dim3(a.kv.Hk, (unsigned)a.kv.P, n), 256, 0, s>>>(a, first);
   });
 }
-template <int D, int NT>
+template <int D>
 hipError_t launch_stream(const AttnArgs& a, hipStream_t s) {
   // 8 waves a block as far as their registers go: fewer, longer shares leave less to join
   constexpr int kTeam = D <= 128 ? 8 : 4;
-  attention_keys_kernel<D, NT, kTeam, true><<<dim3(kStreamBlocks), 64 * kTeam, 0, s>>>(a, 0);
-  attention_join_kernel<D, NT><<<dim3(kStreamBlocks, 4), kJoinThreads, 0, s>>>(a);
+  attention_keys_kernel<D, 16, kTeam, true><<<dim3(kStreamBlocks), 64 * kTeam, 0, s>>>(a, 0);
+  attention_join_kernel<D><<<dim3(kStreamBlocks, 4), kJoinThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 template <int D>
@@ -1256,8 +1327,11 @@ hipError_t launch_columns(const AttnArgs& a, const AttnPlan& plan, hipStream_t s
 template <int D>
 hipError_t launch_head(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
   switch (plan.kind) {
-    case kAttnKeys: return launch_keys<D, 1>(a, plan, s);
-    case kAttnStream: return launch_stream<D, 1>(a, s);
+    case kAttnKeys:
+      if constexpr (D <= 128)
+        if (plan.columns == 8) return launch_keys<D, 8>(a, plan, s);
+      return launch_keys<D, 16>(a, plan, s);
+    case kAttnStream: return launch_stream<D>(a, s);
     default: return launch_columns<D>(a, plan, s);
   }
 }
@@ -1288,6 +1362,10 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
     const int64_t longest = units >= 128 ? 4096 : 2048;
     if (max_length <= longest || units >= 4096) {
       p.kind = kAttnKeys;
+      if (D <= 128 && columns <= (int64_t)8 * B) {
+        p.columns = 8;
+        p.items = (columns + (int64_t)B * part_extra(G, 3)) / 8;
+      }
     } else {
       p.kind = kAttnStream;
       // some 5 us, or 12 tiles of 8 waves; with fewer groups than that a block has one

@@ -353,6 +353,7 @@ struct AttnPlan {
   AttnKind kind;
   int splits;               // kAttnColumns: of the keys
   int begin;                // kAttnStream: what a group of columns costs to begin, in tiles
+  int columns;              // kAttnKeys: of a group, 8 or (0) 16
   int64_t items;            // groups of columns of one head that are set aside
   size_t workspace;
 };
