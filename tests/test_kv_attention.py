@@ -115,6 +115,18 @@ def test_split_keys(length):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_shares_of_long_keys(D):
+    # equal shares of the keys, few columns and more than one group of them
+    say(f"case: kv attention shares D={D}")
+    for b, Hq in ((Batch([1, 2], [4700, 2300], page=64), 2), (Batch([1], [9000], page=64), 5),
+                  (Batch([1, 0, 3], [2500, 40, 4100], page=32, before=1, behind=1), 6),
+                  (Batch([1], [4200], page=64), 17)):
+        check(b, 1, Hq, 1, D, dt=F32)
+    check(Batch([1, 2], [4700, 2300], page=64), 1, 4, 1, D, window=3000, causal=D % 64 == 0)
+
+
+@pytest.mark.gpu
 def test_rows_that_see_nothing():
     # more rows than places, no pages, an empty sequence, a table without places
     b = Batch([12, 4, 5], [4, 64, 0])
