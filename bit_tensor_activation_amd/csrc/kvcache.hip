@@ -125,12 +125,19 @@ __device__ __forceinline__ uint32_t quantize(const float (&x)[E], uint32_t (&cod
 
 // ---- the usual form: 8 lanes a token, its features in registers ----
 //
-// A lane holds two runs of W = D/16 features of a key, those that turn into each
-// other (W*i and D/2 + W*i where halves pair, neighbours else), and 2*W neighbouring
-// features of a value. Codes of values turn in LDS: a thread merges a dword of 4
-// features of each of 8 tokens into 4 rows of 8 tokens, 12 instructions for 32
-// codes. Takes whole heads turned or none, rows on 16 bytes, and D a multiple of 64
-// (a run of whole dwords' codes).
+// A lane holds two runs of W features of a key, those that turn into each other (W*i
+// and dim/2 + W*i where halves pair, neighbours else), and 2*W neighbouring features of
+// a value; where D is no multiple of 64 some of the 8 lanes are idle. Codes of values
+// turn in LDS: a thread merges a dword of 4 features of each of 8 tokens into 4 rows of
+// 8 tokens, 12 instructions for 32 codes. Takes rows and tables on 16 bytes, and a
+// number of turned features that whole lanes have.
+// P=8, 16384 tokens, half of them turned: D = 128 55 -> 22 us by the general kernel and here,
+// 96 45 -> 20.
+template <int D>
+struct HeadLanes {
+  static constexpr int W = D % 64 == 0 ? D / 16 : D == 32 ? 4 : D == 96 ? 8 : 16;
+  static constexpr int kLanes = D / (2 * W);
+};
 template <int W, int kType>
 __device__ __forceinline__ void load_run(const void* base, int64_t first, float (&x)[W]) {
 #pragma unroll
@@ -154,32 +161,38 @@ template <int D, int kType>
 __global__ __launch_bounds__(kThreads) void kv_append_heads_kernel(HeadRows k, HeadRows v,
                                                                    RopeArgs rope, KvArgs a,
                                                                    uint32_t first_item) {
-  constexpr int W = D / 16, kPitch = D / 4 + 1;
+  constexpr int W = HeadLanes<D>::W, kLanes = HeadLanes<D>::kLanes, kPitch = D / 4 + 1;
   __shared__ uint32_t codes[kBlockTokens * kPitch];
   const int64_t shard = blockIdx.y, item = first_item + blockIdx.z;
   const int head = blockIdx.x;
   Place at;
   if (!find_place(a, item, shard, head, &at)) return;
-  const int t = threadIdx.x / 8, sub = threadIdx.x % 8;
-  const bool mine = t >= at.from && t < at.to;
-  const int64_t row = at.row + (mine ? t : at.from);   // (idle lanes read a row that is there)
-  const bool halves = rope.cos && rope.style == kHalf;
-  const int f0 = halves ? W * sub : 2 * W * sub, f1 = halves ? D / 2 + f0 : f0 + W;
+  const int t = threadIdx.x / 8, in_row = threadIdx.x % 8;
+  const bool busy = kLanes == 8 || in_row < kLanes;
+  const int sub = busy ? in_row : 0;                   // (idle lanes read what is there)
+  const bool token = t >= at.from && t < at.to, mine = token && busy;
+  const int64_t row = at.row + (token ? t : at.from);
+  const bool turn = rope.cos && 2 * W * sub < rope.dim, halves = turn && rope.style == kHalf;
+  const int f0 = halves ? W * sub : 2 * W * sub, f1 = halves ? rope.dim / 2 + f0 : f0 + W;
   float x[W], y[W], c[W], s[W], u[W], w[W];
   const int64_t kb = shard * k.shard + row * k.pitch + head * k.head;
   const int64_t vb = shard * v.shard + row * v.pitch + head * v.head + 2 * W * sub;
   load_run<W, kType>(k.p, kb + f0, x);
   load_run<W, kType>(k.p, kb + f1, y);
-  const int64_t pos = at.first + (mine ? t : at.from);
+  const int64_t pos = at.first + (token ? t : at.from);
   const bool known = pos < rope.rows;
-  if (rope.cos) {
-    const int64_t e = (known ? pos : 0) * (D / 2) + W * sub;
+  if (turn) {
+    const int64_t e = (known ? pos : 0) * (rope.dim / 2) + W * sub;
     load_run<W, kF32>(rope.cos, e, c);
     load_run<W, kF32>(rope.sin, e, s);
   }
   load_run<W, kType>(v.p, vb, u);
   load_run<W, kType>(v.p, vb + W, w);
   if (at.at < 0) return;
+  if (!busy) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) x[e] = y[e] = u[e] = w[e] = 0.0f;
+  }
   uint8_t* block = a.cache + at.at;
   // this thread's part of the values' block: features 4*fq .. of tokens 8*group ..
   const int fq = threadIdx.x / 4, group = threadIdx.x % 4;
@@ -197,7 +210,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_heads_kernel(HeadRows k, H
           old[i][r] = *(const uint32_t*)(block + 16 * D + (4 * (fq + 64 * i) + r) * 16 + group * 4);
   }
 
-  if (rope.cos) {
+  if (turn && busy) {
     if (!known) {
 #pragma unroll
       for (int e = 0; e < W; ++e) c[e] = s[e] = __uint_as_float(0x7fc00000u);
@@ -237,10 +250,12 @@ __global__ __launch_bounds__(kThreads) void kv_append_heads_kernel(HeadRows k, H
   for (int e = 0; e < W; ++e) z[e] = u[e], z[W + e] = w[e];
   const uint32_t vw = quantize<2 * W>(z, code);
   if (mine && sub == 0) *(uint32_t*)(block + 32 * D + 128 + t * 4) = vw;
+  if (busy) {
 #pragma unroll
-  for (int e = 0; e < 2 * W; e += 4)
-    codes[t * kPitch + (2 * W * sub + e) / 4] =
-        code[e] | code[e + 1] << 8 | code[e + 2] << 16 | code[e + 3] << 24;
+    for (int e = 0; e < 2 * W; e += 4)
+      codes[t * kPitch + (2 * W * sub + e) / 4] =
+          code[e] | code[e + 1] << 8 | code[e + 2] << 16 | code[e + 3] << 24;
+  }
   lds_barrier();
   if (!mask) return;
 #pragma unroll
@@ -462,20 +477,13 @@ hipError_t gather(const HeadRows& k, const HeadRows& v, const KvArgs& a, hipStre
 hipError_t launch_kv_append(const HeadRows& k, const HeadRows& v, const RopeArgs& rope,
                             const KvArgs& a, hipStream_t s) {
   const bool vec = on16(k) && on16(v);
-  const bool whole = !rope.cos || (rope.dim == a.D && ((uintptr_t)rope.cos & 15) == 0 &&
-                                   ((uintptr_t)rope.sin & 15) == 0);
-  if (vec && whole && a.D % 64 == 0) {
-#define BTQ_CALL(N) \
-  (k.type == kF32 ? append_heads<N, kF32>(k, v, rope, a, s) : append_heads<N, kBf16>(k, v, rope, a, s))
-    switch (a.D) {
-      case 64: return BTQ_CALL(64);
-      case 128: return BTQ_CALL(128);
-      case 192: return BTQ_CALL(192);
-      default: return BTQ_CALL(256);
-    }
-#undef BTQ_CALL
-  }
-#define BTQ_CALL(N) (vec ? append<N, true>(k, v, rope, a, s) : append<N, false>(k, v, rope, a, s))
+  const bool table = !rope.cos || (((uintptr_t)rope.cos & 15) == 0 && ((uintptr_t)rope.sin & 15) == 0);
+  // turned features have to be those of whole lanes
+#define BTQ_CALL(N)                                                                        \
+  (vec && table && (!rope.cos || rope.dim % (2 * HeadLanes<N>::W) == 0)                    \
+       ? (k.type == kF32 ? append_heads<N, kF32>(k, v, rope, a, s)                         \
+                         : append_heads<N, kBf16>(k, v, rope, a, s))                       \
+       : (vec ? append<N, true>(k, v, rope, a, s) : append<N, false>(k, v, rope, a, s)))
   BTQ_FOR_HEAD(a.D, BTQ_CALL)
 #undef BTQ_CALL
 }

@@ -116,6 +116,16 @@ def test_rotations_and_types(dt, dim):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_part_of_a_head_turned(D):
+    say(f"case: kv append part turned D={D}")
+    for style in ("half", "pairs"):
+        for dim in (D // 4, D // 2, 3 * D // 4):
+            check(BATCHES[6], 1, 2, D, dim=dim, style=style, dt=BF16, fused=False)
+            check(BATCHES[7], 1, 1, D, dim=dim, style=style, dt=F32, fused=False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shift", [0, 1, 2, 3, 4, 8])
 def test_rows_on_any_element(shift):
     for dt in (BF16, F32):
