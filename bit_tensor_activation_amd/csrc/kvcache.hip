@@ -133,11 +133,9 @@ __device__ __forceinline__ uint32_t quantize(const float (&x)[E], uint32_t (&cod
 // number of turned features that whole lanes have.
 // P=8, 16384 tokens, half of them turned: D = 128 55 -> 22 us by the general kernel and here,
 // 96 45 -> 20.
-template <int D>
-struct HeadLanes {
-  static constexpr int W = D % 64 == 0 ? D / 16 : D == 32 ? 4 : D == 96 ? 8 : 16;
-  static constexpr int kLanes = D / (2 * W);
-};
+// (D = 192 takes 8 lanes of 24 features or 6 of 32: all of a head turned 31 against 42 us,
+// 64 features of it, which only the second form takes, 41 and 98 by the general kernel.)
+constexpr int head_run(int D) { return D % 64 == 0 ? D / 16 : D == 32 ? 4 : D == 96 ? 8 : 16; }
 template <int W, int kType>
 __device__ __forceinline__ void load_run(const void* base, int64_t first, float (&x)[W]) {
 #pragma unroll
@@ -157,11 +155,11 @@ __device__ __forceinline__ void load_run(const void* base, int64_t first, float 
   }
 }
 
-template <int D, int kType>
+template <int D, int W, int kType>
 __global__ __launch_bounds__(kThreads) void kv_append_heads_kernel(HeadRows k, HeadRows v,
                                                                    RopeArgs rope, KvArgs a,
                                                                    uint32_t first_item) {
-  constexpr int W = HeadLanes<D>::W, kLanes = HeadLanes<D>::kLanes, kPitch = D / 4 + 1;
+  constexpr int kLanes = D / (2 * W), kPitch = D / 4 + 1;
   __shared__ uint32_t codes[kBlockTokens * kPitch];
   const int64_t shard = blockIdx.y, item = first_item + blockIdx.z;
   const int head = blockIdx.x;
@@ -451,11 +449,14 @@ hipError_t each_launch(const KvArgs& a, F f) {
     default: return CALL(256);           \
   }
 
-template <int D, int kType>
+template <int D, int W>
 hipError_t append_heads(const HeadRows& k, const HeadRows& v, const RopeArgs& rope, const KvArgs& a,
                         hipStream_t s) {
   return each_launch(a, [&](dim3 grid, uint32_t first) {
-    kv_append_heads_kernel<D, kType><<<grid, kThreads, 0, s>>>(k, v, rope, a, first);
+    if (k.type == kF32)
+      kv_append_heads_kernel<D, W, kF32><<<grid, kThreads, 0, s>>>(k, v, rope, a, first);
+    else
+      kv_append_heads_kernel<D, W, kBf16><<<grid, kThreads, 0, s>>>(k, v, rope, a, first);
   });
 }
 template <int D, bool kVector>
@@ -477,13 +478,14 @@ hipError_t gather(const HeadRows& k, const HeadRows& v, const KvArgs& a, hipStre
 hipError_t launch_kv_append(const HeadRows& k, const HeadRows& v, const RopeArgs& rope,
                             const KvArgs& a, hipStream_t s) {
   const bool vec = on16(k) && on16(v);
-  const bool table = !rope.cos || (((uintptr_t)rope.cos & 15) == 0 && ((uintptr_t)rope.sin & 15) == 0);
-  // turned features have to be those of whole lanes
-#define BTQ_CALL(N)                                                                        \
-  (vec && table && (!rope.cos || rope.dim % (2 * HeadLanes<N>::W) == 0)                    \
-       ? (k.type == kF32 ? append_heads<N, kF32>(k, v, rope, a, s)                         \
-                         : append_heads<N, kBf16>(k, v, rope, a, s))                       \
-       : (vec ? append<N, true>(k, v, rope, a, s) : append<N, false>(k, v, rope, a, s)))
+  const bool on = vec && (!rope.cos || (((uintptr_t)rope.cos & 15) == 0 && ((uintptr_t)rope.sin & 15) == 0));
+  // runs of W features take turned ones that are those of whole lanes
+  auto runs = [&](int W) { return on && (!rope.cos || rope.dim % (2 * W) == 0); };
+  if (a.D == 192 && !runs(head_run(192)) && runs(16)) return append_heads<192, 16>(k, v, rope, a, s);
+#define BTQ_CALL(N)                                                      \
+  (runs(head_run(N)) ? append_heads<N, head_run(N)>(k, v, rope, a, s)    \
+   : vec             ? append<N, true>(k, v, rope, a, s)                 \
+                     : append<N, false>(k, v, rope, a, s))
   BTQ_FOR_HEAD(a.D, BTQ_CALL)
 #undef BTQ_CALL
 }
