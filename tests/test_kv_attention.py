@@ -115,6 +115,16 @@ def test_split_keys(length):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160])
+def test_few_columns_on_average(D):
+    # groups of 8 columns, several of them in some sequences and rows of two in some
+    for Hq in (1, 3, 4):
+        b = Batch([9, 1, 0, 1, 2, 1, 1, 1, 1, 1, 0, 1, 0], [300, 1, 7, 129, 64, 513, 33, 2, 96, 700, 3, 40, 0], page=64)
+        check(b, 2, Hq, 1, D, dt=F32)
+        check(b, 1, 2 * Hq, 2, D, window=70, causal=Hq != 3)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
 def test_shares_of_long_keys(D):
     # equal shares of the keys, few columns and more than one group of them
