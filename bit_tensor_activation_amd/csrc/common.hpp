@@ -440,6 +440,7 @@ __device__ __forceinline__ int find_sequence(const KvArgs& a, int mul, int shift
     hi = min(hi, lo + step);
     if (step == 1) {
       *sub = item - (((int64_t)__builtin_amdgcn_readlane(start, n - 1) * mul + (int64_t)lo * extra) >> shift);
+      if (*sub < 0) return -1;   // lane n - 1 is none of those counted: starts do not ascend
       *range = cut_range(a, __builtin_amdgcn_readlane(start, n - 1),
                          __builtin_amdgcn_readlane(next, n - 1),
                          __builtin_amdgcn_readlane(length, n - 1));

@@ -456,6 +456,34 @@ def test_many_columns_captured():
         assert torch.equal(out, eager), n
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("starts", [[0, 8, 8, 0, 1, 2, 3, 4, 5], [8, 7, 6, 5, 4, 3, 2, 1, 0],
+                                    [5, -9, 700, 3, -2 ** 31, 2 ** 31 - 1, 8, 0, 2]])
+def test_starts_that_do_not_ascend_stay_inside_the_tensors(starts):
+    # the results are unspecified, the guards before and behind them are not (the item
+    # search itself is tested in test_item_search.py)
+    say(f"case: kv attention starts {starts}")
+    # columns of 8 and of 16 in whole groups, equal shares, and many columns in one
+    # piece and in several
+    for T, Hq, D, length, ml in ((8, 8, 64, 300, 300), (8, 8, 160, 300, 300), (8, 4, 64, 5000, 0),
+                                 (130, 8, 64, 300, 300), (300, 8, 128, 5000, 0)):
+        b = Batch([T], [length], page=64)
+        n = len(starts) - 1
+        tb = torch.from_numpy(np.repeat(b.table, n, 0)).to(DEV)
+        lengths = torch.full((n,), length, dtype=torch.int32, device=DEV)
+        cache = torch.from_numpy(random_cache(b, 1, 1, D)).to(DEV)
+        q = torch.randn((1, T, Hq, D), device=DEV).to(BF16)
+        st = torch.tensor(starts, dtype=torch.int32, device=DEV)
+        room = 1 << 20
+        out = torch.full((2 * room + T * Hq * D,), 5.0, device=DEV)
+        lse = torch.full((2 * room + T * Hq,), 5.0, device=DEV)
+        B.btq_kv_attention(q, st, lengths, tb, cache, max_length=ml,
+                           out=out[room:-room].view(1, T, Hq * D), lse=lse[room:-room].view(1, T, Hq))
+        torch.cuda.synchronize()
+        for x in (out, lse):
+            assert (x[:room] == 5).all() and (x[-room:] == 5).all()
+
+
 # ---- CPU: all return before any HIP call ---------------------------------------
 
 A = 0x10000
