@@ -299,6 +299,11 @@ struct RopeArgs {
   int64_t rows;
   int dim, style;           // btq_rope
 };
+// Whether the tables have a row for a position. cos and sin of one that they have not
+// are NaN, so that nothing computed from it passes for a result.
+__device__ __forceinline__ bool in_table(const RopeArgs& r, int64_t pos) {
+  return pos >= 0 && pos < r.rows;
+}
 
 struct HeadArgs {
   HeadRows x, y;

@@ -30,12 +30,6 @@ __device__ __forceinline__ const float* head_weight(const HeadArgs& a, int64_t p
   return a.k_weight ? a.k_weight + p * a.kw_shard + (h - a.Hq) * a.kw_head : nullptr;
 }
 
-// cos and sin of a token whose position is past the table: NaN, so that nothing
-// computed from it passes for a result.
-__device__ __forceinline__ bool in_table(const RopeArgs& r, int pos) {
-  return pos >= 0 && pos < r.rows;
-}
-
 // ---- general kernel: any size, stride and alignment; a wave a head, which reads it
 // again for each sum (from L1) ----
 __device__ __forceinline__ float wave_sum(float x) {

@@ -178,7 +178,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_heads_kernel(HeadRows k, H
   load_run<W, kType>(k.p, kb + f0, x);
   load_run<W, kType>(k.p, kb + f1, y);
   const int64_t pos = at.first + (token ? t : at.from);
-  const bool known = pos < rope.rows;
+  // (the place of a row that is dropped may be negative: its loads come before that is known)
+  const bool known = in_table(rope, pos);
   if (turn) {
     const int64_t e = (known ? pos : 0) * (rope.dim / 2) + W * sub;
     load_run<W, kF32>(rope.cos, e, c);
@@ -305,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(HeadRows k, HeadRow
     if (rope.cos) {
       const int half = rope.dim / 2;
       const int64_t pos = at.first + t;
-      const bool known = pos < rope.rows;
+      const bool known = in_table(rope, pos);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int i = f0 + e;

@@ -182,6 +182,16 @@ def test_places_without_a_page_and_before_the_sequence():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,dim", [(128, 128), (128, 10), (192, 64)])
+def test_rows_before_the_sequence_with_tables(D, dim):
+    # far more rows than places: the others' places are negative, and their rows of the
+    # tables are none (nothing before the tables is read)
+    b = Batch([700, 90], [12, 40], page=32)
+    check(b, 1, 2, D, dim=dim)
+    check(b, 1, 1, D, dim=dim, style="pairs", dt=F32, rows=5)
+
+
+@pytest.mark.gpu
 def test_positions_past_the_table_are_nan():
     check(Batch([6], [40]), 1, 1, 64, dim=32, rows=37)
 
