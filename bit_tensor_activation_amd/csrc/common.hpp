@@ -415,7 +415,7 @@ __device__ __forceinline__ SeqRange uniform(const SeqRange& s) {
 }
 
 // Work items lie sequence after sequence. An item covers 2^shift of a sequence's
-// rows*mul, and b's begin at floor((starts[b]*mul + b*extra) / 2^shift). That leaves
+// rows*mul, and b's begin at floor((begin*mul + b*extra) / 2^shift). That leaves
 // each sequence as many as it needs with extra 2^shift less the largest power of 2 up to
 // 2^shift that divides mul (part_extra), for parts that begin at the first row, and with
 // 2*2^shift for parts that begin at a multiple of 2^shift in the sequence. The grid then
@@ -437,7 +437,8 @@ __device__ __forceinline__ int find_sequence(const KvArgs& a, int mul, int shift
     const int step = (hi - lo + 63) >> 6;
     const int b = lo + lane * step;
     const int at = min(b, a.B - 1);
-    const int start = a.starts[at], next = a.starts[at + 1], length = a.lengths[at];
+    // (cut as cut_range does, so that items are numbered by the rows that there are)
+    const int start = clamp_int(a.starts[at], 0, (int)a.T), next = a.starts[at + 1], length = a.lengths[at];
     const int64_t first = ((int64_t)start * mul + (int64_t)b * extra) >> shift;
     const int n = __popcll(__ballot(b < hi && first <= item));
     if (n == 0) return -1;

@@ -504,8 +504,9 @@ int btq_block_norm(const void *y, int y_type, const void *residual, int r_type,
  *    places are not in the cache. The table's places, max_pages*page_size, may be
  *    2^30 at most.
  *  - These arrays are read on the device. Whatever they hold, no call touches
- *    memory outside its tensors (starts are cut to [0,T], lengths to the table's
- *    places); where starts do not ascend, the results are unspecified.
+ *    memory outside its tensors. Starts are cut to [0,T] and lengths to the table's
+ *    places, and rows and places follow from the cut ones; where starts do not
+ *    ascend, the results are unspecified.
  *  - cache u8 [P,pages,Hk,page_size/32,btq_kv_block_bytes(D)], 16-byte aligned;
  *    page_size a power of 2 from 32 to 65536, D a multiple of 32 up to 256.
  *    A block holds 32 tokens of a key head:

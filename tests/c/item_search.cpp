@@ -166,7 +166,7 @@ void check(std::vector<int32_t> starts, std::vector<int32_t> lengths, int T, int
 }  // namespace
 
 int main(int argc, char** argv) {
-  const bool any_order = argc > 1 && argv[1][0] == 'a';
+  const bool any_order = argc > 1 && argv[1][0] == 'u';
   std::mt19937 g(7);
   if (any_order) check({0, 8, 8, 0, 1, 2, 3, 4, 5}, std::vector<int32_t>(8, 9), 8, 8, false);
   for (int i = 0; i < 150; ++i) {

@@ -34,4 +34,9 @@ def search(tmp_path_factory):
 
 
 def test_items_stay_inside_the_batch_whatever_the_starts_hold(search):
-    search("any order")
+    search("unordered")
+
+
+def test_every_row_of_ascending_starts_has_one_item(search):
+    # starts before 0 and past T among them, which are cut to the batch
+    search("sorted")

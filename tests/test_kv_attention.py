@@ -484,6 +484,30 @@ def test_starts_that_do_not_ascend_stay_inside_the_tensors(starts):
             assert (x[:room] == 5).all() and (x[-room:] == 5).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("first,last", [(-5, 4), (-2 ** 31, 0), (-40, 2 ** 30)])
+def test_starts_outside_the_batch_are_cut(first, last):
+    # the same rows as with starts cut to [0,T], by each kernel (as in the test above)
+    for new, Hq, D, length, ml in (([3, 2, 3], 1, 64, 300, 300), ([3, 2, 3], 16, 160, 300, 300),
+                                   ([3, 2, 3], 4, 64, 5000, 0), ([30, 90, 10], 8, 64, 300, 300),
+                                   ([100, 30, 170], 8, 128, 5000, 0)):
+        b = Batch(new, [length, length - 7, 200], page=64)
+        starts, lengths, tb = b.dev()
+        cache = torch.from_numpy(random_cache(b, 1, 1, D)).to(DEV)
+        q = torch.randn((1, b.T, Hq, D), device=DEV).to(BF16)
+        wide = starts.clone()
+        wide[0] = first
+        wide[-1] += last
+        got = []
+        for st in (starts, wide):
+            out = torch.full((1, b.T, Hq * D), 5.0, device=DEV)
+            lse = torch.full((1, b.T, Hq), 5.0, device=DEV)
+            B.btq_kv_attention(q, st, lengths, tb, cache, max_length=ml, out=out, lse=lse)
+            got.append((out, lse))
+        assert not (got[0][0] == 5).any()
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 # ---- CPU: all return before any HIP call ---------------------------------------
 
 A = 0x10000

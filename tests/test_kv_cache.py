@@ -259,6 +259,25 @@ def test_gather_of_one_and_of_any_stretch():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("first,last", [(-5, 4), (-2 ** 31, 0), (0, 3), (-40, 2 ** 31 - 11 - 70)])
+def test_starts_outside_the_batch_are_cut(first, last):
+    # the same bytes and rows as with starts cut to [0,T]
+    b = Batch([40, 30, 5], [90, 30, 5], page=32)
+    starts, lengths, tb = b.dev()
+    x = torch.randn((2, b.T, 2, 64), device=DEV).to(BF16)
+    wide = starts.clone()
+    wide[0] = first
+    wide[-1] += last
+    held = []
+    for st in (starts, wide):
+        cache = torch.zeros((2, b.pages, 1, 1, block_bytes(64)), dtype=torch.uint8, device=DEV)
+        B.btq_kv_append(x[:, :, :1], x[:, :, 1:], st, lengths, tb, cache)
+        held.append((cache, *B.btq_kv_gather(st, lengths, tb, cache, tokens=b.T)))
+    for got, want in zip(held[1], held[0]):
+        assert want.any() and torch.equal(got, want)
+
+
+@pytest.mark.gpu
 def test_no_shards_and_empty_batches():
     b = Batch([40], [40])
     x = torch.randn((40, 4, 64), device=DEV).to(BF16)
