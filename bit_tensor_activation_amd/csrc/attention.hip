@@ -104,6 +104,14 @@ __device__ __forceinline__ float column_sum(float v) {
   return column_combine(v, [](float a, float b) { return a + b; });
 }
 
+// Keys of a wave behind which it takes 128 + z off the sums. Those hold up to 143 for a
+// value of some steps, and every instruction rounds the whole of it: taken off at the end
+// only, the error grew with a wave's keys, to 3.1e-2 of a row at 131072 of them. 3e-4 of a
+// row, whatever their number, is what is left (the weights' rounding makes 1.7e-3). It costs
+// the columns' kernel 2 to 3% at D = 128 (2048 new tokens over 32768: 2330 -> 2395 us; as much
+// with 8 times as many keys, so it is not the subtractions), others up to 2% at D = 256.
+constexpr int kOffsetKeys = 1024;
+
 // Keeps a uniform branch a branch: without it the compiler turns short ones into
 // selects that every pass pays for.
 __device__ __forceinline__ void keep_branch() { asm volatile(""); }
@@ -186,6 +194,15 @@ struct Columns {
       for (int d = 0; d < ND; ++d) o[n][d] = v4f{0, 0, 0, 0};
       m2[n] = kNegInf;
       l[n] = 0.0f;
+    }
+  }
+  // Takes the zero points off what is summed so far (kOffsetKeys).
+  __device__ __forceinline__ void take_off() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[n][d] -= oz[n];
+      oz[n] = v4f{0, 0, 0, 0};
     }
   }
   // (a column that does not exist repeats the first one; its results go nowhere)
@@ -412,7 +429,12 @@ struct KeysWave {
     }
     // whether columns see different keys
     const int uneven = c.all_lo > c.any_lo || c.all_hi < c.any_hi ? 2 : 0;
+    int done = 0;
     for (int tile = begin; tile < end; tile += step) {
+      if (++done % (kOffsetKeys / kTile) == 0) {
+        keep_branch();
+        c.take_off();
+      }
       const int key0 = tile * kTile;
       const bool full = key0 >= c.all_lo && key0 + kTile <= c.all_hi && __ballot(!there) == 0;
       place(tile + step, end, cl / 4, pk, &kat);
@@ -1205,6 +1227,10 @@ __global__ __launch_bounds__(256, 2) void attention_columns_kernel(AttnArgs a, u
     const int blocks = uniform(buf[even].there[0] | buf[even].there[1] << 1);
     const bool full = blocks == 3 && key0 >= c.all_lo && key0 + kColsTile <= c.all_hi;
     compute(buf[even], buf[even ^ 1], key0, blocks << 1 | (full ? 0 : 1));
+    if ((tile - kt.begin + 1) % (kOffsetKeys / kColsTile) == 0) {
+      keep_branch();
+      c.take_off();
+    }
     load(tile + 2);
     lds_barrier();
   }
