@@ -356,6 +356,26 @@ int check_head_rows(int64_t P, int64_t T, int64_t H, int64_t D, int64_t shard, i
   return D > most ? BTQ_ERR_SHAPE : BTQ_OK;
 }
 
+// Heads that a call writes, too: no element may belong to two of them, or lanes would
+// write it in no order. From the smallest stride on, each is at least what those before
+// it span.
+int check_out_rows(int64_t P, int64_t T, int64_t H, int64_t D, int64_t shard, int64_t pitch,
+                   int64_t head) {
+  const int st = check_head_rows(P, T, H, D, shard, pitch, head);
+  if (st != BTQ_OK) return st;
+  int64_t stride[3] = {head, pitch, shard}, count[3] = {H, T, P}, span = D;
+  for (int i = 0; i < 3; ++i) {
+    int least = i;
+    for (int j = i + 1; j < 3; ++j)
+      if (count[j] > 1 && (count[least] <= 1 || stride[j] < stride[least])) least = j;
+    if (count[least] <= 1) return BTQ_OK;
+    if (stride[least] < span) return BTQ_ERR_SHAPE;
+    span += stride[least] * (count[least] - 1);
+    stride[least] = stride[i], count[least] = count[i];
+  }
+  return BTQ_OK;
+}
+
 int check_rope(const float* cos, const float* sin, int64_t rows, int64_t dim, int64_t D, int rope) {
   if (rope != BTQ_ROPE_HALF && rope != BTQ_ROPE_PAIRS) return BTQ_ERR_ARG;
   if (!cos != !sin) return BTQ_ERR_ARG;
@@ -534,7 +554,7 @@ int btq_head_norm_rope(const void* x, int x_type, int64_t x_shard, int64_t x_pit
   const int64_t H = q_heads + k_heads;
   int st = check_dims(P, T, H * D, 0);
   if (st == BTQ_OK) st = check_head_rows(P, T, H, D, x_shard, x_pitch, x_head);
-  if (st == BTQ_OK) st = check_head_rows(P, T, H, D, y_shard, y_pitch, y_head);
+  if (st == BTQ_OK) st = check_out_rows(P, T, H, D, y_shard, y_pitch, y_head);
   if (st == BTQ_OK) st = check_head_rows(P, 1, H, D, qw_shard, 0, qw_head);
   if (st == BTQ_OK) st = check_head_rows(P, 1, H, D, kw_shard, 0, kw_head);
   if (st == BTQ_OK) st = check_rope(cos_table, sin_table, rope_rows, rope_dim, D, rope);
@@ -587,8 +607,12 @@ int btq_kv_gather(const int32_t* seq_starts, const int32_t* lengths, int64_t B,
                   int64_t v_shard, int64_t v_pitch, int64_t v_head, void* stream) {
   int st = check_kv(P, T, Hk, D, seq_starts, lengths, B, page_table, max_pages, cache, pages,
                     page_size);
-  if (st == BTQ_OK) st = check_head_rows(P, T, Hk, D, k_shard, k_pitch, k_head);
-  if (st == BTQ_OK) st = check_head_rows(P, T, Hk, D, v_shard, v_pitch, v_head);
+  if (st == BTQ_OK)
+    st = k ? check_out_rows(P, T, Hk, D, k_shard, k_pitch, k_head)
+           : check_head_rows(P, T, Hk, D, k_shard, k_pitch, k_head);
+  if (st == BTQ_OK)
+    st = v ? check_out_rows(P, T, Hk, D, v_shard, v_pitch, v_head)
+           : check_head_rows(P, T, Hk, D, v_shard, v_pitch, v_head);
   if (st != BTQ_OK) return st;
   if (!value_type(y_type) || (T > 0 && B > 0 && !k && !v)) return BTQ_ERR_ARG;
   if (!aligned(k, value_align(y_type)) || !aligned(v, value_align(y_type))) return BTQ_ERR_ALIGN;

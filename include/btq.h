@@ -492,7 +492,8 @@ int btq_block_norm(const void *y, int y_type, const void *residual, int r_type,
  * Extra conventions of these calls
  *  - Heads: x[p,t,h,:] starts at element p*x_shard + t*x_pitch + h*x_head and its
  *    D features are contiguous, so the heads of a fused projection's rows are
- *    taken where they lie. Strides are >= 0.
+ *    taken where they lie. Strides are >= 0. Those of an output leave no element to
+ *    two heads: each (of a size above 1) is at least what the smaller ones span.
  *  - A batch is B sequences one after another: the rows of sequence b are
  *    seq_starts[b] <= t < seq_starts[b+1] (i32 [B+1], ascending), lengths[b] (i32
  *    [B]) is the number of its tokens in the cache WITH those rows, so row t has

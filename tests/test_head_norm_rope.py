@@ -223,6 +223,19 @@ def test_python_refusals():
         B.btq_head_norm_rope(x, 2, eps=-1.0)
 
 
+@pytest.mark.gpu
+def test_outputs_whose_heads_overlap_are_refused():
+    x = torch.zeros((2, 4, 3, 64), device=DEV, dtype=BF16)
+    y = torch.zeros((2, 4, 3, 64), device=DEV, dtype=BF16)
+    for out in (y[:, :, :1].expand(2, 4, 3, 64), y[:, :1].expand(2, 4, 3, 64), y[:1].expand(2, 4, 3, 64),
+                y.as_strided((2, 4, 3, 64), (768, 192, 32, 1))):
+        with pytest.raises(RuntimeError):
+            B.btq_head_norm_rope(x, 2, out=out)
+    # an input may be expanded, and an output may lie in any order
+    turned = torch.zeros((3, 2, 4, 80), device=DEV, dtype=BF16).permute(1, 2, 0, 3)[..., :64]
+    B.btq_head_norm_rope(x[:, :, :1].expand(2, 4, 3, 64), 2, out=turned)
+
+
 # ---- CPU: all return before any HIP call ---------------------------------------
 
 A = 0x10000
@@ -252,3 +265,19 @@ def test_refusals():
     for kw in (dict(x=A + 1), dict(y=A + 1), dict(xt=0, x=A + 2), dict(pos=A + 2), dict(cos=A + 2),
                dict(sin=A + 1), dict(qw=A + 2), dict(kw=A + 1)):
         assert call(**kw) == ALIGN, kw
+
+
+def test_overlapping_outputs():
+    SHAPE = _lib.BTQ_ERR_SHAPE
+    # (inputs of the same strides are taken: they get as far as the null pointer)
+    for n in (dict(s=0, p=384, h=128), dict(s=1536, p=0, h=128), dict(s=1536, p=384, h=0),
+              dict(s=1536, p=384, h=127), dict(s=1536, p=383, h=128), dict(s=1535, p=384, h=128),
+              dict(s=128, p=256, h=1023), dict(s=0, p=0, h=0)):
+        assert call(P=2, xs=1536, ys=n["s"], yp=n["p"], yh=n["h"]) == SHAPE, n
+        assert call(P=2, xs=n["s"], xp=n["p"], xh=n["h"], ys=1536, x=None) == _lib.BTQ_ERR_ARG, n
+    for n in (dict(s=1536, p=384, h=128), dict(s=128, p=256, h=1024), dict(s=512, p=128, h=1024),
+              dict(s=1 << 40, p=1 << 30, h=1 << 20)):
+        assert call(P=2, xs=1536, ys=n["s"], yp=n["p"], yh=n["h"], y=None) == _lib.BTQ_ERR_ARG, n
+    # strides of an axis of one do not count
+    assert call(T=1, yp=0, y=None) == _lib.BTQ_ERR_ARG
+    assert call(qh=1, kh=0, yh=0, yp=128, y=None) == _lib.BTQ_ERR_ARG

@@ -380,3 +380,13 @@ def test_gather_refusals():
         assert gather(**kw) == ARG, kw
     for kw in (dict(k=A + 1), dict(v=A + 1), dict(yt=0, v=A + 2), dict(cache=A + 4)):
         assert gather(**kw) == ALIGN, kw
+
+
+def test_gather_into_overlapping_heads():
+    for kw in (dict(kh=0), dict(kp=0), dict(vh=127), dict(vp=255), dict(P=2, ks=0, vs=1024),
+               dict(P=2, ks=1024, vs=0)):
+        assert gather(**kw) == SHAPE, kw
+        assert append(**kw, k=None) == ARG, kw          # the same strides of inputs
+    assert gather(k=None, v=None, kh=0, vh=0) == ARG
+    assert gather(k=None, ks=0, kp=0, kh=0, v=A + 1) == ALIGN    # (one that is not written)
+    assert gather(T=1, kp=0, vp=0, k=A + 1) == ALIGN
