@@ -609,8 +609,10 @@ int btq_kv_gather(const int32_t *seq_starts, const int32_t *lengths, int64_t B,
  * bf16 for the second product. NaN or Inf in a query gives NaN; a NaN key or value
  * gives NaN to the queries that see it and to no others.
  * With many queries a sequence, those of up to 128 (query, head) pairs are held as fp16
- * relative to the largest of them: exact down to 2^-27 of it. With queries of up to 2^100
- * and scale up to 2^30 nothing overflows where the scores do not.
+ * relative to the largest of them: exact down to 2^-27 of it. With queries of up to 2^100,
+ * scale up to 2^30 and values of up to 2^80 nothing overflows where q.k and the scores do
+ * not, whatever the number of keys. Larger values may give NaN: the sums on the way hold up to
+ * 2^8*(143*1024 + 15*keys) steps of a value's scale.
  *   q         bf16 [P,T,Hq,D] in; fastest with heads on 16 bytes
  *   scale     > 0, at most 2^127
  *   max_length  an upper bound of lengths (0: the table's places) by which the

@@ -248,6 +248,38 @@ def test_maximum_that_rises_late():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("power", [-100, 79])
+def test_values_of_any_size(power):
+    # scales of values times a power of 2, by every kernel: the same rows times that, to the bit.
+    # The first 1024 keys, with which every wave of a block begins, score 7 powers of 2 below
+    # the others, which the maximum does not follow: their weights are near 2^7. (Values of
+    # 4*2^79 are beyond the 2^80 that is promised.)
+    for b, Hq, D in ((Batch([1, 1], [2000, 700], page=64), 4, 64), (Batch([1, 1], [2000, 700], page=64), 4, 160),
+                     (Batch([1], [9000], page=64), 5, 64), (Batch([64], [1900], page=64), 8, 64),
+                     (Batch([64], [1900], page=64), 8, 160)):
+        cache = random_cache(b, 1, 1, D)
+        words = cache[..., 32 * D:].view(np.uint32)
+        words[..., :32] = 0x3f804300                       # keys: scale 1, z 0
+        codes = cache[..., :16 * D]
+        codes[:] = 0x11                                    # of ones
+        for s in range(b.B):
+            for j in range(min(1024, b.lengths[s])):
+                page, block, t = b.where(s, j)
+                codes[0, page, 0, block, t * D // 2:(t + 1) * D // 2] = 0
+        starts, lengths, tb = b.dev()
+        q = torch.full((1, b.T, Hq, D), 7 / D / 1.4426950408889634, device=DEV).to(BF16)
+        got = []
+        for n in (0, power):
+            words[..., 32:] += np.uint32((n << 23) & 0xffffffff)
+            lse = torch.empty((1, b.T, Hq), device=DEV)
+            out = B.btq_kv_attention(q, starts, lengths, tb, torch.from_numpy(cache).to(DEV), scale=1.0,
+                                     out_dtype=F32, lse=lse)
+            got.append((out, lse))
+        assert torch.isfinite(got[1][0]).all() and (got[0][0].abs() > 2.0 ** -9).any()
+        assert torch.equal(got[1][0], got[0][0] * 2.0 ** power) and torch.equal(got[1][1], got[0][1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shift,gap", [(0, 0), (1, 0), (3, 5), (8, 64), (0, 3)])
 def test_query_strides_and_alignment(shift, gap):
     check(BATCHES[7], 2, 4, 2, 64, shift=shift, gap=gap)
