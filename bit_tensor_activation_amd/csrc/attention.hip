@@ -851,7 +851,8 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
   constexpr int C = 16, kVec = D / 4;
   constexpr int kSpan = C / 4;                                       // columns of a block
   constexpr int kItems = kSpan * kVec;
-  constexpr int kTeams = kItems >= kJoinThreads ? 1 : kJoinThreads / kItems;
+  constexpr int kTeams = kJoinThreads / kItems;
+  static_assert(kTeams >= 2, "threads");
   __shared__ v4f sums[kTeams][kItems];
   __shared__ float stat[kTeams][kItems][2];
   const Cut cut = cuts<D, C>(a)[blockIdx.x];
@@ -860,73 +861,67 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
   const int cols = seq.n * a.G, first = blockIdx.y * kSpan, col0 = (cut.group << 4) + first;
   if (col0 >= cols) return;
   const int64_t slots = 2 * kStreamBlocks;
-  for (int i = threadIdx.x % (kTeams == 1 ? kJoinThreads : kItems); i < kItems;
-       i += kTeams == 1 ? kJoinThreads : kItems) {
-    const int team = kTeams == 1 ? 0 : threadIdx.x / kItems;
-    const int c = i / kVec, d = (i - c * kVec) * 4;
-    const bool live = team < kTeams && col0 + c < cols;
-    // relative to a running maximum, 8 blocks at a time
-    float m = kNegInf, l = 0.0f;
-    v4f x = {0, 0, 0, 0};
-    if (live) {
-      const int span = (cut.parts + kTeams - 1) / kTeams, end = min((team + 1) * span, cut.parts);
-      for (int p0 = team * span; p0 < end; p0 += 8) {
-        float ms[8], ls[8];
-        v4f ys[8];
+  // (threads behind the last whole team have no part)
+  const int team = threadIdx.x / kItems, i = threadIdx.x - team * kItems;
+  const int c = i / kVec, d = (i - c * kVec) * 4;
+  const bool live = team < kTeams && col0 + c < cols;
+  // relative to a running maximum, 8 blocks at a time
+  float m = kNegInf, l = 0.0f;
+  v4f x = {0, 0, 0, 0};
+  if (live) {
+    const int span = (cut.parts + kTeams - 1) / kTeams, end = min((team + 1) * span, cut.parts);
+    for (int p0 = team * span; p0 < end; p0 += 8) {
+      float ms[8], ls[8];
+      v4f ys[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int p = min(p0 + j, end - 1);
-          const Partial q = partial(a, 2 * ((int64_t)blockIdx.x + p) + (p == 0), slots, C, D);
-          const float2 st = *(const float2*)(q.stats + 2 * (first + c));
-          ms[j] = p0 + j < end ? st.x : kNegInf;
-          ls[j] = p0 + j < end ? st.y : 0.0f;
-          ys[j] = *(const v4f*)(q.sums + (int64_t)(first + c) * D + d);
-        }
-        float top = m;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, ms[j]);
-        float f = share(m, l, top);
-        l *= f;
-        x *= f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          f = share(ms[j], ls[j], top);
-          l += ls[j] * f;
-          if (p0 + j < end) x += ys[j] * f;
-        }
-        m = top;
+      for (int j = 0; j < 8; ++j) {
+        const int p = min(p0 + j, end - 1);
+        const Partial q = partial(a, 2 * ((int64_t)blockIdx.x + p) + (p == 0), slots, C, D);
+        const float2 st = *(const float2*)(q.stats + 2 * (first + c));
+        ms[j] = p0 + j < end ? st.x : kNegInf;
+        ls[j] = p0 + j < end ? st.y : 0.0f;
+        ys[j] = *(const v4f*)(q.sums + (int64_t)(first + c) * D + d);
       }
-    }
-    if constexpr (kTeams > 1) {
-      if (team < kTeams) {
-        sums[team][i] = x;
-        stat[team][i][0] = m;
-        stat[team][i][1] = l;
-      }
-      __syncthreads();
-      if (team == 0) {
-        float top = m;
+      float top = m;
 #pragma unroll
-        for (int t = 1; t < kTeams; ++t) top = fmaxf(top, stat[t][i][0]);
-        float f = share(m, l, top);
-        m = top;
-        l *= f;
-        x *= f;
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, ms[j]);
+      float f = share(m, l, top);
+      l *= f;
+      x *= f;
 #pragma unroll
-        for (int t = 1; t < kTeams; ++t) {
-          f = share(stat[t][i][0], stat[t][i][1], top);
-          l += stat[t][i][1] * f;
-          x += sums[t][i] * f;
-        }
+      for (int j = 0; j < 8; ++j) {
+        f = share(ms[j], ls[j], top);
+        l += ls[j] * f;
+        if (p0 + j < end) x += ys[j] * f;
       }
+      m = top;
     }
-    if (live && team == 0) {
-      const int64_t at = out_row(a, seq, cut.hk / a.kv.Hk, (int)(cut.hk % a.kv.Hk), col0 + c);
-      const float r = l == 0.0f ? 0.0f : 1.0f / l;
-      store_out2(a, at * D + d, x[0] * r, x[1] * r);
-      store_out2(a, at * D + d + 2, x[2] * r, x[3] * r);
-      if (a.lse && d == 0) a.lse[at] = lse_of(m, l);
+  }
+  if (team < kTeams) {
+    sums[team][i] = x;
+    stat[team][i][0] = m;
+    stat[team][i][1] = l;
+  }
+  __syncthreads();
+  if (live && team == 0) {
+    float top = m;
+#pragma unroll
+    for (int t = 1; t < kTeams; ++t) top = fmaxf(top, stat[t][i][0]);
+    float f = share(m, l, top);
+    m = top;
+    l *= f;
+    x *= f;
+#pragma unroll
+    for (int t = 1; t < kTeams; ++t) {
+      f = share(stat[t][i][0], stat[t][i][1], top);
+      l += stat[t][i][1] * f;
+      x += sums[t][i] * f;
     }
+    const int64_t at = out_row(a, seq, cut.hk / a.kv.Hk, (int)(cut.hk % a.kv.Hk), col0 + c);
+    const float r = l == 0.0f ? 0.0f : 1.0f / l;
+    store_out2(a, at * D + d, x[0] * r, x[1] * r);
+    store_out2(a, at * D + d + 2, x[2] * r, x[3] * r);
+    if (a.lse && d == 0) a.lse[at] = lse_of(m, l);
   }
 }
 
