@@ -202,6 +202,24 @@ def test_tp_block_with_attention():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cached", [70, 0])
+def test_tp_block_error_of_attention(cached):
+    s = tp_block.prepare(2, 12, 256, 256, 192, 8)
+    tp_block.prepare_attention(s, 3, cached, 1)
+    x = tp_block.attend(s).view(BF16)
+    # Over the cache as it is: activations and weights in 8 bits, of rows of 256 normal values
+    # up to 4.2, are off by 4.2/127/sqrt(12) = 0.0095 each, queries by 0.0135, and so scores
+    # (keys have 1 in the mean square) and rows; three roundings to bf16 add 0.003.
+    err = tp_block.relative_error(x, tp_block.exact_attention(s))
+    # Over the rows before their codes, projection, norm, rotation and places among what is
+    # compared: steps of up to 7/15 for 128 normal values, off by 7/15/sqrt(12) = 0.135, by keys
+    # and by values.
+    rows = tp_block.relative_error(x, tp_block.exact_attention(s, cached=False))
+    say(f"  error of x {err}, against rows {rows}")
+    assert err <= 0.02 and rows <= 0.2
+
+
+@pytest.mark.gpu
 def test_tp_block_command_with_attention():
     r = subprocess.run([sys.executable, os.path.join(ROOT, "tp_block.py"), "--P", "2", "--T", "6", "--H",
                         "256", "--K", "256", "--N", "128", "--k", "8", "--steps", "2", "--cached", "40",

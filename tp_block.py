@@ -22,6 +22,9 @@ through the block. Every shard has K/D query heads and --kv_heads key heads:
       --btq_head_norm_rope--> norm and rotation, in place
       --btq_kv_append--> cache       --btq_kv_attention--> x [P,T,K]
 
+and the script measures x against attention in float64 over what the cache holds, and over
+the keys and values before they were quantized.
+
     python tp_block.py                        # P=8 T=2048 H=4096 K=512 N=2048
     python tp_block.py --T 8 --H 8192 --K 1024 --N 1024
     python tp_block.py --T 32 --H 8192 --K 1024 --N 1024 --cached 2000 --B 32
@@ -105,7 +108,7 @@ def prepare_attention(s: dict, B_: int, cached: int, kv_heads: int, D: int = 128
     s["positions"] = (torch.arange(T, device=dev) % n + cached).int()
     if cached:
         old = torch.arange(0, B_ * cached + 1, cached, device=dev, dtype=torch.int32)
-        kv = rnd(2, P, B_ * cached, kv_heads, D).to(torch.bfloat16)
+        s["kv"] = kv = rnd(2, P, B_ * cached, kv_heads, D).to(torch.bfloat16)
         B.btq_kv_append(kv[0], kv[1], old, torch.full_like(s["lengths"], cached), s["table"],
                         s["cache"])
 
@@ -123,31 +126,47 @@ def attend(s):
                               max_length=s["length"])
 
 
-def exact_attention(s):
-    """x in float64 from the unquantized projection; the keys and values are those
-    that the cache holds."""
+def exact_attention(s, cached: bool = True):
+    """x in float64 from the unquantized projection. The keys and values are those that
+    the cache holds, or, without `cached`, the rows that were put there before they were
+    quantized, those of the new tokens from the projection."""
     P, T, D, Hq, Hk = s["P"], s["T"], s["D"], s["heads"], s["kv_heads"]
-    n, L = T // len(s["lengths"]), s["length"]
-    every = torch.arange(0, len(s["lengths"]) * L + 1, L, device=s["h"].device, dtype=torch.int32)
-    k, v = B.btq_kv_gather(every, s["lengths"], s["table"], s["cache"], tokens=int(every[-1]),
-                           dtype=torch.float32)
+    seqs, L = len(s["lengths"]), s["length"]
+    n = T // seqs
+    c, sn = (s[t][s["positions"].long()].double()[:, None] for t in ("cos", "sin"))
+
+    def project(p, first, heads, weight=None):
+        y = s["h"].double() @ s["w0_exact"][p, first * D:(first + heads) * D].double().t().contiguous()
+        y = y.view(T, heads, D)
+        if weight is None:
+            return y
+        y = y * torch.rsqrt((y * y).mean(-1, keepdim=True) + EPS) * weight.double()
+        a, b = y[..., :D // 2], y[..., D // 2:]
+        return torch.cat((a * c - b * sn, b * c + a * sn), -1)
+
+    def rows(p):
+        """Keys and values [seqs,L,Hk,D]."""
+        new = (project(p, Hq, Hk, s["k_weight"]), project(p, Hq + Hk, Hk))
+        new = [x.view(seqs, n, Hk, D) for x in new]
+        if L == n:
+            return new
+        return [torch.cat((o[p].double().view(seqs, L - n, Hk, D), x), 1) for o, x in zip(s["kv"], new)]
+    if cached:
+        every = torch.arange(0, seqs * L + 1, L, device=s["h"].device, dtype=torch.int32)
+        k, v = (x.view(P, seqs, L, Hk, D) for x in B.btq_kv_gather(
+            every, s["lengths"], s["table"], s["cache"], tokens=seqs * L, dtype=torch.float32))
+    seen = (torch.arange(L, device=s["h"].device) <= torch.arange(L - n, L, device=s["h"].device)[:, None])
     out = []
     for p in range(P):
-        q = s["h"].double() @ s["w0_exact"][p, :Hq * D].double().t().contiguous()
-        q = q.view(T, Hq, D)
-        q = q * torch.rsqrt((q * q).mean(-1, keepdim=True) + EPS) * s["q_weight"].double()
-        c, sn = (s[t][s["positions"].long()].double()[:, None] for t in ("cos", "sin"))
-        a, b = q[..., :D // 2], q[..., D // 2:]
-        q = torch.cat((a * c - b * sn, b * c + a * sn), -1)
-        rows = []
-        for i in range(T // n):
-            seen = (torch.arange(L, device=q.device)
-                    <= torch.arange(L - n, L, device=q.device)[:, None])
+        q = project(p, 0, Hq, s["q_weight"])
+        kp, vp = (k[p].double(), v[p].double()) if cached else rows(p)
+        x = []
+        for i in range(seqs):
             for h in range(Hq):
-                kk, vv = (x[p, i * L:(i + 1) * L, h // (Hq // Hk)].double() for x in (k, v))
+                kk, vv = (u[i, :, h // (Hq // Hk)] for u in (kp, vp))
                 t = q[i * n:(i + 1) * n, h] @ kk.t().contiguous() * D ** -0.5
-                rows.append(torch.softmax(t.masked_fill(~seen, -float("inf")), -1) @ vv)
-        out.append(torch.stack(rows).view(T // n, Hq, n, D).transpose(1, 2).reshape(T, Hq * D))
+                x.append(torch.softmax(t.masked_fill(~seen, -float("inf")), -1) @ vv)
+        out.append(torch.stack(x).view(seqs, Hq, n, D).transpose(1, 2).reshape(T, Hq * D))
     return torch.stack(out)
 
 
@@ -238,7 +257,9 @@ def main() -> int:
                        "heads": s["heads"], "kv_heads": s["kv_heads"]},
             "attention_us": round(time_us(lambda: attend(s), a.steps), 1),
             "step_us": round(time_us(lambda: (s.update(x=attend(s)), step(s)), a.steps), 1),
-            "relative_error": {"x": round(relative_error(s["x"].view(torch.bfloat16), exact_attention(s)), 5)}}))
+            # against attention over the cache as it is, and over the rows before their codes
+            "relative_error": {name: round(relative_error(s["x"].view(torch.bfloat16), exact_attention(s, cached)), 5)
+                               for name, cached in (("x", True), ("x_rows", False))}}))
         return 0
     print(json.dumps({
         "config": {n: s[n] for n in "PTHKNk"},
