@@ -11,9 +11,11 @@
 #include <ATen/ops/zeros.h>
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <exception>
 #include <initializer_list>
 #include <string>
 
@@ -237,10 +239,9 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
   try {
     return f();
   } catch (const Raised&) {
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "unknown error");
+    // torch's own, as its calls from Python raise them (torch.OutOfMemoryError, say)
+    if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -185,6 +185,27 @@ def test_splits_of_one_context_merge_by_their_sums():
 
 
 @pytest.mark.gpu
+def test_no_memory_for_what_a_call_makes():
+    # refused by torch's allocator, at a hundredth of the card, as a call of torch's is
+    d = Decoder()
+    qkv, starts, lengths, pos = d.batch([0, 0, 0], [2, 1, 1])
+    d.step(qkv, starts, lengths, pos)
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(0.01)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            B.btq_kv_gather(starts, lengths, d.table, d.cache, tokens=1 << 25)
+        big = qkv[:, :1, :d.Hq].expand(2, 1 << 24, d.Hq, d.D)
+        with pytest.raises(torch.OutOfMemoryError):
+            B.btq_head_norm_rope(big, d.Hq)
+        with pytest.raises(torch.OutOfMemoryError):
+            B.btq_kv_attention(big, starts, lengths, d.table, d.cache)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    d.step(qkv, starts, lengths, pos)
+
+
+@pytest.mark.gpu
 def test_tp_block_with_attention():
     s = tp_block.prepare(2, 12, 256, 256, 192, 8)
     tp_block.prepare_attention(s, 3, 70, 1)
