@@ -617,7 +617,7 @@ def btq_head_norm_rope(x: torch.Tensor, q_heads: int, norm: str = "rms",
     a row for each head, [heads,D] or [P,heads,D]. cos and sin float32
     [rows, rope_dim/2] with positions int32 [T], or neither. rope pairs feature i
     with i + rope_dim/2 ("half") or 2i with 2i+1 ("pairs"). out (by default x's
-    type, contiguous) may be x itself.
+    type, contiguous) may be x itself; no two of its heads may share elements.
     """
     return _bound("head_norm_rope", x, stream, x, q_heads, norm, q_weight, k_weight, eps, positions,
                   cos, sin, rope, out, out_dtype)
@@ -653,7 +653,8 @@ def btq_kv_gather(seq_starts: torch.Tensor, lengths: torch.Tensor, page_table: t
                   dtype: torch.dtype = torch.bfloat16, stream=None):
     """(k, v): what the cache holds for the batch's rows, as btq_kv_append's arguments
     name them. Without k and v both are made, [P,tokens,Hk,D] of `dtype` (zeros in
-    rows of no sequence); with one of them only that one is filled."""
+    rows of no sequence); with one of them only that one is filled. k and v may lie in any
+    order of strides in which no two heads share elements."""
     return _bound("kv_gather", cache, stream, seq_starts, lengths, page_table, cache, tokens, k, v,
                   dtype)
 
@@ -678,7 +679,8 @@ def btq_kv_attention(q: torch.Tensor, seq_starts: torch.Tensor, lengths: torch.T
     unless given; window > 0 keeps that many keys up to the query's own place;
     max_length, an upper bound of lengths, helps to share out the keys. out bf16
     (q's form of it) or float32, contiguous (zeros in rows of no sequence where
-    it is made here); lse float32 [P,T,Hq] is filled if given.
+    it is made here; weights are rounded to bf16 for either); lse float32 [P,T,Hq] is
+    filled if given.
     """
     return _bound("kv_attention", q, stream, q, seq_starts, lengths, page_table, cache, scale, causal,
                   window, max_length, out, out_dtype, lse, workspace)

@@ -3,8 +3,8 @@
 //
 // These calls launch kernels of 3 to 10 us. Checking and passing some 30 arguments
 // from Python takes 6 us a call, the launch itself 3.5; here the former takes under
-// 1 (one token's head norm 9.9 -> 4.9 us a call, a decode step of 5 launches
-// 41 -> 17.6).
+// 1 (host time: one token's head norm 9.9 -> 4.2 us, the 4 calls of a step, which
+// make their outputs, 41 -> 21).
 #include <Python.h>
 
 #include <ATen/ops/empty.h>

@@ -659,8 +659,8 @@ int btq_kv_attention(const void* q, int64_t q_shard, int64_t q_pitch, int64_t q_
   const btq::AttnArgs a = {
       rows, btq::on16(rows),
       kv_args(P, T, Hk, D, seq_starts, lengths, B, page_table, max_pages, cache, pages, page_size),
-      (int)Hq, (int)(Hq / Hk), (uint32_t)(((uint64_t(1) << 32) + Hq / Hk - 1) / (Hq / Hk)), scale * 1.4426950408889634f, causal != 0,
-      (int)(window > kMaxPlaces ? 0 : window), out, out_type, lse, (float*)workspace, plan.splits,
+      (int)Hq, (int)(Hq / Hk), (uint32_t)(((uint64_t(1) << 32) + Hq / Hk - 1) / (Hq / Hk)),
+      scale * 1.4426950408889634f, causal != 0, (int)(window > kMaxPlaces ? 0 : window), out, out_type, lse, (float*)workspace, plan.splits,
       plan.begin};
   return hip_status(btq::launch_kv_attention(a, plan, (hipStream_t)stream));
 }

@@ -131,6 +131,8 @@ __device__ __forceinline__ void static_for(F f) {
 // ---- what a wave keeps of its columns: 16*NT of them, column n*16 + lane%16 in
 // the 4 lanes of that number ----
 //
+// NT is 1 in the keys' kernel, which alone calls take() and weights(); the columns' kernel has
+// 1 or 2 and raises its maximum between its own instructions.
 // Queries are operand B of the first product: bf16 as they come, or, for keys as
 // fp16, fp16 taken by a power of 2 to a largest of 2^13 or more: exact down to 2^-27
 // of that.
@@ -1364,11 +1366,15 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
   const int G = Hq / Hk;
   const int64_t heads = P * Hk, columns = T * G;
   p.splits = 1;
-  // Columns of a sequence, on average, up to which the keys' kernels are faster, with
-  // D = 128 and 8 heads, us by keys against by columns: 64 sequences of 3000 keys with 96
-  // columns each 169 against 191, with 128 204 against 241, with 192 299 against 242; one
-  // of 16000 with 128 columns 40 against 144. Over short contexts the groups' beginnings
-  // weigh more: 64 of 300 keys with 64 columns 36 against 40, with 96 52 against 43.
+  // Columns of a sequence, on average, up to which the keys' kernels are faster. D = 128, 8
+  // heads on one, P = 8, us by keys against by columns: 64 sequences of 3000 keys with 96
+  // columns each 155 against 182, with 128 204 against 195, with 192 302 against 287; one
+  // of 16000 with 128 columns 39 against 154. Over short contexts the groups' beginnings
+  // weigh more: 64 of 300 keys with 64 columns 36 against 40, with 96 49 against 42.
+  // With one head on one the same limits hold (3000 keys, 128 columns: 203 against 249, 192:
+  // 300 against 298; 300 keys, 64: 36 against 41, 96: 51 against 44), at D = 64 the long one is
+  // low (192: 194 against 230) and at D = 256 the short one high (64: 93 against 66; long, 128:
+  // 535 against 540).
   const int64_t few = max_length > 512 ? 128 : 64;
   if (columns <= few * B) {
     p.items = (columns + (int64_t)B * part_extra(G, 4)) / 16;
@@ -1379,7 +1385,7 @@ AttnPlan attn_plan(int64_t P, int64_t T, int Hq, int Hk, int D, int B, int64_t m
     // equal share of a full chip, which costs a second launch and a beginning for every
     // cut. D = 128, us whole against in shares: 128 groups of 2000 keys 15 against 18, of
     // up to 4000 24 against 31, 256 of 4000 29 against 34, of up to 6000 37 against 36,
-    // 512 of up to 8000 73 against 67; 64 groups of 4000 26 against 21.
+    // 512 of up to 8000 73 against 67; 64 groups of 4000 26 against 21. (Other D: not measured.)
     const int64_t longest = units >= 128 ? 4096 : 2048;
     if (max_length <= longest || units >= 4096) {
       p.kind = kAttnKeys;

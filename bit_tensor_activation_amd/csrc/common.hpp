@@ -343,7 +343,7 @@ struct AttnArgs {
   bool q_on16;              // every head starts on 16 bytes
   KvArgs kv;
   int Hq, G;                // query heads, those of one key head
-  uint32_t G_inverse;       // 2^32/G rounded up (G = 1: see abi.hip)
+  uint32_t G_inverse;       // 2^32/G rounded up; of G = 1 it would not fit, and nothing reads it
   float scale2;             // scale * log2(e)
   int causal, window;       // window 0: none
   void* out;                // [P,T,Hq*D]

@@ -569,9 +569,10 @@ int btq_head_norm_rope(const void *x, int x_type, int64_t x_shard, int64_t x_pit
  * passes the largest fp32, gets scale NaN and codes 0: queries that see it get NaN.
  *   k, v      fp32 or bf16 (both x_type) [P,T,Hk,D] in
  * A row whose place is negative (more rows than lengths[b]) or has no page is
- * dropped. Other places of the pages keep what they hold. Two rows of a call must not have the
- * same place in the cache (sequences that share a page may, where it is not
- * written). Calls that write one page must not run at once, and one that reads it
+ * dropped. Other places of the pages keep what they hold. A block of 32 places that a call
+ * writes must belong to one sequence of it: sequences may share the pages of a prefix that
+ * is there already, not one that both write, not even at places of their own (a byte holds
+ * two of them). Calls that write one page must not run at once, and one that reads it
  * must wait for them.
  */
 int btq_kv_append(const void *k, const void *v, int x_type, int64_t k_shard, int64_t k_pitch,
